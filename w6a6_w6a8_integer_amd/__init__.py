@@ -16,6 +16,10 @@ Entry points (same names as the C ABI):
 * :func:`gemm_w6ax_splitk` the GEMM with K split over workgroups (mid-sized M),
   fp32 partials summed in a fixed order
 * :func:`gemm_w6ax_group_dots`  the int32 group dots (verification)
+
+The operators a decoding step runs around the layers (4-bit matrix-vector products,
+block tables, paged cache writes, attention for drafted tokens) are in ``serve.py`` and
+are reached from here too.
 """
 from __future__ import annotations
 
@@ -102,7 +106,8 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is not built: run __graft_entry__.build() "
                                "(there is no CPU fallback)")
         h = ctypes.CDLL(LIB_PATH)  # after `import torch`, so the HIP runtime is shared
-        for name, (res, args) in {**SIGNATURES, **PEAK_SIGNATURES}.items():
+        for name, (res, args) in {**SIGNATURES, **PEAK_SIGNATURES,
+                                  **SERVE_SIGNATURES}.items():
             fn = getattr(h, name)
             fn.restype = res
             fn.argtypes = args
@@ -542,3 +547,8 @@ class W6AxLinear:
             return linear_w6ax(x_fp16.contiguous(), self.w_packed, self.s_w, self.N, self.abits)
         q_a, s_a = quant_act(x_fp16.contiguous(), self.abits)
         return gemm_w6ax(q_a, s_a, self.w_packed, self.s_w, self.N, self.abits, path=path)
+
+
+from .serve import SIGNATURES as SERVE_SIGNATURES  # noqa: E402  (needs the checks above)
+from .serve import (W4Linear, block_tables, gemv_w4, kv_cache, kv_cache_write,  # noqa: E402,F401
+                    pack_w4, tree_attention, tree_attention_workspace_bytes)

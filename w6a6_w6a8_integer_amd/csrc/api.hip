@@ -9,6 +9,7 @@
 #include <atomic>
 
 #include "../../include/flexq.h"
+#include "abi_checks.h"
 #include "kernels.h"
 
 // Staging memory of flexq_linear_w6ax_noalloc (activation codes, then their scales):
@@ -19,27 +20,18 @@ static __device__ __align__(256) unsigned char scratch[FLEXQ_NOALLOC_SCRATCH_BYT
 
 namespace {
 
+using flexq::aligned;
+using flexq::launched;
+using flexq::overlap;
+using flexq::Range;
+using flexq::range_of;
+
 constexpr int64_t kGroup = FLEXQ_GROUP_SIZE;
 
 // Size limits keep every in-kernel 32-bit buffer offset and grid dimension in range.
 constexpr int64_t kMaxM = 65535LL * 16;  // 1,048,560 tokens
 constexpr int64_t kMaxN = 1LL << 24;
 constexpr int64_t kMaxK = 1LL << 22;
-
-struct Range {
-  uintptr_t lo, hi;
-};
-
-inline Range range_of(const void* p, uint64_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return {a, a + (uintptr_t)bytes};
-}
-
-inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
-inline bool aligned(const void* p, uintptr_t a) {
-  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
 
 inline flexq_status check_k(int64_t K, int32_t group_size) {
   if (K <= 0) return FLEXQ_ERROR_INVALID_VALUE;
@@ -64,10 +56,6 @@ inline flexq_status check_m(int64_t M) {
   return FLEXQ_SUCCESS;
 }
 
-inline flexq_status launched(hipError_t e) {
-  return e == hipSuccess ? FLEXQ_SUCCESS : FLEXQ_ERROR_LAUNCH;
-}
-
 // most K slices flexq_gemm_w6ax_splitk accepts
 constexpr int64_t kMaxSplits = 64;
 
@@ -86,12 +74,6 @@ int tile_of_path(int path) {
          : path == FLEXQ_PATH_PREFILL_64X128  ? flexq::kTile64x128
                                               : flexq::kTileAuto;
 }
-
-#define FLEXQ_TRY(expr)                       \
-  do {                                        \
-    const flexq_status s_ = (expr);           \
-    if (s_ != FLEXQ_SUCCESS) return s_;       \
-  } while (0)
 
 flexq_status validate_gemm_operands(const int8_t* q_a, const float* s_a, const uint32_t* w_packed,
                                     const uint16_t* s_w, int64_t M, int64_t N, int64_t K,

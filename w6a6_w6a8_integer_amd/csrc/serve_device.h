@@ -1,0 +1,39 @@
+// serve_device.h -- gfx950 device helpers of the decoding-step kernels: 16-bit element
+// types and their MFMAs.
+#pragma once
+#include "w6_device.h"
+
+namespace flexq {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// 16x16x32 MFMA on 16-bit elements: lane l supplies A row l % 16 and B column l % 16, the
+// eight elements of k-slots 8 (l / 16) ..; D lane l holds column l % 16, rows
+// 4 (l / 16) + 0 .. 3, in fp32.  A and B agree on what k each slot stands for; the
+// kernels use that freedom to take fragments in the order memory holds them.
+struct Half {
+  static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint16_t bits(float f) { return float_to_half_bits(f); }
+  static __device__ __forceinline__ float value(uint16_t h) { return half_bits_to_float(h); }
+  static constexpr uint32_t kExponent = 0x7C00u;  // all ones: infinity or NaN
+};
+
+struct Bfloat {
+  static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint16_t bits(float f) {
+    return __builtin_bit_cast(uint16_t, (__bf16)f);
+  }
+  static __device__ __forceinline__ float value(uint16_t h) {
+    return __builtin_bit_cast(float, (uint32_t)h << 16);
+  }
+  static constexpr uint32_t kExponent = 0x7F80u;
+};
+
+}  // namespace flexq
