@@ -146,7 +146,7 @@ flexq_status flexq_kv_cache_write(const uint16_t* k, int64_t k_stride_t, int64_t
    Errors: INVALID_VALUE (null, negative size or stride, no page, dtype, H % Hkv, scale
    not finite, max_new > 32 * mask_words with a tree_mask, workspace too small, an output or
    the workspace overlapping another argument), UNSUPPORTED (D, page_size, q strides %
-   8, H > 4096, B > 4096, T > 2^24, max_new > 65536, max_blocks * page_size > 2^26,
+   8, H > 4096, B > 4096, T > 2^24, max_new > 65536, max_blocks * page_size > 2^24,
    num_pages * Hkv * page_size / 16 >= 2^31, alignment). */
 flexq_status flexq_tree_attention(const uint16_t* q, int32_t dtype, int64_t q_stride_t,
                                   int64_t q_stride_h, const uint16_t* k_cache,

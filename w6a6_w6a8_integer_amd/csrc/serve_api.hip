@@ -210,7 +210,7 @@ flexq_status flexq_tree_attention(const uint16_t* q, int32_t dtype, int64_t q_st
     return FLEXQ_ERROR_INVALID_VALUE;
   FLEXQ_TRY(check_attention_sizes(B, max_new, H, Hkv, D));
   FLEXQ_TRY(check_cache(num_pages, Hkv, D, page_size));
-  if (max_blocks > (1LL << 26) / page_size || T > (1LL << 24)) return FLEXQ_ERROR_UNSUPPORTED;
+  if (max_blocks > (1LL << 24) / page_size || T > (1LL << 24)) return FLEXQ_ERROR_UNSUPPORTED;
   if (tree_mask && max_new > 32 * mask_words) return FLEXQ_ERROR_INVALID_VALUE;
   if (mask_words > (1LL << 24)) return FLEXQ_ERROR_UNSUPPORTED;
   if (B == 0 || T == 0 || max_new == 0) return FLEXQ_SUCCESS;

@@ -19,6 +19,12 @@ struct Half {
   }
   static __device__ __forceinline__ uint16_t bits(float f) { return float_to_half_bits(f); }
   static __device__ __forceinline__ float value(uint16_t h) { return half_bits_to_float(h); }
+  // Two fp32 values in [0, 1] each as the sum of two halves: cut, then what was cut off
+  static __device__ __forceinline__ u32x2 split(float x, float y) {
+    const auto h = __builtin_amdgcn_cvt_pkrtz(x, y);
+    const auto l = __builtin_amdgcn_cvt_pkrtz(x - (float)h[0], y - (float)h[1]);
+    return u32x2{__builtin_bit_cast(uint32_t, h), __builtin_bit_cast(uint32_t, l)};
+  }
   static constexpr uint32_t kExponent = 0x7C00u;  // all ones: infinity or NaN
 };
 
@@ -32,6 +38,14 @@ struct Bfloat {
   }
   static __device__ __forceinline__ float value(uint16_t h) {
     return __builtin_bit_cast(float, (uint32_t)h << 16);
+  }
+  static __device__ __forceinline__ u32x2 split(float x, float y) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, x), b = __builtin_bit_cast(uint32_t, y);
+    const float ax = __builtin_bit_cast(float, a & 0xFFFF0000u);
+    const float by = __builtin_bit_cast(float, b & 0xFFFF0000u);
+    return u32x2{__builtin_amdgcn_perm(b, a, 0x07060302u),
+                 __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, y - by),
+                                       __builtin_bit_cast(uint32_t, x - ax), 0x07060302u)};
   }
   static constexpr uint32_t kExponent = 0x7F80u;
 };
