@@ -28,15 +28,24 @@ constexpr int kWaves = 4;
 constexpr int kUnitsPerCu = 2;
 // What starting on a request costs, in 32-key steps, and the least share of a workgroup.
 constexpr uint32_t kHead = 2, kMinShare = 8;
+// Probabilities are at most 2^kLag before the division (fp16 holds 2^15).
+constexpr float kLag = 8.0f;
 
 typedef __attribute__((address_space(1))) const void* global_ptr_t;
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef __attribute__((address_space(4))) const int32_t* scalar_ptr_t;
 
-// (max, sum) over the four lanes that hold one row (l, l ^ 16, l ^ 32, l ^ 48)
+// (max, sum) over the four lanes that hold one row (l, l ^ 16, l ^ 32, l ^ 48).  A swap of
+// x with itself gives both halves of the exchange, each in every lane.
 __device__ __forceinline__ float row_max(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(u, u, false, false));
+  const uint32_t a0 = a[0], a1 = a[1];
+  const float y = fmaxf(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
+  const uint32_t v = __builtin_bit_cast(uint32_t, y);
+  const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+  const uint32_t b0 = b[0], b1 = b[1];
+  return fmaxf(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
 }
 __device__ __forceinline__ float row_sum(float x) {
   x += __shfl_xor(x, 16);
@@ -55,6 +64,9 @@ __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
+
+// x, known to be the same in every lane (so that it and what follows from it is scalar)
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
 
@@ -204,13 +216,24 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
   const int block_row0 = id / 8 % row_blocks * kRowsBlock;
   int b;
   uint32_t before;
-  const Plan plan = make_plan(a, shares, share, b, before);
+  Plan plan = make_plan(a, shares, share, b, before);
+  plan.total = uniform(plan.total);
+  plan.shares = uniform(plan.shares);
+  b = uniform(b);
+  before = uniform(before);
   if (b >= a.B) return;
-  const uint32_t share_end = plan.start(share + 1);
+  const uint32_t share_end = uniform(plan.start(share + 1));
   const int group = a.H / a.Hkv;
   const Parts parts = parts_of(a, shares, a.max_new * group);
   const int per_page = 1 << (a.page_shift - 4);  // 16-token blocks of a page
-  const float scale = a.scale * kLog2e;
+  // A negative scale goes into the queries' signs and a zero one into the queries, so that
+  // the scores' order is the scaled ones'.  The reference m a row's probabilities are
+  // taken against is kept unscaled and raised only where a score exceeds it by a factor of
+  // 2^kLag: l and O are in proportion to 2^-m whatever m is.
+  const float scale = a.scale != 0.0f ? fabsf(a.scale) * kLog2e : 1.0f;
+  const float lag = fminf(kLag / scale, 3e38f);
+  const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+  const uint32_t keep_q = a.scale != 0.0f ? 0xFFFFFFFFu : 0u;
 
   // what a lane takes of a step's fragments: half of the step, and where in a block
   const bool key_wave = wave < 2;
@@ -220,12 +243,12 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
       : a.vc + (wave - 2) * DT * 256 + c * 16 + 8 * (p & 1);
 
   for (; b < a.B && before < share_end; ++b) {
-    const uint32_t weight = request_weight(a, b);
+    const uint32_t weight = uniform(request_weight(a, b));
     if (weight == 0) continue;
     const int steps = (int)(weight - kHead);
     // this share's steps of the request
     const uint32_t first_step = before + kHead;
-    const uint32_t x0 = plan.start(share);
+    const uint32_t x0 = uniform(plan.start(share));
     const int begin = x0 > first_step ? (int)(x0 - first_step) : 0;
     const int own_end = (int)min((int64_t)steps, (int64_t)share_end - first_step);
     before += weight;
@@ -233,9 +256,9 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
     const uint32_t s0 = plan.share_of(first_step), s1 = plan.share_of(first_step + steps - 1);
     if (threadIdx.x == 0 && hk == 0 && block_row0 == 0 && share == s0)
       parts.plan[b] = {(int)s0, (int)s1};
-    const int cu = a.cu[b];
-    const int n_new = request_new(a, b);
-    const int ctx = request_ctx(a, b);
+    const int cu = uniform(a.cu[b]);
+    const int n_new = uniform(request_new(a, b));
+    const int ctx = uniform(request_ctx(a, b));
     const int rows = n_new * group;
     if (block_row0 >= rows) continue;
     const int len = min(ctx + n_new, a.max_blocks << a.page_shift);
@@ -244,7 +267,8 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
       const int last = min(block_row0 + kRowsBlock, rows) - 1;
       end = min(end, (ctx + last / group + 32) >> 5);
     }
-    const int row0 = block_row0 + wave * kRowsWave;
+    // where the last waves have fewer rows, a compute unit's next workgroup turns them round
+    const int row0 = block_row0 + (id >> 8 & 1 ? kWaves - 1 - wave : wave) * kRowsWave;
     const bool idle = row0 >= rows;  // a wave that only stages
 
     u32x4 qf[NT][DT];
@@ -258,14 +282,14 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
       const uint16_t* q = a.q + t * a.q_st + (int64_t)(hk * group + r % group) * a.q_sh + 8 * p;
 #pragma unroll
       for (int ks = 0; ks < DT; ++ks)
-        qf[rt][ks] = in ? *reinterpret_cast<const u32x4*>(q + 32 * ks) : u32x4{};
+        qf[rt][ks] = in ? (*reinterpret_cast<const u32x4*>(q + 32 * ks) & keep_q) ^ flip : u32x4{};
     }
 
     // Table entry of the 16 tokens at 32 step + 16 half (-1 past the request's tokens), and
     // the 16-token block of the cache it stands for (-1 where there is none).
     const scalar_ptr_t table = (scalar_ptr_t)(a.table + (int64_t)b * a.max_blocks);
     auto page_of = [&](int step, int half) {
-      const int pos = step * 32 + half * 16;
+      const int pos = min(step, end - 1) * 32 + half * 16;
       return pos < len ? table[pos >> a.page_shift] : -1;
     };
     auto block_of = [&](int id, int step, int half) {
@@ -299,7 +323,15 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
     }
 
     barrier();  // the stages of the request before have been read
-    for (int step = begin; step < min(end, begin + S - 1); ++step) stage(step);
+    // S - 1 steps, the last again where there are fewer: with a fixed number of loads behind
+    // it the wait for q (before the loop, not in it) leaves them in flight.
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) stage(begin + i);
+    wait_vm<(S - 1) * DT>();
+#pragma unroll
+    for (int rt = 0; rt < NT; ++rt)
+#pragma unroll
+      for (int ks = 0; ks < DT; ++ks) asm volatile("" : "+v"(qf[rt][ks]));
     for (int step = begin; step < end; ++step) {
       if (end - step >= S - 1)
         wait_vm<(S - 2) * DT>();
@@ -311,35 +343,35 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
       const u32x4* kf = reinterpret_cast<const u32x4*>(lds + (step % S) * kStage) + lane;
       const u32x4* vf = kf + 2 * DT * 64;
 
+      // S = K Q^T; then the values' fragments are on their way while P is formed
+      u32x4 f[OT];
+#pragma unroll
+      for (int i = 0; i < OT; ++i) f[i] = kf[i * 64];
       f32x4 s[NT][2] = {};
 #pragma unroll
       for (int ks = 0; ks < DT; ++ks)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const u32x4 k = kf[(t * DT + ks) * 64];
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int rt = 0; rt < NT; ++rt) s[rt][t] = E::mfma(k, qf[rt][ks], s[rt][t]);
-        }
+          for (int rt = 0; rt < NT; ++rt) s[rt][t] = E::mfma(f[t * DT + ks], qf[rt][ks], s[rt][t]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < OT; ++i) f[i] = vf[i * 64];
+      __builtin_amdgcn_sched_barrier(0);
 
       // Keys that are no context (drafted, or none at all) or on no page: the wave masks.
       const uint32_t hole = (uint32_t)(holes >> (2 * (step & 31))) & 3u;
       const bool masked = hole != 0 || step * 32 + 32 > ctx;
-      const int key0 = step * 32 + 8 * p;  // this lane's first key
-      uint32_t there = 0xFFu;              // keys that exist
-      if (masked) there = (hole >> (p >> 1)) & 1u ? 0u : low_bits(len - key0);
-      uint32_t seen[NT];
-      u32x4 hi[NT], lo[NT];
+      uint32_t seen[NT];                  // attended keys among this lane's eight
+      uint32_t there = 0xFFu;             // keys that exist
+      bool poison = false;                // a value is infinite or NaN
+      if (masked) {
+        const int key0 = step * 32 + 8 * p;  // this lane's first key
+        const int j0 = key0 - ctx;           // its drafted index (may be negative)
+        there = (hole >> (p >> 1)) & 1u ? 0u : low_bits(len - key0);
 #pragma unroll
-      for (int rt = 0; rt < NT; ++rt) {
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = s[rt][e >> 2][e & 3] * scale;
-        seen[rt] = 0xFFu;
-        if (masked) {
-          // attended keys among this lane's eight: the context, then the tree's bits (or,
-          // for a chain, the tokens up to the row's own)
-          const int j0 = key0 - ctx;  // drafted index of the first key (may be negative)
-          if (a.mask) {
+        for (int rt = 0; rt < NT; ++rt) {
+          if (a.mask) {  // the context, then the tree's bits
             seen[rt] = low_bits(-j0);
             const int64_t t = (int64_t)cu + tok[rt];
             if (j0 > -8 && tok[rt] < n_new && t >= 0 && t < a.T) {
@@ -349,21 +381,41 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
               const uint32_t w1 = w + 1 < a.mask_words ? (uint32_t)words[w + 1] : 0u;
               seen[rt] |= (uint32_t)(((uint64_t)w1 << 32 | w0) >> (j0 & 31)) & 0xFFu;
             }
-          } else {
+          } else {  // a chain: the tokens up to the row's own
             seen[rt] = low_bits(tok[rt] + 1 - j0);
           }
           seen[rt] &= there;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (!((seen[rt] >> e) & 1u)) x[e] = -INFINITY;
+            if (!((seen[rt] >> e) & 1u)) s[rt][e >> 2][e & 3] = -INFINITY;
         }
-        float top = x[0];
+        // values of keys that do not exist are zeroed, and infinite and NaN ones for now
+        bool bad = false;
 #pragma unroll
-        for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t keep =
+              ((there >> (2 * i)) & 1u) * 0xFFFFu | ((there >> (2 * i + 1)) & 1u) * 0xFFFF0000u;
+#pragma unroll
+          for (int dt = 0; dt < OT; ++dt) {
+            const uint32_t w = f[dt][i] & keep, ex = not_finite<E>(w);
+            bad |= ex != 0;
+            f[dt][i] = w & ~ex;
+          }
+        }
+        poison = __ballot(bad) != 0;
+      }
+
+      u32x4 hi[NT], lo[NT];
+#pragma unroll
+      for (int rt = 0; rt < NT; ++rt) {
+        float top = s[rt][0][0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) top = fmaxf(top, s[rt][e >> 2][e & 3]);
         top = row_max(top);
-        if (__ballot(top > m[rt])) {  // most steps raise no row's maximum
+        if (__ballot(top > m[rt] + lag)) {  // rare after a request's first step
           top = fmaxf(m[rt], top);
-          const float by = __builtin_amdgcn_exp2f(m[rt] - (top == -INFINITY ? 0.0f : top));
+          const float by =
+              __builtin_amdgcn_exp2f((m[rt] - (top == -INFINITY ? 0.0f : top)) * scale);
           m[rt] = top;
           l[rt] *= by;
 #pragma unroll
@@ -371,11 +423,11 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[rt][dt][i] *= by;
         }
-        const float ref = m[rt] == -INFINITY ? 0.0f : m[rt];
+        const float ref = m[rt] == -INFINITY ? 0.0f : -m[rt] * scale;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float v0 = __builtin_amdgcn_exp2f(x[2 * i] - ref);
-          const float v1 = __builtin_amdgcn_exp2f(x[2 * i + 1] - ref);
+          const float v0 = __builtin_amdgcn_exp2f(fmaf(s[rt][i >> 1][2 * i & 3], scale, ref));
+          const float v1 = __builtin_amdgcn_exp2f(fmaf(s[rt][i >> 1][(2 * i & 3) + 1], scale, ref));
           l[rt] += v0 + v1;
           const u32x2 both = E::split(v0, v1);
           hi[rt][i] = both[0];
@@ -383,40 +435,14 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
         }
       }
 
-      if (!masked) {
 #pragma unroll
-        for (int dt = 0; dt < OT; ++dt) {
-          const u32x4 v = vf[dt * 64];
-#pragma unroll
-          for (int rt = 0; rt < NT; ++rt) {
-            o[rt][dt] = E::mfma(v, hi[rt], o[rt][dt]);
-            o[rt][dt] = E::mfma(v, lo[rt], o[rt][dt]);
-          }
-        }
-        continue;
-      }
-      // values of keys that do not exist are zeroed, and infinite and NaN ones for now
-      uint32_t keep[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        keep[i] = ((there >> (2 * i)) & 1u) * 0xFFFFu | ((there >> (2 * i + 1)) & 1u) * 0xFFFF0000u;
-      bool bad = false;
-#pragma unroll
-      for (int dt = 0; dt < OT; ++dt) {
-        u32x4 v = vf[dt * 64];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = v[i] & keep[i], ex = not_finite<E>(w);
-          bad |= ex != 0;
-          v[i] = w & ~ex;
-        }
+      for (int dt = 0; dt < OT; ++dt)
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt) {
-          o[rt][dt] = E::mfma(v, hi[rt], o[rt][dt]);
-          o[rt][dt] = E::mfma(v, lo[rt], o[rt][dt]);
+          o[rt][dt] = E::mfma(f[dt], hi[rt], o[rt][dt]);
+          o[rt][dt] = E::mfma(f[dt], lo[rt], o[rt][dt]);
         }
-      }
-      if (__ballot(bad) == 0) continue;
+      if (!poison) continue;
       // Infinite and NaN values reach only the rows that attend their keys: one key at a
       // time, and a row that does not attend it keeps its sum.
       for (int k = 0; k < 32; ++k) {
@@ -443,6 +469,7 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
 #pragma unroll
     for (int rt = 0; rt < NT; ++rt) {
       const float sum = row_sum(l[rt]);
+      const float top = m[rt] == -INFINITY ? m[rt] : m[rt] * scale;
       const int row = row0 + rt * 16 + c;
       if (row >= rows) continue;
       if (s0 != s1) {
@@ -450,14 +477,14 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
         const int64_t at = (place * a.Hkv + hk) * (a.max_new * group) + row;
 #pragma unroll
         for (int dt = 0; dt < OT; ++dt) parts.out[at * (D / 4) + 4 * dt + p] = o[rt][dt];
-        if (p == 0) parts.stat[at] = {m[rt], sum};
+        if (p == 0) parts.stat[at] = {top, sum};
       } else {
         const int64_t t = (int64_t)cu + tok[rt];
         if (t >= 0 && t < a.T) {
 #pragma unroll
           for (int dt = 0; dt < OT; ++dt)
             write_row<E>(a, t, hk * group + row % group, 4 * dt + p, o[rt][dt],
-                         m[rt] == -INFINITY ? 0.0f : m[rt], sum);
+                         top == -INFINITY ? 0.0f : top, sum);
         }
       }
     }

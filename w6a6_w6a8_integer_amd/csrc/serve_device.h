@@ -22,7 +22,7 @@ struct Half {
   // Two fp32 values in [0, 1] each as the sum of two halves: cut, then what was cut off
   static __device__ __forceinline__ u32x2 split(float x, float y) {
     const auto h = __builtin_amdgcn_cvt_pkrtz(x, y);
-    const auto l = __builtin_amdgcn_cvt_pkrtz(x - (float)h[0], y - (float)h[1]);
+    const auto l = __builtin_amdgcn_cvt_pkrtz(fmaf(-(float)h[0], 1.0f, x), fmaf(-(float)h[1], 1.0f, y));
     return u32x2{__builtin_bit_cast(uint32_t, h), __builtin_bit_cast(uint32_t, l)};
   }
   static constexpr uint32_t kExponent = 0x7C00u;  // all ones: infinity or NaN
