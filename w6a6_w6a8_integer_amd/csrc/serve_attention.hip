@@ -73,35 +73,40 @@ __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory
 }  // namespace
 
 // The plan.  Request b weighs kHead + steps_b, steps_b = ceil((ctx + new) / 32) its 32-key
-// steps (0 without new tokens), the weights laid end to end make U, and share i of G
-// is [U i / G, U (i + 1) / G): equal work whatever the lengths.  A share holds the end of one
-// request, whole ones, and the beginning of another.  Whole ones are written out; of the
-// others each share keeps statistics and sums in the workspace (place 2 i the end,
+// steps (0 without new tokens); the weights laid end to end are cut into G shares that
+// differ by one unit at most: equal work whatever the lengths.  A share holds the end of
+// one request, whole ones, and the beginning of another.  Whole ones are written out; of
+// the others each share keeps statistics and sums in the workspace (place 2 i the end,
 // 2 i + 1 the beginning), and a second kernel joins them in order.  The lengths live on the
 // GPU, so every wave forms the plan itself.
 struct Plan {
-  uint32_t total;   // U
-  uint32_t shares;  // G
-  __device__ uint32_t start(uint32_t i) const { return (uint32_t)((uint64_t)total * i / shares); }
+  uint32_t shares, size, longer;  // G; `longer` shares of size + 1 come first
+  __device__ uint32_t start(uint32_t i) const { return i * size + min(i, longer); }
   // the share that holds unit x
   __device__ uint32_t share_of(uint32_t x) const {
-    return (uint32_t)((((uint64_t)x + 1) * shares - 1) / total);
+    const uint32_t in_longer = longer * (size + 1);
+    return x < in_longer ? x / (size + 1) : longer + (x - in_longer) / size;
   }
 };
 
-__device__ __forceinline__ int request_new(const AttentionArgs& a, int b) {
-  return min(max(0, a.cu[b + 1] - a.cu[b]), a.max_new);
+struct Request {
+  int cu, n_new, ctx, len;
+  __device__ uint32_t steps() const { return max(1, (len + 31) >> 5); }  // rows without a key too
+  __device__ uint32_t weight() const { return n_new == 0 ? 0 : kHead + steps(); }
+};
+
+__device__ __forceinline__ Request make_request(const AttentionArgs& a, int cu, int cu1, int ctx) {
+  Request r;
+  const int most = a.max_blocks << a.page_shift;
+  r.cu = cu;
+  r.n_new = min(max(0, cu1 - cu), a.max_new);
+  r.ctx = min(max(0, ctx), most);
+  r.len = min(r.ctx + r.n_new, most);
+  return r;
 }
 
-__device__ __forceinline__ int request_ctx(const AttentionArgs& a, int b) {
-  return min(max(0, a.ctx[b]), a.max_blocks << a.page_shift);
-}
-
-__device__ __forceinline__ uint32_t request_weight(const AttentionArgs& a, int b) {
-  const int n = request_new(a, b);
-  if (n == 0) return 0;
-  const int len = min(request_ctx(a, b) + n, a.max_blocks << a.page_shift);
-  return kHead + max(1u, (uint32_t)(len + 31) >> 5);  // one without a key still has rows
+__device__ __forceinline__ Request load_request(const AttentionArgs& a, int b) {
+  return b < a.B ? make_request(a, a.cu[b], a.cu[b + 1], a.ctx[b]) : Request{};
 }
 
 __device__ __forceinline__ uint32_t inclusive_sum(uint32_t v, int lane) {
@@ -113,33 +118,52 @@ __device__ __forceinline__ uint32_t inclusive_sum(uint32_t v, int lane) {
   return v;
 }
 
+// 64 consecutive requests, one a lane.
+struct Window {
+  int base;
+  Request mine;
+  __device__ Request at(int b) const {
+    const int i = b - base;
+    Request r;
+    r.cu = __builtin_amdgcn_readlane(mine.cu, i);
+    r.n_new = __builtin_amdgcn_readlane(mine.n_new, i);
+    r.ctx = __builtin_amdgcn_readlane(mine.ctx, i);
+    r.len = __builtin_amdgcn_readlane(mine.len, i);
+    return r;
+  }
+};
+
 // The plan, and the request that holds the first unit of share i with the units before
-// that request (b = B where the share is empty).  Two levels of 64 lanes: kMaxRequests.
-__device__ __forceinline__ Plan make_plan(const AttentionArgs& a, int shares, uint32_t i, int& b,
-                                          uint32_t& before) {
+// that request (b = B where there is no such share) and a window that begins at or before
+// it.  Two levels of 64 lanes: kMaxRequests.
+__device__ __forceinline__ Plan make_plan(const AttentionArgs& a, uint32_t shares, uint32_t i,
+                                          int& b, uint32_t& before, Window& window) {
   static_assert(kMaxRequests <= 64 * 64, "two levels of 64 lanes");
   const int lane = threadIdx.x & 63;
   const int per = (a.B + 63) / 64;
   uint32_t sum = 0;
+  window.base = 0;
+  window.mine = load_request(a, lane * per);
+  if (lane * per < a.B) sum = window.mine.weight();
 #pragma unroll 4
-  for (int j = 0; j < per; ++j) {
-    const int r = lane * per + j;
-    if (r < a.B) sum += request_weight(a, r);
-  }
+  for (int j = 1; j < per; ++j) sum += load_request(a, lane * per + j).weight();
   const uint32_t inc = inclusive_sum(sum, lane);
+  const uint32_t total = __builtin_amdgcn_readlane(inc, 63);
   Plan plan;
-  plan.total = __builtin_amdgcn_readlane(inc, 63);
-  plan.shares = min((uint32_t)shares, max(1u, plan.total / kMinShare));
+  plan.shares = min(shares, max(1u, total / kMinShare));
+  plan.size = total / plan.shares;
+  plan.longer = total - plan.size * plan.shares;
   b = a.B;
   before = 0;
-  if (i >= plan.shares || plan.total == 0) return plan;
+  if (i >= plan.shares || total == 0) return plan;
   const uint32_t x = plan.start(i);
   const int at = __builtin_ctzll(__ballot(inc > x));
   before = __builtin_amdgcn_readlane(inc - sum, at);
   b = at * per;
   if (per > 1) {
-    const int r = b + lane;
-    const uint32_t w = lane < per && r < a.B ? request_weight(a, r) : 0;
+    window.base = b;
+    window.mine = load_request(a, b + lane);
+    const uint32_t w = lane < per ? window.mine.weight() : 0;
     const uint32_t in = inclusive_sum(w, lane);
     const int k = __builtin_ctzll(__ballot(before + in > x));
     before += __builtin_amdgcn_readlane(in - w, k);
@@ -216,13 +240,10 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
   const int block_row0 = id / 8 % row_blocks * kRowsBlock;
   int b;
   uint32_t before;
-  Plan plan = make_plan(a, shares, share, b, before);
-  plan.total = uniform(plan.total);
-  plan.shares = uniform(plan.shares);
-  b = uniform(b);
-  before = uniform(before);
+  Window window;
+  const Plan plan = make_plan(a, shares, share, b, before, window);
   if (b >= a.B) return;
-  const uint32_t share_end = uniform(plan.start(share + 1));
+  const uint32_t share_begin = plan.start(share), share_end = plan.start(share + 1);
   const int group = a.H / a.Hkv;
   const Parts parts = parts_of(a, shares, a.max_new * group);
   const int per_page = 1 << (a.page_shift - 4);  // 16-token blocks of a page
@@ -243,25 +264,25 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
       : a.vc + (wave - 2) * DT * 256 + c * 16 + 8 * (p & 1);
 
   for (; b < a.B && before < share_end; ++b) {
-    const uint32_t weight = uniform(request_weight(a, b));
+    if (b - window.base >= 64) {
+      window.base = b;
+      window.mine = load_request(a, b + lane);
+    }
+    const Request r = window.at(b);
+    const uint32_t weight = r.weight();
     if (weight == 0) continue;
-    const int steps = (int)(weight - kHead);
+    const int cu = r.cu, n_new = r.n_new, ctx = r.ctx, len = r.len, steps = (int)r.steps();
     // this share's steps of the request
     const uint32_t first_step = before + kHead;
-    const uint32_t x0 = uniform(plan.start(share));
-    const int begin = x0 > first_step ? (int)(x0 - first_step) : 0;
-    const int own_end = (int)min((int64_t)steps, (int64_t)share_end - first_step);
+    const int begin = share_begin > first_step ? (int)(share_begin - first_step) : 0;
+    const int own_end = min(steps, (int)(share_end - first_step));
     before += weight;
     if (own_end <= begin) continue;
     const uint32_t s0 = plan.share_of(first_step), s1 = plan.share_of(first_step + steps - 1);
     if (threadIdx.x == 0 && hk == 0 && block_row0 == 0 && share == s0)
       parts.plan[b] = {(int)s0, (int)s1};
-    const int cu = uniform(a.cu[b]);
-    const int n_new = uniform(request_new(a, b));
-    const int ctx = uniform(request_ctx(a, b));
     const int rows = n_new * group;
     if (block_row0 >= rows) continue;
-    const int len = min(ctx + n_new, a.max_blocks << a.page_shift);
     int end = own_end;
     if (!a.mask) {  // a chain: nothing past the last row's token
       const int last = min(block_row0 + kRowsBlock, rows) - 1;
@@ -282,7 +303,7 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
       const uint16_t* q = a.q + t * a.q_st + (int64_t)(hk * group + r % group) * a.q_sh + 8 * p;
 #pragma unroll
       for (int ks = 0; ks < DT; ++ks)
-        qf[rt][ks] = in ? (*reinterpret_cast<const u32x4*>(q + 32 * ks) & keep_q) ^ flip : u32x4{};
+        qf[rt][ks] = in ? *reinterpret_cast<const u32x4*>(q + 32 * ks) : u32x4{};
     }
 
     // Table entry of the 16 tokens at 32 step + 16 half (-1 past the request's tokens), and
@@ -331,7 +352,10 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
 #pragma unroll
     for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
-      for (int ks = 0; ks < DT; ++ks) asm volatile("" : "+v"(qf[rt][ks]));
+      for (int ks = 0; ks < DT; ++ks) {
+        asm volatile("" : "+v"(qf[rt][ks]));
+        qf[rt][ks] = (qf[rt][ks] & keep_q) ^ flip;
+      }
     for (int step = begin; step < end; ++step) {
       if (end - step >= S - 1)
         wait_vm<(S - 2) * DT>();
@@ -500,10 +524,10 @@ __global__ __launch_bounds__(256) void join_parts_kernel(const AttentionArgs a, 
   const int b = blockIdx.z, hk = blockIdx.y;
   const int group = a.H / a.Hkv;
   const int row = blockIdx.x * kRows + threadIdx.x / (D / 4), d4 = threadIdx.x % (D / 4);
-  if (threadIdx.x >= kRows * (D / 4) || row >= request_new(a, b) * group) return;
   const Parts parts = parts_of(a, shares, a.max_new * group);
-  const int2 plan = parts.plan[b];
-  if (plan.x == plan.y) return;
+  const int2 plan = parts.plan[b];  // not set for a request without new tokens
+  const Request request = load_request(a, b);
+  if (threadIdx.x >= kRows * (D / 4) || row >= request.n_new * group || plan.x == plan.y) return;
   const int64_t stride = (int64_t)a.Hkv * (a.max_new * group);
   // the first share's place is 2 i + 1, the others' 2 i
   const int64_t at0 = (2 * (int64_t)plan.x + 1) * stride + (int64_t)hk * (a.max_new * group) + row;
@@ -525,7 +549,7 @@ __global__ __launch_bounds__(256) void join_parts_kernel(const AttentionArgs a, 
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] = fmaf(o[k], by, acc[k]);
   }
-  const int64_t t = (int64_t)a.cu[b] + row / group;
+  const int64_t t = (int64_t)request.cu + row / group;
   if (t >= 0 && t < a.T) write_row<E>(a, t, hk * group + row % group, d4, acc, ref, total);
 }
 
