@@ -61,7 +61,7 @@ size_t flexq_packed_w4_bytes(int64_t N, int64_t K);
      s_w   [K/group_size][N] fp16 bits, 2-byte aligned      (output)
    group_size is 32, 64 or 128.  N == 0 is a no-op.  Errors: INVALID_VALUE (null,
    N < 0, K <= 0, dtype, overlap), UNSUPPORTED (group_size, K % 128, N % 16,
-   N > 2^24, K > 2^22, alignment). */
+   N > 2^24, K > 2^22, N * K / group_size >= 2^29, alignment). */
 flexq_status flexq_pack_w4(const uint16_t* w, int32_t dtype, int64_t N, int64_t K,
                            int32_t group_size, uint32_t* w4, uint16_t* s_w_fp16, void* stream);
 
@@ -71,12 +71,22 @@ flexq_status flexq_pack_w4(const uint16_t* w, int32_t dtype, int64_t N, int64_t 
      x     [M][K] of dtype, rows x_stride elements apart, 16-byte aligned rows
      w4, s_w_fp16 as flexq_pack_w4 writes them; s_w_fp16 8-byte aligned
      y     [M][N] of dtype, 8-byte aligned (output)
-   M == 0 or N == 0 is a no-op.  Errors: INVALID_VALUE (null, negative size, dtype,
-   x_stride < K with M > 1, overlap), UNSUPPORTED (as flexq_pack_w4, x_stride % 8,
-   M > 1,048,560, alignment). */
+     workspace  flexq_gemv_w4_workspace_bytes(M, N, K) bytes, 16-byte aligned (NULL where
+           that is 0), overwritten; not to be used by other work until this call's kernels
+           have run
+   The result does not depend on the order in which workgroups run.  M == 0 or N == 0 is
+   a no-op.  Errors: INVALID_VALUE (null, negative size, dtype, x_stride < K with M > 1,
+   workspace too small, overlap), UNSUPPORTED (as flexq_pack_w4, x_stride % 8,
+   x_stride > 2^24, M > 1,048,560, alignment). */
 flexq_status flexq_gemv_w4(const uint16_t* x, int32_t dtype, int64_t x_stride,
                            const uint32_t* w4, const uint16_t* s_w_fp16, int64_t M, int64_t N,
-                           int64_t K, int32_t group_size, uint16_t* y, void* stream);
+                           int64_t K, int32_t group_size, void* workspace,
+                           size_t workspace_bytes, uint16_t* y, void* stream);
+
+/* Bytes of workspace flexq_gemv_w4 needs on the current device: 0 up to 4 rows of moderate
+   length and for weights of many rows, else fp32 sums of slices of K.  0 for a size that it
+   refuses or that makes it a no-op. */
+size_t flexq_gemv_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* Block tables and slot maps of a step.  Request b holds ctx_lens[b] tokens in the
    pages block_table[b][0 .. have_b - 1], have_b = ceil(ctx_lens[b] / page_size), and

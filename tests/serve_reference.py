@@ -5,9 +5,10 @@ Bounds.  u = 2^-23 is the largest relative error of one fp32 operation (a matrix
 instruction may truncate).  A sum of n products in any order errs by at most
 n u sum|products|.
 
-* gemv_w4: 128 products a group, then the group sums: (128 + G + 16) u S with
-  S = sum |s x q|, and the rounding of the output (2^-11 fp16, 2^-8 bf16, doubled where
-  the fp16 result is subnormal by an absolute 2^-25).
+* gemv_w4: a group's codes enter as q + 24 and 24 sum x is taken off, so its partial sums
+  reach 31 sum|x|; 32 products an instruction, eight instructions a group: 40 u of that.
+  The group sums add (G + 16) u S with S = sum |s x q|, and the output is rounded
+  (2^-11 fp16, 2^-8 bf16, and an absolute 2^-24 for a subnormal fp16).
 * attention: a score errs by d = (D + 8) u scale sum|q k| (the conversion to base 2 and
   the maximum's subtraction included), so a probability by a factor 1 +- 2 d; the sum
   over the keys adds (L / 32 + 64) u and the two-part probabilities 2^-16 of each, in the
@@ -54,14 +55,15 @@ def pack_w4(q):
 
 
 def gemv(x, q, s, group):
-    """(Y, S) in 64 bits: x [M][K], q [N][K], s [N][K / group]."""
-    w = q.astype(np.float64) * np.repeat(s.astype(np.float64), group, 1)
-    x = x.astype(np.float64)
-    return x @ w.T, np.abs(x) @ np.abs(w).T
+    """(Y, bound of the fp32 sums' error) in 64 bits: x [M][K], q [N][K], s [N][K / group]."""
+    s = np.repeat(s.astype(np.float64), group, 1)
+    w, x = q.astype(np.float64) * s, x.astype(np.float64)
+    groups = q.shape[1] // group
+    return x @ w.T, U * ((groups + 16) * (np.abs(x) @ np.abs(w).T) + 40 * 31 * (np.abs(x) @ s.T))
 
 
-def gemv_tolerance(y, S, groups, dtype):
-    return (128 + groups + 16) * U * S + OUT_EPS[dtype] * np.abs(y) * (1 + 2.0 ** -7) \
+def gemv_tolerance(y, sums, dtype):
+    return sums + OUT_EPS[dtype] * np.abs(y) * (1 + 2.0 ** -7) \
         + OUT_ABS[dtype]
 
 

@@ -79,8 +79,8 @@ def test_gemv_w4(fq, M, N, K, group, dtype):
     w4 = torch.from_numpy(ref.pack_w4(q).view(np.int32)).to(DEV)
     sw = torch.from_numpy(np.ascontiguousarray(s.T)).to(DEV)
     y = fq.gemv_w4(x.to(DEV), w4, sw, N)
-    want, S = ref.gemv(x.double().numpy(), q, s, group)
-    tol = ref.gemv_tolerance(want, S, K // group, dtype)
+    want, sums = ref.gemv(x.double().numpy(), q, s, group)
+    tol = ref.gemv_tolerance(want, sums, dtype)
     err = np.abs(y.double().cpu().numpy() - want)
     assert (err <= tol).all(), (float((err / tol).max()), np.argwhere(err > tol)[:4].tolist())
     assert torch.equal(y, fq.gemv_w4(x.to(DEV), w4, sw, N))
@@ -103,8 +103,8 @@ def test_gemv_w4_strided_rows_guards_and_stream(fq):
     with torch.cuda.stream(side):
         fq.gemv_w4(x, w4, sw, N, y=y)
     torch.cuda.current_stream().wait_stream(side)
-    want, S = ref.gemv(x.double().cpu().numpy(), q, s, 128)
-    assert (np.abs(y.double().cpu().numpy() - want) <= ref.gemv_tolerance(want, S, 3, F16)).all()
+    want, sums = ref.gemv(x.double().cpu().numpy(), q, s, 128)
+    assert (np.abs(y.double().cpu().numpy() - want) <= ref.gemv_tolerance(want, sums, F16)).all()
     assert bool((buf[:4] == -1).all()) and bool((buf[4 + M * N:] == -1).all())
 
 
@@ -124,14 +124,45 @@ def test_gemv_w4_propagates_infinities_and_nan(fq):
     assert bool(y[1].isnan().all())
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_gemv_w4_infinities_and_the_top_of_the_range(fq, dtype, group):
+    """Infinite activations give infinities of the code's sign (NaN for a zero code), and
+    activations at the top of the type's range whose sums stay finite are summed."""
+    M, N, K = 20, 64, 256
+    r = rng(16, group)
+    q = r.integers(-7, 8, (N, K))
+    s = np.full((N, K // group), 2.0 ** -8, np.float16)
+    x = normal(r, (M, K), dtype)
+    x[3, 130] = float("inf")
+    x[17, 5] = -float("inf")
+    big = torch.finfo(dtype).max
+    x[6] = 0
+    x[6, 10], x[6, 11] = big, -big
+    w4 = torch.from_numpy(ref.pack_w4(q).view(np.int32)).to(DEV)
+    y = fq.gemv_w4(x.to(DEV), w4, torch.from_numpy(np.ascontiguousarray(s.T)).to(DEV), N)
+    y = y.double().cpu().numpy()
+    for row, k, sign in ((3, 130, 1), (17, 5, -1)):
+        want = np.where(q[:, k] == 0, NAN, np.where(sign * q[:, k] > 0, np.inf, -np.inf))
+        assert np.array_equal(y[row], want, equal_nan=True)
+    # products and their sum are fp32: in bfloat16 those of larger codes pass its range
+    a, b = float(big) * q[:, 10], float(big) * q[:, 11]
+    fits = np.maximum(np.maximum(np.abs(a), np.abs(b)), np.abs(a - b)) < 3.4e38
+    assert fits.any()
+    assert np.allclose(y[6][fits], ((a - b) * 2.0 ** -8)[fits], rtol=2.0 ** -7)
+    other = [m for m in range(M) if m not in (3, 6, 17)]
+    want, sums = ref.gemv(x[other].double().numpy(), q, s, group)
+    assert (np.abs(y[other] - want) <= ref.gemv_tolerance(want, sums, dtype)).all()
+
+
 def test_w4_linear(fq):
     r = rng(4)
     w, x = normal(r, (64, 256), BF16, 0.02), normal(r, (3, 256), BF16)
     layer = fq.W4Linear(w.to(DEV), group=32)
     q, s = ref.quantize_w4(w.float().numpy(), 32)
-    want, S = ref.gemv(x.double().numpy(), q, s, 32)
+    want, sums = ref.gemv(x.double().numpy(), q, s, 32)
     y = layer(x.to(DEV)).double().cpu().numpy()
-    assert (np.abs(y - want) <= ref.gemv_tolerance(want, S, 8, BF16)).all()
+    assert (np.abs(y - want) <= ref.gemv_tolerance(want, sums, BF16)).all()
 
 
 # ---- block tables --------------------------------------------------------------------

@@ -53,15 +53,29 @@ def test_pack_w4_rejects_bad_arguments(fq):
 
 
 def test_gemv_w4_rejects_bad_arguments(fq):
-    def call(x=A, dtype=0, stride=128, w4=2 * A, s=3 * A, M=4, N=16, K=128, group=128, y=4 * A):
-        return fq.lib().flexq_gemv_w4(x, dtype, stride, w4, s, M, N, K, group, y, None)
+    need = fq.lib().flexq_gemv_w4_workspace_bytes
+    assert need(1, 4096, 4096) == 0 and need(64, 57344, 8192) == 0
+    assert need(13, 5120, 13824) % (13 * 5120 * 4) == 0 and need(13, 5120, 13824) > 0
+    assert need(0, 16, 128) == 0 and need(5, 24, 128) == 0 and need(5, 16, 100) == 0
 
+    def call(x=A, dtype=0, stride=128, w4=2 * A, s=3 * A, M=4, N=16, K=128, group=128, y=4 * A,
+             ws=None, wb=0):
+        return fq.lib().flexq_gemv_w4(x, dtype, stride, w4, s, M, N, K, group, ws, wb, y, None)
+
+    big = dict(M=13, N=512, K=2048, stride=2048)    # K in slices: a workspace is needed
+    wb = need(13, 512, 2048)
+    assert wb > 0
+    assert call(**big) == INVALID and call(**big, ws=5 * A, wb=wb - 1) == INVALID
+    assert call(**big, ws=5 * A + 8, wb=wb) == UNSUPPORTED
+    for over in (A, 2 * A + 64, 3 * A, 4 * A - 64):
+        assert call(**big, ws=over, wb=wb) == INVALID, over
     for kw in (dict(x=None), dict(w4=None), dict(s=None), dict(y=None), dict(M=-1), dict(N=-16),
                dict(K=0), dict(dtype=-1), dict(stride=120), dict(y=A + 64), dict(y=2 * A + 64),
-               dict(y=3 * A + 8), dict(stride=1 << 20, y=A + (3 << 21))):
+               dict(y=3 * A + 8), dict(stride=1 << 20, y=A + (3 << 20))):
         assert call(**kw) == INVALID, kw
     for kw in (dict(group=48), dict(K=100), dict(N=8), dict(x=A + 8), dict(w4=2 * A + 8),
-               dict(s=3 * A + 2), dict(y=4 * A + 4), dict(stride=132), dict(M=1 << 21)):
+               dict(s=3 * A + 2), dict(y=4 * A + 4), dict(stride=132), dict(M=1 << 21),
+               dict(stride=(1 << 24) + 8), dict(N=1 << 23, K=1 << 14, group=128)):
         assert call(**kw) == UNSUPPORTED, kw
     assert call(M=0, x=None, y=None) == SUCCESS
     assert call(N=0, w4=None, y=None) == SUCCESS

@@ -550,5 +550,6 @@ class W6AxLinear:
 
 
 from .serve import SIGNATURES as SERVE_SIGNATURES  # noqa: E402  (needs the checks above)
-from .serve import (W4Linear, block_tables, gemv_w4, kv_cache, kv_cache_write,  # noqa: E402,F401
-                    pack_w4, tree_attention, tree_attention_workspace_bytes)
+from .serve import (W4Linear, block_tables, gemv_w4, gemv_w4_workspace_bytes,  # noqa: E402,F401
+                    kv_cache, kv_cache_write, pack_w4, tree_attention,
+                    tree_attention_workspace_bytes)

@@ -40,6 +40,7 @@ flexq_status check_w4(int64_t N, int64_t K, int32_t group_size) {
   if (N < 0 || K <= 0) return FLEXQ_ERROR_INVALID_VALUE;
   if (group_size != 32 && group_size != 64 && group_size != 128) return FLEXQ_ERROR_UNSUPPORTED;
   if (N % 16 != 0 || N > kMaxN || K % 128 != 0 || K > kMaxK) return FLEXQ_ERROR_UNSUPPORTED;
+  if (N * (K / group_size) >= (1LL << 29)) return FLEXQ_ERROR_UNSUPPORTED;  // 32-bit offsets
   return FLEXQ_SUCCESS;
 }
 
@@ -97,9 +98,15 @@ flexq_status flexq_pack_w4(const uint16_t* w, int32_t dtype, int64_t N, int64_t 
                                         (hipStream_t)stream));
 }
 
+size_t flexq_gemv_w4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || M > kMaxM || N <= 0 || check_w4(N, K, 128) != FLEXQ_SUCCESS) return 0;
+  return flexq::gemv_w4_workspace_bytes(M, N, K);
+}
+
 flexq_status flexq_gemv_w4(const uint16_t* x, int32_t dtype, int64_t x_stride,
                            const uint32_t* w4, const uint16_t* s_w_fp16, int64_t M, int64_t N,
-                           int64_t K, int32_t group_size, uint16_t* y, void* stream) {
+                           int64_t K, int32_t group_size, void* workspace,
+                           size_t workspace_bytes, uint16_t* y, void* stream) {
   FLEXQ_TRY(check_dtype(dtype));
   if (M < 0) return FLEXQ_ERROR_INVALID_VALUE;
   FLEXQ_TRY(check_w4(N, K, group_size));
@@ -108,19 +115,23 @@ flexq_status flexq_gemv_w4(const uint16_t* x, int32_t dtype, int64_t x_stride,
   if (!x || !w4 || !s_w_fp16 || !y) return FLEXQ_ERROR_INVALID_VALUE;
   if (M > 1) {
     if (x_stride < K) return FLEXQ_ERROR_INVALID_VALUE;
-    if (x_stride % 8 != 0 || x_stride > kMaxStride) return FLEXQ_ERROR_UNSUPPORTED;
+    if (x_stride % 8 != 0 || x_stride > (1LL << 24)) return FLEXQ_ERROR_UNSUPPORTED;
   } else {
     x_stride = K;
   }
-  if (!aligned(x, 16) || !aligned(w4, 16) || !aligned(s_w_fp16, 8) || !aligned(y, 8))
+  const size_t need = flexq::gemv_w4_workspace_bytes(M, N, K);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FLEXQ_ERROR_INVALID_VALUE;
+  if (!aligned(x, 16) || !aligned(w4, 16) || !aligned(s_w_fp16, 8) || !aligned(y, 8) ||
+      !aligned(workspace, 16))
     return FLEXQ_ERROR_UNSUPPORTED;
-  if (any_overlap(range_of(y, (uint64_t)M * N * 2),
-                  {range_of(x, span(1, 0, M, x_stride, K, 2)),
-                   range_of(w4, flexq_packed_w4_bytes(N, K)),
-                   range_of(s_w_fp16, (uint64_t)N * (K / group_size) * 2)}))
+  const Range in[3] = {range_of(x, span(1, 0, M, x_stride, K, 2)),
+                       range_of(w4, flexq_packed_w4_bytes(N, K)),
+                       range_of(s_w_fp16, (uint64_t)N * (K / group_size) * 2)};
+  const Range ry = range_of(y, (uint64_t)M * N * 2), ws = range_of(workspace, need);
+  if (any_overlap(ry, {in[0], in[1], in[2], ws}) || any_overlap(ws, {in[0], in[1], in[2]}))
     return FLEXQ_ERROR_INVALID_VALUE;
   return launched(flexq::launch_gemv_w4(x, dtype == FLEXQ_BF16, x_stride, w4, s_w_fp16, M, N, K,
-                                        group_size, y, (hipStream_t)stream));
+                                        group_size, workspace, y, (hipStream_t)stream));
 }
 
 flexq_status flexq_block_tables(const int32_t* ctx_lens, const int32_t* new_lens, int64_t B,

@@ -4,6 +4,8 @@
 // Y[m][n] = sum_g s[g][n] * sum_{k in g} x[m][k] q[n][k].  A 16-bit activation times a
 // code in [-8, 7] is exact in fp32, so the MFMA sums a group's products without an
 // earlier rounding and the scale is applied once per group in fp32.
+#include <algorithm>
+
 #include "kernels.h"
 #include "serve_device.h"
 #include "serve_kernels.h"
@@ -11,6 +13,34 @@
 namespace flexq {
 
 namespace {
+
+constexpr uint32_t kRsrcWord3 = 0x00020000u;  // raw 32-bit dword buffer, gfx9 style
+constexpr int kNonTemporal = 2;                // cache-policy bit of buffer loads
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes,
+                                           kRsrcWord3);
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+// s_waitcnt vmcnt(N) alone (gfx9 encoding: vmcnt[3:0], expcnt[6:4], lgkmcnt[11:8],
+// vmcnt[5:4] in [15:14]).
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+// 16 bytes a lane from memory to LDS: lane l's at `to` + 16 l, zeros past the buffer.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, char* to, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr_t)to, 16, off, 0, 0, 0);
+}
+
+// A barrier for what went through LDS alone: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 
 // dword of row n, column k = 128 kb + 32 j + 8 p (+ c)
 __device__ __forceinline__ int64_t w4_dword(int64_t n, int kb, int j, int p, int64_t kbs) {
@@ -52,71 +82,461 @@ __global__ __launch_bounds__(256) void pack_w4_kernel(const uint16_t* __restrict
   if ((k0 & (G - 1)) == 0) sw[(int64_t)(k0 / G) * N + n] = s16;
 }
 
-// One workgroup = one 16-row tile of the weight x up to 16 NT activation rows; its W waves
-// take the 128-deep k-blocks in turn and their sums are added in wave order at the end.
-// D of the MFMA: column = activation row, rows = weight rows 4 (lane / 16) + i.
-template <class E, int G, int NT, int W>
-__global__ __launch_bounds__(64 * W) void gemv_w4_kernel(
+// Both kernels below are bound by HBM (0.5 byte a weight) up to some 30 rows.
+//
+// A code u = q + 8 becomes a 16-bit float with its four bits as the top of the mantissa
+// of 16 + u = q + 24: two bit operations for two codes, and the sum over a group starts
+// from -24 sum x, which one more MFMA (a constant matrix) forms for all T tiles.  The
+// products are exact in fp32 and at most 31 |x|, so the sums lose up to three bits of
+// fp32 against those of q itself, far below the output's rounding.  With an infinite or NaN
+// activation, or near the top of the range, that difference is not a number where the
+// definition may be one; such a group is taken again with the codes' own values.
+template <class E>
+struct Code;
+template <>
+struct Code<Half> {
+  static constexpr int kShift = 6;  // of u in the mantissa
+  static constexpr uint32_t kBase = 0x4C004C00u, kMinus24 = 0xCE00CE00u;
+};
+template <>
+struct Code<Bfloat> {
+  static constexpr int kShift = 3;
+  static constexpr uint32_t kBase = 0x41804180u, kMinus24 = 0xC1C0C1C0u;
+};
+
+// Eight codes as q + 24.  mask and base are Code<E>'s, held in a scalar and a vector
+// register so that each pair is a shift and one and-or (a literal apiece would not fit).
+template <class E>
+__device__ __forceinline__ u32x4 codes_plus_24(uint32_t d, uint32_t mask, uint32_t base) {
+  u32x4 a;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int up = Code<E>::kShift - 4 * i;
+    a[i] = ((up >= 0 ? d << up : d >> -up) & mask) | base;
+  }
+  return a;
+}
+
+// eight codes as q
+template <class E>
+__device__ __forceinline__ u32x4 codes(uint32_t d) {
+  u32x4 a;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int lo = (int)((d >> (4 * i)) & 15u) - 8, hi = (int)((d >> (4 * i + 16)) & 15u) - 8;
+    a[i] = E::bits((float)lo) | (uint32_t)E::bits((float)hi) << 16;
+  }
+  return a;
+}
+
+// acc += scale * dot, four consecutive weight rows
+__device__ __forceinline__ void scale_add(f32x4& acc, f32x4 dot, u32x2 scales) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    acc[i] = fmaf(half_bits_to_float((uint16_t)(scales[i >> 1] >> (16 * (i & 1)))), dot[i], acc[i]);
+}
+
+__device__ __forceinline__ bool not_finite(f32x4 v) {
+  return fmaf(v[0], 0.0f, v[1] * 0.0f) + fmaf(v[2], 0.0f, v[3] * 0.0f) != 0.0f;
+}
+
+template <class E>
+__device__ __forceinline__ void store_four(uint16_t* to, f32x4 v) {
+  u32x2 o;
+  o[0] = E::bits(v[0]) | (uint32_t)E::bits(v[1]) << 16;
+  o[1] = E::bits(v[2]) | (uint32_t)E::bits(v[3]) << 16;
+  *reinterpret_cast<u32x2*>(to) = o;
+}
+
+// acc[n] += k-block kb of a tile with the codes' own values, straight from memory
+template <class E, int G, int NT>
+__device__ __forceinline__ void exact_block(f32x4* acc, const uint32_t* w4, const uint16_t* sw,
+                                            const uint16_t* x, int64_t x_stride, int rows, int N,
+                                            int kbs, int tile, int kb) {
+  const int lane = threadIdx.x & 63, c = lane & 15, p = lane >> 4;
+  const u32x4 w = reinterpret_cast<const u32x4*>(w4)[((int64_t)tile * kbs + kb) * 64 + lane];
+#pragma unroll
+  for (int g = 0; g < 128 / G; ++g) {
+    const u32x2 scales = *reinterpret_cast<const u32x2*>(
+        sw + (int64_t)(kb * (128 / G) + g) * N + tile * 16 + 4 * p);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint16_t* row = x + (int64_t)min(n * 16 + c, rows - 1) * x_stride + kb * 128 + p * 8;
+      f32x4 dot = {};
+#pragma unroll
+      for (int j = g * (G / 32); j < (g + 1) * (G / 32); ++j)
+        dot = E::mfma(codes<E>(w[j]), *reinterpret_cast<const u32x4*>(row + j * 32), dot);
+      scale_add(acc[n], dot, scales);
+    }
+  }
+}
+
+// Up to four rows.  An item is T adjacent 16-row tiles of the weight; a persistent
+// workgroup owns a run of items, its W waves take the 128-deep k-blocks of an item in turn
+// (a wave's part of a tile and k-block is 1 KB in one piece), and the waves' sums are added
+// in wave order through LDS.  P steps of loads are in flight, on into the next item.
+//
+// All loads are buffer loads and no branch is around one, so that the waits count exactly
+// the steps in flight.  The addresses only ever grow by constants (the scalar unit is
+// shared by all waves: address arithmetic was what bound an earlier form).  A step past K
+// loads some other weights and zero scales, one past the run nothing that is used.
+//
+// The activations are in LDS, rows K + 32 elements apart, so that only the weights and
+// scales take registers in flight; lanes without a row read the last one's (their columns
+// are not stored).
+template <class E, int G, int T, int W, int P>
+__global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
     const uint16_t* __restrict__ x, int64_t x_stride, const uint32_t* __restrict__ w4,
-    const uint16_t* __restrict__ sw, int M, int N, int K, uint16_t* __restrict__ y) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint16_t* __restrict__ sw, int M, int N, int K, int tiles, int items,
+    uint16_t* __restrict__ y) {
+  constexpr int kGroups = 128 / G;  // of a k-block
+  constexpr int kSteps = G / 32;    // MFMAs of a group
+  extern __shared__ __attribute__((aligned(16))) uint16_t lds_x[];
+  __shared__ f32x4 part[2][W][T][64];
+  __shared__ int again;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, p = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int m0 = blockIdx.y * 64;
   const int kbs = K >> 7;
-  const u32x4* wt = reinterpret_cast<const u32x4*>(w4) + blockIdx.x * (int64_t)kbs * 64 + lane;
-  f32x4 acc[NT] = {};
-  for (int kb = wave; kb < kbs; kb += W) {
-    const u32x4 d = wt[(int64_t)kb * 64];
+  const int rounds = (kbs + W - 1) / W;
+  const int first = (int)((int64_t)items * blockIdx.x / gridDim.x);
+  const int last = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
+
+  struct Slot {
+    u32x4 w[T];
+    u32x2 s[T][kGroups];
+  } ring[P];
+
+  // Loads of one wave step: k-block kb of item, which the offsets stand for.
+  const int64_t run = (int64_t)first * T * kbs * 1024;
+  const auto rw = make_rsrc(reinterpret_cast<const char*>(w4) + run,
+                            (uint32_t)((int64_t)min(last * T, tiles) * kbs * 1024 - run));
+  const auto rs = make_rsrc(sw + first * T * 16,
+                            (uint32_t)((int64_t)(K / G) * N * 2 - (int64_t)first * T * 32));
+  int kb = wave;
+  uint32_t w_off = wave * 1024 + lane * 16, s_off = (uint32_t)wave * kGroups * (N * 2) + 8 * p;
+  uint32_t s_item = 0;
+  auto next_load = [&](Slot& r) {
 #pragma unroll
-    for (int g = 0; g < 128 / G; ++g) {
-      const uint16_t* sp = sw + (int64_t)(kb * (128 / G) + g) * N + n0 + 4 * p;
-      f32x4 dot[NT] = {};
+    for (int t = 0; t < T; ++t) {
+      r.w[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             rw, w_off + t * (kbs * 1024), 0, kNonTemporal));
 #pragma unroll
-      for (int jj = 0; jj < G / 32; ++jj) {
-        const int j = g * (G / 32) + jj;
-        u32x4 a;
+      for (int g = 0; g < kGroups; ++g)
+        r.s[t][g] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                                                  rs, s_off + g * (N * 2) + t * 32, 0, 0));
+    }
+    kb += W;
+    w_off += W * 1024;
+    s_off += W * kGroups * (N * 2);
+    if (kb >= rounds * W) {  // the next item
+      kb = wave;
+      w_off += (T * kbs - rounds * W) * 1024;
+      s_item += T * 32;
+      s_off = (uint32_t)wave * kGroups * (N * 2) + s_item + 8 * p;
+    }
+  };
+
+  uint32_t mask = 0x000F000Fu << Code<E>::kShift, base = Code<E>::kBase;
+  asm("" : "+s"(mask));
+  asm("" : "+v"(base));
+  const uint32_t m24 = Code<E>::kMinus24;
+  const u32x4 minus24 = {m24, m24, m24, m24};
+  const uint16_t* lds_row = lds_x + min(c, M - 1) * (K + 32) + p * 8;
+
+  f32x4 acc[T] = {};
+  auto work = [&](const Slot& r, int round) {
+    // past K the scales are zero, and any activations will do that are a row's
+    const uint16_t* at = lds_row + min(round * W + wave, kbs - 1) * 128;
+    u32x4 xf[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int lo = (int)((d[j] >> (4 * i)) & 15u) - 8;
-          const int hi = (int)((d[j] >> (4 * i + 16)) & 15u) - 8;
-          a[i] = E::bits((float)lo) | (uint32_t)E::bits((float)hi) << 16;
-        }
+    for (int j = 0; j < 4; ++j) xf[j] = *reinterpret_cast<const u32x4*>(at + j * 32);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int m = m0 + t * 16 + c;
-          u32x4 b = {};
-          if (m < M)
-            b = *reinterpret_cast<const u32x4*>(x + m * x_stride + kb * 128 + j * 32 + p * 8);
-          dot[t] = E::mfma(a, b, dot[t]);
-        }
+    for (int g = 0; g < kGroups; ++g) {
+      f32x4 start = {};
+#pragma unroll
+      for (int j = g * kSteps; j < (g + 1) * kSteps; ++j) start = E::mfma(minus24, xf[j], start);
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        f32x4 dot = start;
+#pragma unroll
+        for (int j = g * kSteps; j < (g + 1) * kSteps; ++j)
+          dot = E::mfma(codes_plus_24<E>(r.w[t][j], mask, base), xf[j], dot);
+        scale_add(acc[t], dot, r.s[t][g]);
       }
+    }
+  };
+
+  // the waves' sums, in order; a sum that is not finite is formed again at the end
+  auto finish = [&](int item) {
+    f32x4(*to)[T][64] = part[item & 1];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float s = half_bits_to_float(sp[i]);
+    for (int t = 0; t < T; ++t) {
+      to[wave][t][lane] = acc[t];
+      acc[t] = f32x4{};
+    }
+    lds_barrier();  // (the next item's sums go to the other half)
+    const int t = (wave + item) % W, tile = item * T + t;
+    if (t < T && tile < tiles) {
+      f32x4 s = to[0][t][lane];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t][i] = fmaf(s, dot[t][i], acc[t][i]);
+      for (int v = 1; v < W; ++v) {
+        const f32x4 o = to[v][t][lane];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] += o[k];
+      }
+      if (c < M) {
+        if (not_finite(s)) again = 1;
+        store_four<E>(y + (int64_t)c * N + tile * 16 + 4 * p, s);
+      }
+    }
+  };
+
+  if (threadIdx.x == 0) again = 0;
+  const int pieces = K / 8;  // 16 bytes each
+  for (int i = threadIdx.x; i < M * pieces; i += 64 * W) {
+    const int row = i / pieces, k8 = i % pieces;
+    *reinterpret_cast<u32x4*>(lds_x + row * (K + 32) + k8 * 8) =
+        *reinterpret_cast<const u32x4*>(x + row * x_stride + k8 * 8);
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    next_load(ring[i]);
+    __builtin_amdgcn_sched_barrier(0);  // the waits count on the steps' order
+  }
+  lds_barrier();  // the activations are there
+  int item = first, round = 0;
+  const int steps = (last - first) * rounds;
+  for (int step = 0; step < steps; step += P) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      work(ring[i], round);
+      __builtin_amdgcn_sched_barrier(0);
+      next_load(ring[i]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (++round == rounds) {
+        if (item < last) finish(item);
+        round = 0;
+        ++item;
       }
     }
   }
-  __shared__ f32x4 part[W][NT][64];
+
+  lds_barrier();
+  if (again == 0) return;
+  // Rare: the codes' own values, a k-block at a time.
+  for (item = first; item < last; ++item) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) part[wave][t][lane] = acc[t];
-  __syncthreads();
-  for (int t = wave; t < NT; t += W) {
-    f32x4 s = part[0][t][lane];
+    for (int t = 0; t < T; ++t) {
+      acc[t] = f32x4{};  // the steps past the run left something here
+      const int tile = min(item * T + t, tiles - 1);
+      for (kb = wave; kb < kbs; kb += W)
+        exact_block<E, G, 1>(&acc[t], w4, sw, x, x_stride, M, N, kbs, tile, kb);
+    }
+    finish(item);
+  }
+}
+
+// More rows: a product of 128 T weight rows (T tiles for each of eight waves) and 16 NT rows
+// of x over a slice of K.  A few k-blocks of x at a time go to LDS, straight from memory and
+// shared by the waves; each wave streams its own weights into registers.  Both are two
+// chunks ahead.  Where the weight has too few rows to fill the GPU, K is cut into slices
+// whose fp32 sums go to part [slice][M][N], and join_slices_kernel adds them in order.
+//
+// In LDS a kilobyte block holds eight rows x 128 bytes, loaded as eight whole cache lines;
+// the 16-byte pieces are placed so that the 16 lanes of a fragment read (16 rows, one
+// piece each) meet 16 different banks: piece k of row r at slot 8 (r ^ h) + (k ^ r), h the
+// block's parity.
+constexpr int chunk_blocks(int NT) { return NT == 1 ? 4 : 2; }
+
+template <class E, int G, int NT, int T>
+__global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
+    const uint16_t* __restrict__ x, int64_t x_stride, const uint32_t* __restrict__ w4,
+    const uint16_t* __restrict__ sw, int M, int N, int K, int tiles, int slices,
+    float* __restrict__ part, uint16_t* __restrict__ y) {
+  constexpr int kGroups = 128 / G, kSteps = G / 32;
+  constexpr int kChunk = chunk_blocks(NT);             // k-blocks
+  constexpr int kBlocks = 2 * NT;                      // of eight rows
+  constexpr int kBytes = kChunk * 2 * kBlocks * 1024;  // of x a chunk
+  constexpr int kMine = kChunk * kBlocks / 4;          // kilobytes of it a wave stages
+  constexpr int kAhead = 2;
+  constexpr uint32_t kNowhere = 0x80000000u;
+  __shared__ __attribute__((aligned(1024))) char lds[(kAhead + 1) * kBytes];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, p = lane >> 4;
+  const int m0 = blockIdx.y * 64;
+  const int kbs = K >> 7, chunks = (kbs + kChunk - 1) / kChunk;
+  const int slice = blockIdx.x % slices;
+  const int tile0 = (blockIdx.x / slices * 8 + wave) * T;
+  const int first = (int)((int64_t)chunks * slice / slices);
+  const int last = (int)((int64_t)chunks * (slice + 1) / slices);
+  const int rows = min(M - m0, 16 * NT);
+  const uint16_t* x0 = x + (int64_t)m0 * x_stride;
+
+  // x: this wave's k-block of a chunk, half of it, and blocks; the lane's row and piece
+  const int at = wave * kMine;
+  const int my_kb = at / (2 * kBlocks), my_half = at / kBlocks % 2, my_block = at % kBlocks;
+  const auto rx = make_rsrc(x0, (uint32_t)((rows - 1) * x_stride + K) * 2u);
+  uint32_t x_off[kMine];
 #pragma unroll
-    for (int v = 1; v < W; ++v)
+  for (int i = 0; i < kMine; ++i) {
+    const int b = my_block + i;
+    const int row8 = (lane >> 3) ^ (b & 1), piece = (lane & 7) ^ row8, row = b * 8 + row8;
+    x_off[i] = row < rows ? (uint32_t)(row * x_stride) * 2u + my_half * 128u + piece * 16u
+                          : kNowhere;
+  }
+  auto stage = [&](int chunk) {
+    const int kb = chunk * kChunk + my_kb;
+    const uint32_t k_off = kb < kbs ? kb * 256u : kNowhere;
+    char* to = lds + chunk % (kAhead + 1) * kBytes + at * 1024;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] += part[v][t][lane][i];
-    const int m = m0 + t * 16 + c;
-    if (m < M) {
-      u32x2 o;
-      o[0] = E::bits(s[0]) | (uint32_t)E::bits(s[1]) << 16;
-      o[1] = E::bits(s[2]) | (uint32_t)E::bits(s[3]) << 16;
-      *reinterpret_cast<u32x2*>(y + (int64_t)m * N + n0 + 4 * p) = o;
+    for (int i = 0; i < kMine; ++i)
+      load_to_lds(rx, to + i * 1024, x_off[i] == kNowhere ? kNowhere : x_off[i] + k_off);
+  };
+
+  struct Chunk {
+    u32x4 w[kChunk][T];
+    u32x2 s[kChunk][T][kGroups];
+  } ring[kAhead];
+  const auto rw = make_rsrc(reinterpret_cast<const char*>(w4) + (int64_t)tile0 * kbs * 1024,
+                            (uint32_t)(max(0, min(T, tiles - tile0)) * kbs) * 1024u);
+  const auto rs = make_rsrc(sw + tile0 * 16, tile0 < tiles ? (uint32_t)((int64_t)(K / G) * N * 2 -
+                                                                       (int64_t)tile0 * 32)
+                                                           : 0u);
+  auto load = [&](Chunk& r, int chunk) {
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      const int kb = chunk * kChunk + i;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        r.w[i][t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  rw, (t * kbs + kb) * 1024 + lane * 16, 0,
+                                                  kNonTemporal));
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+          r.s[i][t][g] = __builtin_bit_cast(
+              u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                         rs, (kb * kGroups + g) * (N * 2) + t * 32 + 8 * p, 0, 0));
+      }
+    }
+  };
+
+  uint32_t mask = 0x000F000Fu << Code<E>::kShift, base = Code<E>::kBase;
+  asm("" : "+s"(mask));
+  asm("" : "+v"(base));
+  const uint32_t m24 = Code<E>::kMinus24;
+  const u32x4 minus24 = {m24, m24, m24, m24};
+  const int row8 = c & 7, h = c >> 3;
+  const int frag_row = h * 1024 + ((row8 ^ h) * 8) * 16;
+  f32x4 acc[T][NT] = {};
+  auto work = [&](const Chunk& r, int chunk) {
+    const char* from = lds + chunk % (kAhead + 1) * kBytes;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      u32x4 xf[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          xf[n][j] = *reinterpret_cast<const u32x4*>(
+              from + ((i * 2 + (j >> 1)) * kBlocks + 2 * n) * 1024 + frag_row +
+              ((((j & 1) * 4 + p) ^ row8) * 16));
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        f32x4 start[NT] = {};
+#pragma unroll
+        for (int j = g * kSteps; j < (g + 1) * kSteps; ++j)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) start[n] = E::mfma(minus24, xf[n][j], start[n]);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          f32x4 dot[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) dot[n] = start[n];
+#pragma unroll
+          for (int j = g * kSteps; j < (g + 1) * kSteps; ++j) {
+            const u32x4 a = codes_plus_24<E>(r.w[i][t][j], mask, base);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) dot[n] = E::mfma(a, xf[n][j], dot[n]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) scale_add(acc[t][n], dot[n], r.s[i][t][g]);
+        }
+      }
+    }
+  };
+
+  // A chunk's loads: kMine of x, then the weights' and scales'.  Chunks past the slice
+  // are loaded too (the waits count on them) and not used.
+  constexpr int kLoads = kMine + kChunk * T * (1 + kGroups);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    stage(first + i);
+    __builtin_amdgcn_sched_barrier(0);
+    load(ring[i], first + i);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int chunk = first; chunk < last; chunk += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      // this wave's part of the chunk has come, then everyone's, and the one before is read
+      wait_vm<(kAhead - 1) * kLoads>();
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      stage(chunk + i + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+      if (chunk + i < last) work(ring[i], chunk + i);
+      __builtin_amdgcn_sched_barrier(0);
+      load(ring[i], chunk + i + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+
+  bool bad = false;
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) bad |= not_finite(acc[t][n]);
+  const bool again = __ballot(bad) != 0;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int tile = tile0 + t;
+    if (tile >= tiles) continue;
+    if (again) {  // rare: the codes' own values
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[t][n] = f32x4{};
+      for (int kb = first * kChunk; kb < min(last * kChunk, kbs); ++kb)
+        exact_block<E, G, NT>(acc[t], w4, sw, x0, x_stride, rows, N, kbs, tile, kb);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (n * 16 + c >= rows) continue;
+      const int64_t at = (int64_t)(m0 + n * 16 + c) * N + tile * 16 + 4 * p;
+      if (slices > 1)
+        *reinterpret_cast<f32x4*>(part + (int64_t)slice * M * N + at) = acc[t][n];
+      else
+        store_four<E>(y + at, acc[t][n]);
+    }
+  }
+}
+
+// y = the slices' sums, added in order
+template <class E>
+__global__ __launch_bounds__(256) void join_slices_kernel(const float* __restrict__ part,
+                                                          int64_t quads, int slices,
+                                                          uint16_t* __restrict__ y) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= quads) return;
+  const f32x4* from = reinterpret_cast<const f32x4*>(part) + i;
+  f32x4 s = from[0];
+#pragma unroll 4
+  for (int v = 1; v < slices; ++v) {
+    const f32x4 o = from[v * quads];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] += o[k];
+  }
+  store_four<E>(y + 4 * i, s);
 }
 
 namespace {
@@ -131,29 +551,81 @@ hipError_t pack_any(const uint16_t* w, int64_t N, int64_t K, int group, uint32_t
   return launch_kernel(kernel, grid, dim3(256), stream, w, (int)N, (int)K, w4, sw);
 }
 
+// The few-rows kernel: two workgroups' activations and sums fit a compute unit's LDS.
+bool few_rows(int64_t M, int64_t K) { return M <= 4 && M * (K + 32) * 2 <= 48 * 1024; }
+
+// The other one: tiles a wave, and slices of K that give every compute unit two
+// workgroups of the 16 waves it holds.
+struct Cut {
+  int tiles_a_wave, slices;
+};
+
+Cut cut_of(int64_t M, int64_t N, int64_t K) {
+  Cut cut;
+  cut.tiles_a_wave = 1;
+  const int64_t units = (N / 16 + 7) / 8 * ((M + 63) / 64);
+  const int64_t chunk = chunk_blocks(M <= 16 ? 1 : M <= 32 ? 2 : 4);
+  const int64_t chunks = (K / 128 + chunk - 1) / chunk;
+  const int64_t target = 2 * device_cu_count();
+  cut.slices = (int)std::clamp<int64_t>(target / units, 1, std::min<int64_t>(chunks, 16));
+  return cut;
+}
+
+template <class E, int G, int T>
+hipError_t gemv_launch(const uint16_t* x, int64_t x_stride, const uint32_t* w4,
+                       const uint16_t* sw, int64_t M, int64_t N, int64_t K, uint16_t* y,
+                       hipStream_t stream) {
+  constexpr int W = 8, P = (G == 32 ? 4 : 6) / T;
+  const int64_t tiles = N / 16, items = (tiles + T - 1) / T;
+  const int64_t most = device_cu_count() * (16 / W);  // 16 waves a compute unit
+  return launch_kernel_lds(gemv_w4_kernel<E, G, T, W, P>, dim3((unsigned)std::min(items, most)),
+                           dim3(64 * W), M * (K + 32) * 2, stream, x, x_stride, w4, sw, (int)M,
+                           (int)N, (int)K, (int)tiles, (int)items, y);
+}
+
+template <class E, int G, int NT>
+hipError_t gemm_launch(const uint16_t* x, int64_t x_stride, const uint32_t* w4,
+                       const uint16_t* sw, int64_t M, int64_t N, int64_t K, float* part,
+                       uint16_t* y, hipStream_t stream) {
+  constexpr int T = 1;
+  const Cut cut = cut_of(M, N, K);
+  const int64_t tiles = N / 16;
+  const dim3 grid((unsigned)((tiles + 8 * T - 1) / (8 * T) * cut.slices),
+                  (unsigned)((M + 63) / 64));
+  const hipError_t e =
+      launch_kernel(gemm_w4_kernel<E, G, NT, T>, grid, dim3(512), stream, x, x_stride, w4, sw, (int)M, (int)N, (int)K, (int)tiles, cut.slices, part, y);
+  if (e != hipSuccess || cut.slices == 1) return e;
+  const int64_t quads = M * N / 4;
+  return launch_kernel(join_slices_kernel<E>, dim3((unsigned)((quads + 255) / 256)), dim3(256),
+                       stream, part, quads, cut.slices, y);
+}
+
 template <class E, int G>
 hipError_t gemv_any(const uint16_t* x, int64_t x_stride, const uint32_t* w4, const uint16_t* sw,
-                    int64_t M, int64_t N, int64_t K, uint16_t* y, hipStream_t stream) {
-  constexpr int W = 4;
-  const int64_t rows = M < 64 ? M : 64;
-  const dim3 grid((unsigned)(N / 16), (unsigned)((M + 63) / 64));
-  auto* kernel = rows <= 16   ? gemv_w4_kernel<E, G, 1, W>
-                 : rows <= 32 ? gemv_w4_kernel<E, G, 2, W>
-                              : gemv_w4_kernel<E, G, 4, W>;
-  return launch_kernel(kernel, grid, dim3(64 * W), stream, x, x_stride, w4, sw, (int)M, (int)N,
-                       (int)K, y);
+                    int64_t M, int64_t N, int64_t K, float* part, uint16_t* y,
+                    hipStream_t stream) {
+  if (few_rows(M, K)) return gemv_launch<E, G, 1>(x, x_stride, w4, sw, M, N, K, y, stream);
+  if (M <= 16) return gemm_launch<E, G, 1>(x, x_stride, w4, sw, M, N, K, part, y, stream);
+  if (M <= 32) return gemm_launch<E, G, 2>(x, x_stride, w4, sw, M, N, K, part, y, stream);
+  return gemm_launch<E, G, 4>(x, x_stride, w4, sw, M, N, K, part, y, stream);
 }
 
 template <class E>
 hipError_t gemv_group(const uint16_t* x, int64_t x_stride, const uint32_t* w4,
-                      const uint16_t* sw, int64_t M, int64_t N, int64_t K, int group, uint16_t* y,
-                      hipStream_t stream) {
-  if (group == 32) return gemv_any<E, 32>(x, x_stride, w4, sw, M, N, K, y, stream);
-  if (group == 64) return gemv_any<E, 64>(x, x_stride, w4, sw, M, N, K, y, stream);
-  return gemv_any<E, 128>(x, x_stride, w4, sw, M, N, K, y, stream);
+                      const uint16_t* sw, int64_t M, int64_t N, int64_t K, int group, float* part,
+                      uint16_t* y, hipStream_t stream) {
+  if (group == 32) return gemv_any<E, 32>(x, x_stride, w4, sw, M, N, K, part, y, stream);
+  if (group == 64) return gemv_any<E, 64>(x, x_stride, w4, sw, M, N, K, part, y, stream);
+  return gemv_any<E, 128>(x, x_stride, w4, sw, M, N, K, part, y, stream);
 }
 
 }  // namespace
+
+size_t gemv_w4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (few_rows(M, K)) return 0;
+  const int slices = cut_of(M, N, K).slices;
+  return slices == 1 ? 0 : (size_t)slices * M * N * sizeof(float);
+}
 
 hipError_t launch_pack_w4(const uint16_t* w, bool bf16, int64_t N, int64_t K, int group,
                           uint32_t* w4, uint16_t* sw, hipStream_t stream) {
@@ -163,9 +635,10 @@ hipError_t launch_pack_w4(const uint16_t* w, bool bf16, int64_t N, int64_t K, in
 
 hipError_t launch_gemv_w4(const uint16_t* x, bool bf16, int64_t x_stride, const uint32_t* w4,
                           const uint16_t* sw, int64_t M, int64_t N, int64_t K, int group,
-                          uint16_t* y, hipStream_t stream) {
-  return bf16 ? gemv_group<Bfloat>(x, x_stride, w4, sw, M, N, K, group, y, stream)
-              : gemv_group<Half>(x, x_stride, w4, sw, M, N, K, group, y, stream);
+                          void* workspace, uint16_t* y, hipStream_t stream) {
+  float* part = static_cast<float*>(workspace);
+  return bf16 ? gemv_group<Bfloat>(x, x_stride, w4, sw, M, N, K, group, part, y, stream)
+              : gemv_group<Half>(x, x_stride, w4, sw, M, N, K, group, part, y, stream);
 }
 
 }  // namespace flexq

@@ -11,7 +11,8 @@ hipError_t launch_pack_w4(const uint16_t* w, bool bf16, int64_t N, int64_t K, in
 
 hipError_t launch_gemv_w4(const uint16_t* x, bool bf16, int64_t x_stride, const uint32_t* w4,
                           const uint16_t* sw, int64_t M, int64_t N, int64_t K, int group,
-                          uint16_t* y, hipStream_t stream);
+                          void* workspace, uint16_t* y, hipStream_t stream);
+size_t gemv_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 // most requests a step holds (their prefix sums sit in LDS)
 constexpr int64_t kMaxRequests = 4096;

@@ -25,7 +25,9 @@ _P, _I64, _I32, _SZ, _F = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctyp
 SIGNATURES = {
     "flexq_packed_w4_bytes": (_SZ, [_I64, _I64]),
     "flexq_pack_w4": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _P, _P, _P]),
-    "flexq_gemv_w4": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _I64, _I64, _I64, _I32, _P, _P]),
+    "flexq_gemv_w4": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _I64, _I64, _I64, _I32, _P, _SZ, _P,
+                                     _P]),
+    "flexq_gemv_w4_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "flexq_block_tables": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _P, _I32, _P, _I64, _I64, _P,
                                           _P, _P, _P]),
     "flexq_kv_cache_write": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64,
@@ -80,6 +82,12 @@ def _call(name: str, dev, *args):
         raise _fq.FlexqError(status, name)
 
 
+def _workspace(t, need: int):
+    if isinstance(t, torch.Tensor) and t.dim() != 1:
+        raise ValueError(f"workspace must be 1-D, got shape {tuple(t.shape)}")
+    return _fq._tensor(t, torch.uint8, "workspace", min_bytes=need)
+
+
 def _group(group: int) -> int:
     if group not in (32, 64, 128):
         raise ValueError(f"group = {group} must be 32, 64 or 128")
@@ -113,8 +121,12 @@ def pack_w4(w: torch.Tensor, group: int = 128, w4: torch.Tensor | None = None,
     return w4, s_w
 
 
+def gemv_w4_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_fq.lib().flexq_gemv_w4_workspace_bytes(M, N, K))
+
+
 def gemv_w4(x: torch.Tensor, w4: torch.Tensor, s_w: torch.Tensor, N: int,
-            y: torch.Tensor | None = None):
+            y: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """Y[M][N] = X[M][K] times the 4-bit weights (flexq_gemv_w4), X and Y fp16 or bf16,
     X's rows contiguous (they may be strided); the group size is K / len(s_w).  Meant for
     few rows: the weights are read once per 64 of them."""
@@ -134,9 +146,16 @@ def gemv_w4(x: torch.Tensor, w4: torch.Tensor, s_w: torch.Tensor, N: int,
     if y is None:
         y = torch.empty((M, N), dtype=x.dtype, device=x.device)
     _fq._tensor(y, x.dtype, "y", shape=(M, N))
-    dev = _fq._on_gpu(x=x, w4=w4, s_w=s_w, y=y)
+    need = gemv_w4_workspace_bytes(M, N, K)
+    tensors = dict(x=x, w4=w4, s_w=s_w, y=y)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    if workspace is not None:
+        tensors["workspace"] = _workspace(workspace, need)
+    dev = _fq._on_gpu(**tensors)
     _call("flexq_gemv_w4", dev, x.data_ptr(), code, x.stride(0), w4.data_ptr(), s_w.data_ptr(), M,
-          N, K, K // G, y.data_ptr())
+          N, K, K // G, workspace.data_ptr() if workspace is not None else None,
+          workspace.numel() if workspace is not None else 0, y.data_ptr())
     return y
 
 
@@ -295,9 +314,7 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     need = tree_attention_workspace_bytes(B, max_new, H, Hkv, D)
     if workspace is None:
         workspace = torch.empty(max(16, need), dtype=torch.uint8, device=dev)
-    if isinstance(workspace, torch.Tensor) and workspace.dim() != 1:
-        raise ValueError(f"workspace must be 1-D, got shape {tuple(workspace.shape)}")
-    tensors["workspace"] = _fq._tensor(workspace, torch.uint8, "workspace", min_bytes=need)
+    tensors["workspace"] = _workspace(workspace, need)
     dev = _fq._on_gpu(**tensors)
     _call("flexq_tree_attention", dev, q.data_ptr(), code, q.stride(0), q.stride(1),
           k_cache.data_ptr(), v_cache.data_ptr(), pages, page, block_table.data_ptr(), max_blocks,
