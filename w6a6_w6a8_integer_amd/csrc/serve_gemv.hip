@@ -307,15 +307,16 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
   lds_barrier();  // the activations are there
   int item = first, round = 0;
   const int steps = (last - first) * rounds;
-  for (int step = 0; step < steps; step += P) {
+  for (int step = 0; item < last; step += P) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
+      if (step + i >= steps) break;
       work(ring[i], round);
       __builtin_amdgcn_sched_barrier(0);
       next_load(ring[i]);
       __builtin_amdgcn_sched_barrier(0);
       if (++round == rounds) {
-        if (item < last) finish(item);
+        finish(item);
         round = 0;
         ++item;
       }
@@ -377,7 +378,7 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
   // x: this wave's k-block of a chunk, half of it, and blocks; the lane's row and piece
   const int at = wave * kMine;
   const int my_kb = at / (2 * kBlocks), my_half = at / kBlocks % 2, my_block = at % kBlocks;
-  const auto rx = make_rsrc(x0, (uint32_t)((rows - 1) * x_stride + K) * 2u);
+  const uint32_t x_bytes = (uint32_t)((rows - 1) * x_stride + K) * 2u;
   uint32_t x_off[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
@@ -388,36 +389,41 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
   }
   auto stage = [&](int chunk) {
     const int kb = chunk * kChunk + my_kb;
-    const uint32_t k_off = kb < kbs ? kb * 256u : kNowhere;
+    const auto rx = make_rsrc(x0, kb < kbs && chunk < last ? x_bytes : 0u);
     char* to = lds + chunk % (kAhead + 1) * kBytes + at * 1024;
 #pragma unroll
-    for (int i = 0; i < kMine; ++i)
-      load_to_lds(rx, to + i * 1024, x_off[i] == kNowhere ? kNowhere : x_off[i] + k_off);
+    for (int i = 0; i < kMine; ++i)  // (no row: past the buffer still with K added)
+      load_to_lds(rx, to + i * 1024, x_off[i] + kb * 256u);
   };
 
   struct Chunk {
     u32x4 w[kChunk][T];
     u32x2 s[kChunk][T][kGroups];
   } ring[kAhead];
-  const auto rw = make_rsrc(reinterpret_cast<const char*>(w4) + (int64_t)tile0 * kbs * 1024,
-                            (uint32_t)(max(0, min(T, tiles - tile0)) * kbs) * 1024u);
-  const auto rs = make_rsrc(sw + tile0 * 16, tile0 < tiles ? (uint32_t)((int64_t)(K / G) * N * 2 -
-                                                                       (int64_t)tile0 * 32)
-                                                           : 0u);
+  const char* w0 = reinterpret_cast<const char*>(w4) + (int64_t)tile0 * kbs * 1024;
+  const uint32_t w_bytes = (uint32_t)(max(0, min(T, tiles - tile0)) * kbs) * 1024u;
+  const uint32_t s_bytes =
+      tile0 < tiles ? (uint32_t)((int64_t)(K / G) * N * 2 - (int64_t)tile0 * 32) : 0u;
   auto load = [&](Chunk& r, int chunk) {
+    // (one tile: past K is past the buffer; more: the scales are zero there)
+    const auto rw = make_rsrc(w0, chunk < last ? w_bytes : 0u);
+    const auto rs = make_rsrc(sw + tile0 * 16, chunk < last ? s_bytes : 0u);
+    const uint32_t w_off = chunk * (kChunk * 1024) + lane * 16;
+    uint32_t s_off = (uint32_t)chunk * (kChunk * kGroups) * (N * 2) + 8 * p;
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
-      const int kb = chunk * kChunk + i;
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
+      for (int t = 0; t < T; ++t)
         r.w[i][t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                  rw, (t * kbs + kb) * 1024 + lane * 16, 0,
+                                                  rw, w_off + t * (kbs * 1024) + i * 1024, 0,
                                                   kNonTemporal));
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g)
+      for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+        for (int t = 0; t < T; ++t)
           r.s[i][t][g] = __builtin_bit_cast(
-              u32x2, __builtin_amdgcn_raw_buffer_load_b64(
-                         rs, (kb * kGroups + g) * (N * 2) + t * 32 + 8 * p, 0, 0));
+              u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, s_off + t * 32, 0, 0));
+        s_off += N * 2;
       }
     }
   };
@@ -467,8 +473,8 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
     }
   };
 
-  // A chunk's loads: kMine of x, then the weights' and scales'.  Chunks past the slice
-  // are loaded too (the waits count on them) and not used.
+  // A chunk's loads: kMine of x, then the weights' and scales'.  Those of chunks past the
+  // slice are issued too (the waits count on them) but go nowhere.
   constexpr int kLoads = kMine + kChunk * T * (1 + kGroups);
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
@@ -566,7 +572,7 @@ Cut cut_of(int64_t M, int64_t N, int64_t K) {
   const int64_t units = (N / 16 + 7) / 8 * ((M + 63) / 64);
   const int64_t chunk = chunk_blocks(M <= 16 ? 1 : M <= 32 ? 2 : 4);
   const int64_t chunks = (K / 128 + chunk - 1) / chunk;
-  const int64_t target = 2 * device_cu_count();
+  const int64_t target = device_cu_count();
   cut.slices = (int)std::clamp<int64_t>(target / units, 1, std::min<int64_t>(chunks, 16));
   return cut;
 }
@@ -575,7 +581,7 @@ template <class E, int G, int T>
 hipError_t gemv_launch(const uint16_t* x, int64_t x_stride, const uint32_t* w4,
                        const uint16_t* sw, int64_t M, int64_t N, int64_t K, uint16_t* y,
                        hipStream_t stream) {
-  constexpr int W = 8, P = (G == 32 ? 4 : 6) / T;
+  constexpr int W = 8, P = T == 2 && G == 32 ? 3 : 4;
   const int64_t tiles = N / 16, items = (tiles + T - 1) / T;
   const int64_t most = device_cu_count() * (16 / W);  // 16 waves a compute unit
   return launch_kernel_lds(gemv_w4_kernel<E, G, T, W, P>, dim3((unsigned)std::min(items, most)),
@@ -604,7 +610,13 @@ template <class E, int G>
 hipError_t gemv_any(const uint16_t* x, int64_t x_stride, const uint32_t* w4, const uint16_t* sw,
                     int64_t M, int64_t N, int64_t K, float* part, uint16_t* y,
                     hipStream_t stream) {
-  if (few_rows(M, K)) return gemv_launch<E, G, 1>(x, x_stride, w4, sw, M, N, K, y, stream);
+  if (few_rows(M, K)) {
+    // two tiles an item halve the reads of x and the steps' overhead, one tile leaves the
+    // workgroups' shares more even
+    if (N / 16 >= 4 * 2 * device_cu_count())
+      return gemv_launch<E, G, 2>(x, x_stride, w4, sw, M, N, K, y, stream);
+    return gemv_launch<E, G, 1>(x, x_stride, w4, sw, M, N, K, y, stream);
+  }
   if (M <= 16) return gemm_launch<E, G, 1>(x, x_stride, w4, sw, M, N, K, part, y, stream);
   if (M <= 32) return gemm_launch<E, G, 2>(x, x_stride, w4, sw, M, N, K, part, y, stream);
   return gemm_launch<E, G, 4>(x, x_stride, w4, sw, M, N, K, part, y, stream);
