@@ -1,9 +1,11 @@
-"""Build libflexq.so (the gfx950 HIP kernels behind include/flexq.h) in-tree with hipcc."""
+"""Build libflexq.so (the gfx950 HIP kernels behind include/flexq.h) in-tree with hipcc,
+and _serve.so, the Python binding of the decoding-step calls, with the host compiler."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -32,9 +34,32 @@ FLAGS = [
 ]
 
 
+BINDING = os.path.join(PKG, "_serve.so")
+
+
+def binding_command(out: str) -> list[str]:
+    import torch
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    include = [*cpp_extension.include_paths("cuda"), sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            # what torch's own headers ask for on ROCm
+            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-isystem{p}" for p in include), os.path.join(CSRC, "serve_binding.cpp"),
+            f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
+            f"-Wl,-rpath,{lib}", "-o", out]
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs, procs = [], []
+    cmd = binding_command(BINDING + ".tmp")
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    procs.append(("serve_binding.cpp",
+                  subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
         cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -53,7 +78,8 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         if p.returncode:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"hipcc failed for {failed}")
+        raise RuntimeError(f"the compiler failed for {failed}")
+    os.replace(BINDING + ".tmp", BINDING)
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:

@@ -575,7 +575,10 @@ template <class E, int DT>
 hipError_t launch_rows(const AttentionArgs& a, hipStream_t stream) {
   // stages: what two workgroups' share of a compute unit's LDS holds
   constexpr int S = DT <= 4 ? 4 : 2;
-  const Layout p = layout_of(a.max_new, a.H, a.Hkv, a.D);
+  Layout p = layout_of(a.max_new, a.H, a.Hkv, a.D);
+  // no more shares than the tables' room can fill (short contexts: one, and no join)
+  const int64_t room = kHead + (((int64_t)a.max_blocks << a.page_shift) + 31) / 32;
+  p.shares = (int)std::min<int64_t>(p.shares, std::max<int64_t>(1, a.B * room / kMinShare));
   const int64_t units = (int64_t)p.shares * a.Hkv;
   const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.row_blocks));
   auto* kernel = tree_attention_kernel<E, DT, 1, S>;

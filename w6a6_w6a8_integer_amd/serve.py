@@ -1,7 +1,8 @@
 """The operators a decoding step runs around the quantized layers (C ABI in
 ``include/flexq_serve.h``), bound the same way as the layers themselves: arguments are
-checked here, outputs and workspaces allocated when the caller brings none, and the
-work runs in the HIP kernels on the current stream of the tensors' GPU.
+checked, outputs and workspaces allocated when the caller brings none, and the
+work runs in the HIP kernels on the current stream of the tensors' GPU.  For the calls
+that run once a layer and step the checks are in ``_serve.so`` (csrc/serve_binding.cpp).
 
 * :func:`pack_w4`, :func:`gemv_w4`, :class:`W4Linear`  4-bit group-scaled weights and
   their product with a few activation rows (fp16 or bf16)
@@ -13,7 +14,8 @@ work runs in the HIP kernels on the current stream of the tensors' GPU.
 from __future__ import annotations
 
 import ctypes
-import math
+import importlib.util
+import os
 
 import torch
 
@@ -52,21 +54,27 @@ def _dtype(t, name: str) -> int:
     return code
 
 
-def _rows(t, dtype, name: str, dims: int):
-    """A tensor whose last dimension is contiguous; the others may be strided."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must be {dims}-D, got shape {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    return t
+_calls = None
 
 
-def _int32(t, name: str, shape):
-    return _fq._tensor(t, torch.int32, name, shape=shape)
+def _native():
+    """The functions of _serve.so, bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        lib = _fq.lib()
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_serve.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built: run __graft_entry__.build() "
+                               "(there is no fallback)")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._serve", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, f"flexq_{name}"), ctypes.c_void_p).value
+                      for name in ("gemv_w4", "gemv_w4_workspace_bytes", "block_tables",
+                                   "kv_cache_write", "tree_attention",
+                                   "tree_attention_workspace_bytes")))
+        _calls = module
+    return _calls
 
 
 def _call(name: str, dev, *args):
@@ -80,12 +88,6 @@ def _call(name: str, dev, *args):
             status = fn(*args, stream)
     if status != 0:
         raise _fq.FlexqError(status, name)
-
-
-def _workspace(t, need: int):
-    if isinstance(t, torch.Tensor) and t.dim() != 1:
-        raise ValueError(f"workspace must be 1-D, got shape {tuple(t.shape)}")
-    return _fq._tensor(t, torch.uint8, "workspace", min_bytes=need)
 
 
 def _group(group: int) -> int:
@@ -130,33 +132,7 @@ def gemv_w4(x: torch.Tensor, w4: torch.Tensor, s_w: torch.Tensor, N: int,
     """Y[M][N] = X[M][K] times the 4-bit weights (flexq_gemv_w4), X and Y fp16 or bf16,
     X's rows contiguous (they may be strided); the group size is K / len(s_w).  Meant for
     few rows: the weights are read once per 64 of them."""
-    code = _dtype(x, "x")
-    _rows(x, x.dtype, "x", 2)
-    M, K = x.shape
-    _fq._groups(K, "gemv_w4")
-    N = _fq._cols(N)
-    if not isinstance(s_w, torch.Tensor) or s_w.dim() != 2:
-        raise ValueError("s_w must be a 2-D tensor [K/group][N]")
-    G = s_w.shape[0]
-    if G <= 0 or K % G:
-        raise ValueError(f"s_w must have K / group rows for K = {K}, got {G}")
-    _group(K // G)
-    _fq._tensor(s_w, torch.float16, "s_w", shape=(G, N))
-    _packed4(w4, N, K)
-    if y is None:
-        y = torch.empty((M, N), dtype=x.dtype, device=x.device)
-    _fq._tensor(y, x.dtype, "y", shape=(M, N))
-    need = gemv_w4_workspace_bytes(M, N, K)
-    tensors = dict(x=x, w4=w4, s_w=s_w, y=y)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    if workspace is not None:
-        tensors["workspace"] = _workspace(workspace, need)
-    dev = _fq._on_gpu(**tensors)
-    _call("flexq_gemv_w4", dev, x.data_ptr(), code, x.stride(0), w4.data_ptr(), s_w.data_ptr(), M,
-          N, K, K // G, workspace.data_ptr() if workspace is not None else None,
-          workspace.numel() if workspace is not None else 0, y.data_ptr())
-    return y
+    return (_calls or _native()).gemv_w4(x, w4, s_w, N, y, workspace)
 
 
 class W4Linear:
@@ -180,39 +156,9 @@ def block_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: tor
     entered into block_table[B][max_blocks] in place.  Returns (slot_map[max_tokens],
     cu_new[B + 1], counts[3]); counts = new tokens, pages taken, next free head.  Slots
     past the new tokens, and of tokens no page was left for, are -1."""
-    if isinstance(block_table, torch.Tensor) and block_table.dim() != 2:
-        raise ValueError(f"block_table must be 2-D, got shape {tuple(block_table.shape)}")
-    _fq._tensor(block_table, torch.int32, "block_table")
-    B, max_blocks = block_table.shape
-    dev = block_table.device
-    _int32(ctx_lens, "ctx_lens", (B,))
-    _int32(new_lens, "new_lens", (B,))
-    if isinstance(free_pages, torch.Tensor) and free_pages.dim() != 1:
-        raise ValueError(f"free_pages must be 1-D, got shape {tuple(free_pages.shape)}")
-    _fq._tensor(free_pages, torch.int32, "free_pages")
-    max_tokens = int(max_tokens)
-    if max_tokens < 0:
-        raise ValueError(f"max_tokens = {max_tokens} must not be negative")
-    if slot_map is None:
-        slot_map = torch.empty(max_tokens, dtype=torch.int32, device=dev)
-    if cu_new is None:
-        cu_new = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    if counts is None:
-        counts = torch.empty(3, dtype=torch.int32, device=dev)
-    _int32(slot_map, "slot_map", (max_tokens,))
-    _int32(cu_new, "cu_new", (B + 1,))
-    _int32(counts, "counts", (3,))
-    tensors = dict(block_table=block_table, ctx_lens=ctx_lens, new_lens=new_lens,
-                   free_pages=free_pages, slot_map=slot_map, cu_new=cu_new, counts=counts)
-    if free_head is not None:
-        tensors["free_head"] = _int32(free_head, "free_head", (1,))
-    dev = _fq._on_gpu(**tensors)
-    _call("flexq_block_tables", dev, ctx_lens.data_ptr(), new_lens.data_ptr(), B,
-          free_pages.data_ptr(), free_pages.numel(),
-          free_head.data_ptr() if free_head is not None else None, page_size,
-          block_table.data_ptr(), max_blocks, max_tokens, slot_map.data_ptr(), cu_new.data_ptr(),
-          counts.data_ptr())
-    return slot_map, cu_new, counts
+    return (_calls or _native()).block_tables(ctx_lens, new_lens, free_pages, block_table,
+                                              page_size, max_tokens, free_head, slot_map, cu_new,
+                                              counts)
 
 
 def kv_cache(num_pages: int, Hkv: int, D: int, page_size: int, dtype=torch.float16,
@@ -226,39 +172,12 @@ def kv_cache(num_pages: int, Hkv: int, D: int, page_size: int, dtype=torch.float
     return k, v
 
 
-def _cache(k_cache, v_cache, dtype):
-    """(pages, Hkv, D, page_size) of a paged cache."""
-    if not isinstance(v_cache, torch.Tensor) or v_cache.dim() != 5:
-        raise ValueError("v_cache must be a 5-D tensor [pages][Hkv][page_size/16][D][16]")
-    pages, Hkv, blocks, D, last = v_cache.shape
-    if last != 16 or D not in HEAD_WIDTHS or 16 * blocks not in PAGE_SIZES:
-        raise ValueError(f"v_cache must be [pages][Hkv][page_size/16][D][16] with page_size one "
-                         f"of {PAGE_SIZES} and D one of {HEAD_WIDTHS}, got "
-                         f"{tuple(v_cache.shape)}")
-    _fq._tensor(v_cache, dtype, "v_cache")
-    _fq._tensor(k_cache, dtype, "k_cache", shape=(pages, Hkv, blocks, D // 32, 16, 32))
-    return pages, Hkv, D, 16 * blocks
-
-
 def kv_cache_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
                    k_cache: torch.Tensor, v_cache: torch.Tensor):
     """Keys and values k, v [T][Hkv][D] into the paged cache at the slots
     slot_map int32[T] (flexq_kv_cache_write); negative slots drop their token.  k and v may
     be strided over tokens and heads, as slices of a fused projection's output are."""
-    _dtype(k, "k")
-    _rows(k, k.dtype, "k", 3)
-    pages, Hkv, D, page = _cache(k_cache, v_cache, k.dtype)
-    T = k.shape[0]
-    if tuple(k.shape) != (T, Hkv, D):
-        raise ValueError(f"k must have shape {(T, Hkv, D)}, got {tuple(k.shape)}")
-    _rows(v, k.dtype, "v", 3)
-    if v.shape != k.shape:
-        raise ValueError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
-    _int32(slot_map, "slot_map", (T,))
-    dev = _fq._on_gpu(k=k, v=v, slot_map=slot_map, k_cache=k_cache, v_cache=v_cache)
-    _call("flexq_kv_cache_write", dev, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-          v.stride(0), v.stride(1), slot_map.data_ptr(), T, Hkv, D, pages, page,
-          k_cache.data_ptr(), v_cache.data_ptr())
+    (_calls or _native()).kv_cache_write(k, v, slot_map, k_cache, v_cache)
 
 
 def tree_attention_workspace_bytes(B: int, max_new: int, H: int, Hkv: int, D: int) -> int:
@@ -280,46 +199,6 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     None is a chain (j up to the token itself).  max_new bounds the new tokens of one
     request (default: T).  Returns out [T][H][D], or (out, lse fp32[T][H]) where lse is
     asked for."""
-    code = _dtype(q, "q")
-    _rows(q, q.dtype, "q", 3)
-    T, H, D = q.shape
-    pages, Hkv, Dc, page = _cache(k_cache, v_cache, q.dtype)
-    if Dc != D or Hkv <= 0 or H % Hkv:
-        raise ValueError(f"q [{T}][{H}][{D}] does not fit a cache of {Hkv} heads of {Dc}")
-    if isinstance(block_table, torch.Tensor) and block_table.dim() != 2:
-        raise ValueError(f"block_table must be 2-D, got shape {tuple(block_table.shape)}")
-    _fq._tensor(block_table, torch.int32, "block_table")
-    B, max_blocks = block_table.shape
-    _int32(ctx_lens, "ctx_lens", (B,))
-    _int32(cu_new, "cu_new", (B + 1,))
-    max_new = T if max_new is None else int(max_new)
-    tensors = dict(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                   ctx_lens=ctx_lens, cu_new=cu_new)
-    words = 0
-    if tree_mask is not None:
-        if isinstance(tree_mask, torch.Tensor) and tree_mask.dim() != 2:
-            raise ValueError(f"tree_mask must be 2-D, got shape {tuple(tree_mask.shape)}")
-        words = tree_mask.shape[1] if isinstance(tree_mask, torch.Tensor) else 0
-        tensors["tree_mask"] = _int32(tree_mask, "tree_mask", (T, words))
-        if max_new > 32 * words:
-            raise ValueError(f"tree_mask has {32 * words} bits a token; max_new = {max_new}")
-    dev = q.device
-    if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=dev)
-    tensors["out"] = _fq._tensor(out, q.dtype, "out", shape=(T, H, D))
-    if lse is None and return_lse:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    if lse is not None:
-        tensors["lse"] = _fq._tensor(lse, torch.float32, "lse", shape=(T, H))
-    need = tree_attention_workspace_bytes(B, max_new, H, Hkv, D)
-    if workspace is None:
-        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=dev)
-    tensors["workspace"] = _workspace(workspace, need)
-    dev = _fq._on_gpu(**tensors)
-    _call("flexq_tree_attention", dev, q.data_ptr(), code, q.stride(0), q.stride(1),
-          k_cache.data_ptr(), v_cache.data_ptr(), pages, page, block_table.data_ptr(), max_blocks,
-          ctx_lens.data_ptr(), cu_new.data_ptr(), B, T, max_new, H, Hkv, D,
-          tree_mask.data_ptr() if tree_mask is not None else None, words,
-          1.0 / math.sqrt(D) if scale is None else float(scale), workspace.data_ptr(),
-          workspace.numel(), out.data_ptr(), lse.data_ptr() if lse is not None else None)
-    return out if lse is None else (out, lse)
+    return (_calls or _native()).tree_attention(q, k_cache, v_cache, block_table, ctx_lens,
+                                                cu_new, tree_mask, scale, max_new, out, lse,
+                                                return_lse, workspace)
