@@ -124,8 +124,8 @@ flexq_status flexq_block_tables(const int32_t* ctx_lens, const int32_t* new_lens
                elements, the tensors' own), 16-byte aligned rows
      slot_map  int32[T]      k_cache, v_cache  the layouts above, 16-byte aligned
    T == 0 is a no-op.  Errors: INVALID_VALUE (null, negative size, negative stride, a
-   cache overlapping another argument), UNSUPPORTED (D, page_size, strides % 8, T * Hkv *
-   D >= 2^34, num_pages * Hkv * page_size / 16 >= 2^31, alignment). */
+   cache overlapping another argument), UNSUPPORTED (D, page_size, strides % 8, Hkv >
+   65535, T * Hkv * D >= 2^34, num_pages * Hkv * page_size / 16 >= 2^31, alignment). */
 flexq_status flexq_kv_cache_write(const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h,
                                   const uint16_t* v, int64_t v_stride_t, int64_t v_stride_h,
                                   const int32_t* slot_map, int64_t T, int64_t Hkv, int64_t D,

@@ -176,7 +176,8 @@ flexq_status flexq_kv_cache_write(const uint16_t* k, int64_t k_stride_t, int64_t
   if (T < 0 || k_stride_t < 0 || k_stride_h < 0 || v_stride_t < 0 || v_stride_h < 0)
     return FLEXQ_ERROR_INVALID_VALUE;
   FLEXQ_TRY(check_cache(num_pages, Hkv, D, page_size));
-  if (T >= (1LL << 34) / D / Hkv + 1 || T * Hkv * D >= (1LL << 34)) return FLEXQ_ERROR_UNSUPPORTED;
+  if (Hkv > 65535 || T >= (1LL << 34) / D / Hkv + 1 || T * Hkv * D >= (1LL << 34))
+    return FLEXQ_ERROR_UNSUPPORTED;
   if (T == 0) return FLEXQ_SUCCESS;
   if (!k || !v || !slot_map || (num_pages > 0 && (!k_cache || !v_cache)))
     return FLEXQ_ERROR_INVALID_VALUE;

@@ -58,6 +58,7 @@ __device__ __forceinline__ int find(const int* start, int n, int v) {
 // L2), then takes its share of the new pages and of the slot map; a slot
 // on a new page reads the free list, not the table another workgroup may be writing, so
 // one launch does.
+template <int PER>
 __global__ __launch_bounds__(kScanThreads) void block_tables_kernel(
     const int* __restrict__ ctx_lens, const int* __restrict__ new_lens, int B,
     const int* __restrict__ free_pages, int num_free, const int* __restrict__ free_head, int shift,
@@ -93,6 +94,7 @@ __global__ __launch_bounds__(kScanThreads) void block_tables_kernel(
   }
   __syncthreads();
 
+  const bool wide = (reinterpret_cast<uintptr_t>(slots) & 15) == 0;
   const int stride = gridDim.x * kScanThreads, first = blockIdx.x * kScanThreads + threadIdx.x;
   for (int b = first; b <= B; b += stride) cu_new[b] = cu[b];
   if (first == 0) {
@@ -108,51 +110,142 @@ __global__ __launch_bounds__(kScanThreads) void block_tables_kernel(
     if (col >= 0 && col < max_blocks)
       table[(int64_t)b * max_blocks + col] = f >= 0 && f < num_free ? free_pages[f] : -1;
   }
-  for (int64_t t = first; t < max_tokens; t += stride) {
-    int slot = -1;
-    if (t < base.x) {
-      const int b = find(cu, B, (int)t);
-      const int64_t c = max(0, ctx_lens[b]);
-      const int64_t pos = c + (t - cu[b]);
-      const int64_t have = (c + page - 1) >> shift;
-      const int64_t col = pos >> shift;
-      int id = -1;
-      if (col >= 0 && col < max_blocks) {
-        const int64_t f = (int64_t)head + off[b] + (col - have);
-        if (col < have)
-          id = table[(int64_t)b * max_blocks + col];
-        else if (f >= 0 && f < num_free)
-          id = free_pages[f];
+  // PER slots a thread: one search, then on from token to token.
+  for (int64_t t0 = PER * (int64_t)first; t0 < max_tokens; t0 += PER * (int64_t)stride) {
+    int slot[PER];
+    int b = 0, next = 0, id = -1;  // request, its last token + 1, page of column `col`
+    int64_t c = 0, col = -1;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int64_t t = t0 + j;
+      slot[j] = -1;
+      if (t >= base.x) continue;
+      if (j == 0 || t >= next) {
+        b = j == 0 ? find(cu, B, (int)t) : b + 1;
+        while (t >= cu[b + 1]) ++b;  // (requests without new tokens)
+        next = cu[b + 1];
+        c = max(0, ctx_lens[b]);
+        col = -1;
       }
-      if (id >= 0) slot = (int)(((int64_t)id << shift) + (pos & (page - 1)));
+      const int64_t pos = c + (t - cu[b]), now = pos >> shift;
+      if (now != col) {
+        col = now;
+        const int64_t have = (c + page - 1) >> shift, f = (int64_t)head + off[b] + (col - have);
+        id = -1;
+        if (col < max_blocks) {
+          if (col < have)
+            id = table[(int64_t)b * max_blocks + col];
+          else if (f >= 0 && f < num_free)
+            id = free_pages[f];
+        }
+      }
+      if (id >= 0) slot[j] = (int)(((int64_t)id << shift) + (pos & (page - 1)));
     }
-    slots[t] = slot;
+    if constexpr (PER % 4 == 0) {
+      if (t0 + PER <= max_tokens && wide) {
+#pragma unroll
+        for (int j = 0; j < PER; j += 4)
+          *reinterpret_cast<int4*>(slots + t0 + j) =
+              make_int4(slot[j], slot[j + 1], slot[j + 2], slot[j + 3]);
+        continue;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (t0 + j < max_tokens) slots[t0 + j] = slot[j];
   }
 }
 
-// One thread = 8 consecutive elements of one head of one token: a 16-byte piece of the
-// keys' row, or 8 elements of the values that go to 8 places 32 bytes apart.
+// New keys and values into the cache, a copy bound by HBM (read and written once).
+//
+// In the cache the keys of a token are 64-byte pieces and the values have the token
+// innermost, eight tokens of one d in 16 bytes (half a 16-token block).  So tokens whose
+// slots run on through the same half block form a group: its values go through LDS and
+// come out as columns, a whole group (eight tokens) in 16-byte stores, a shorter one (the
+// ends of a prompt, single tokens, scattered slots) element by element.  A workgroup owns
+// the groups that begin among its kTokens tokens, for one head; the last may reach seven
+// tokens further.
+template <int D, int kTokens>
 __global__ __launch_bounds__(256) void kv_cache_write_kernel(
     const uint16_t* __restrict__ k, int64_t k_st, int64_t k_sh, const uint16_t* __restrict__ v,
-    int64_t v_st, int64_t v_sh, const int* __restrict__ slots, int64_t items, int Hkv, int D,
-    int64_t num_slots, int shift, uint16_t* __restrict__ kc, uint16_t* __restrict__ vc) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= items) return;
-  const int per_row = D / 8;
-  const int d = (int)(i % per_row) * 8;
-  const int64_t th = i / per_row;
-  const int h = (int)(th % Hkv);
-  const int64_t t = th / Hkv;
-  const int64_t slot = slots[t];
-  if (slot < 0 || slot >= num_slots) return;
-  const int64_t r = slot & ((1 << shift) - 1);
-  const int64_t block = ((slot >> shift) * Hkv + h) * (1 << (shift - 4)) + (r >> 4);
-  const u32x4 ke = *reinterpret_cast<const u32x4*>(k + t * k_st + h * k_sh + d);
-  *reinterpret_cast<u32x4*>(kc + block * 16 * D + (d >> 5) * 512 + (r & 15) * 32 + (d & 31)) = ke;
-  const u32x4 ve = *reinterpret_cast<const u32x4*>(v + t * v_st + h * v_sh + d);
-  uint16_t* dst = vc + block * 16 * D + d * 16 + (r & 15);
+    int64_t v_st, int64_t v_sh, const int* __restrict__ slots, int T, int Hkv, int64_t num_slots,
+    int shift, uint16_t* __restrict__ kc, uint16_t* __restrict__ vc) {
+  constexpr int kPieces = D / 8;       // 16-byte pieces of a row
+  constexpr int kPitch = D + 8;        // of a token's row in LDS, elements
+  constexpr int kMost = kTokens + 7;
+  __shared__ __attribute__((aligned(16))) uint16_t tile[kMost * kPitch];
+  __shared__ int slot_of[kMost + 1];   // of token t0 - 1 + i, -1 where it is dropped
+  __shared__ int begin[kTokens], length[kTokens];  // of the groups, begin from t0
+  __shared__ int groups, first, end;       // and the tokens they hold, from t0
+  const int h = blockIdx.y, t0 = blockIdx.x * kTokens, tid = threadIdx.x;
+  if (tid <= kMost) {
+    const int t = t0 - 1 + tid;
+    const int64_t slot = t >= 0 && t < T ? slots[t] : -1;
+    slot_of[tid] = slot >= 0 && slot < num_slots ? (int)slot : -1;
+  }
+  __syncthreads();
+  if (tid < kTokens) {  // one wave
+    const int* s = slot_of + 1 + tid;
+    const bool kept = s[0] >= 0;
+    const bool leads = kept && ((s[0] & 7) == 0 || s[-1] != s[0] - 1);
+    int n = 1;
+    while (leads && (s[0] + n & 7) != 0 && s[n] == s[0] + n) ++n;
+    const uint64_t mask = __ballot(leads);
+    if (leads) {
+      const int at = __builtin_popcountll(mask & ((1ull << tid) - 1));
+      begin[at] = tid;
+      length[at] = n;
+      if ((mask >> tid) >> 1 == 0) end = tid + n;
+    }
+    if (tid == 0) {
+      groups = __builtin_popcountll(mask);
+      first = mask ? __builtin_ctzll(mask) : 0;
+      if (!mask) end = 0;
+    }
+  }
+  __syncthreads();
+  const int at0 = first, n = end - first;
+  // every load of the workgroup before its first store
+  constexpr int kTurns = (kMost * kPieces + 255) / 256;
+  u32x4 ke[kTurns], ve[kTurns];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dst[e * 16] = (uint16_t)(ve[e >> 1] >> (16 * (e & 1)));
+  for (int u = 0; u < kTurns; ++u) {
+    const int i = tid + u * 256, t = i / kPieces, d = i % kPieces * 8;
+    if (i >= n * kPieces) break;
+    const int64_t from = t0 + at0 + t;
+    ke[u] = *reinterpret_cast<const u32x4*>(k + from * k_st + h * k_sh + d);
+    ve[u] = *reinterpret_cast<const u32x4*>(v + from * v_st + h * v_sh + d);
+  }
+#pragma unroll
+  for (int u = 0; u < kTurns; ++u) {
+    const int i = tid + u * 256, t = i / kPieces, d = i % kPieces * 8;
+    if (i >= n * kPieces) break;
+    const int slot = slot_of[1 + at0 + t];
+    if (slot < 0) continue;  // dropped
+    *reinterpret_cast<u32x4*>(tile + t * kPitch + d) = ve[u];
+    const int r = slot & ((1 << shift) - 1);
+    const int64_t block = ((int64_t)(slot >> shift) * Hkv + h) * (1 << (shift - 4)) + (r >> 4);
+    *reinterpret_cast<u32x4*>(kc + block * (16 * D) + (d >> 5) * 512 + (r & 15) * 32 + (d & 31)) =
+        ke[u];
+  }
+  __syncthreads();
+  for (int i = tid; i < groups * D; i += 256) {
+    const int g = i / D, d = i % D;
+    const int len = length[g], slot = slot_of[1 + begin[g]];
+    const uint16_t* from = tile + (begin[g] - at0) * kPitch + d;
+    const int r = slot & ((1 << shift) - 1);
+    const int64_t block = ((int64_t)(slot >> shift) * Hkv + h) * (1 << (shift - 4)) + (r >> 4);
+    uint16_t* to = vc + block * (16 * D) + d * 16 + (r & 15);
+    if (len == 8) {
+      u32x4 out;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        out[j] = from[2 * j * kPitch] | (uint32_t)from[(2 * j + 1) * kPitch] << 16;
+      *reinterpret_cast<u32x4*>(to) = out;
+    } else {
+      for (int j = 0; j < len; ++j) to[j] = from[j * kPitch];
+    }
+  }
 }
 
 hipError_t launch_block_tables(const int32_t* ctx, const int32_t* add, int64_t B,
@@ -160,10 +253,14 @@ hipError_t launch_block_tables(const int32_t* ctx, const int32_t* add, int64_t B
                                int page_size, int32_t* table, int64_t max_blocks,
                                int64_t max_tokens, int32_t* slots, int32_t* cu, int32_t* counts,
                                hipStream_t stream) {
-  const int64_t work = std::max<int64_t>(max_tokens, B);
-  const int64_t grid = std::min<int64_t>(work / kScanThreads + 1, 4 * device_cu_count());
+  // One slot a thread while those threads fit the GPU twice over; then eight, which share
+  // the search and most page lookups.
+  const int64_t most = 4 * device_cu_count();
+  const int per = max_tokens <= most * kScanThreads / 4 ? 1 : 8;
+  const int64_t work = std::max<int64_t>((max_tokens + per - 1) / per, B);
+  const int64_t grid = std::min<int64_t>(work / kScanThreads + 1, most);
   const size_t lds = (size_t)(B + 1) * 2 * sizeof(int);
-  return launch_kernel_lds(block_tables_kernel, dim3((unsigned)grid), dim3(kScanThreads), lds,
+  return launch_kernel_lds(per == 1 ? block_tables_kernel<1> : block_tables_kernel<8>, dim3((unsigned)grid), dim3(kScanThreads), lds,
                            stream, ctx, add, (int)B, free_pages, (int)num_free, head,
                            __builtin_ctz((unsigned)page_size), table, (int)max_blocks,
                            (int)max_tokens, slots, cu, counts);
@@ -174,10 +271,20 @@ hipError_t launch_kv_cache_write(const uint16_t* k, int64_t k_st, int64_t k_sh,
                                  const int32_t* slots, int64_t T, int64_t Hkv, int64_t D,
                                  int64_t num_pages, int page_size, uint16_t* kc, uint16_t* vc,
                                  hipStream_t stream) {
-  const int64_t items = T * Hkv * (D / 8);
-  return launch_kernel(kv_cache_write_kernel, dim3((unsigned)((items + 255) / 256)), dim3(256),
-                       stream, k, k_st, k_sh, v, v_st, v_sh, slots, items, (int)Hkv, (int)D,
-                       num_pages * page_size, __builtin_ctz((unsigned)page_size), kc, vc);
+  // sixteen tokens a workgroup where that is what it takes to have two for a compute unit
+  const int tokens = (T + 63) / 64 * Hkv >= 2 * device_cu_count() ? 64 : 16;
+  const dim3 grid((unsigned)((T + tokens - 1) / tokens), (unsigned)Hkv);
+  auto* kernel = tokens == 64 ? (D == 64    ? kv_cache_write_kernel<64, 64>
+                                 : D == 96  ? kv_cache_write_kernel<96, 64>
+                                 : D == 128 ? kv_cache_write_kernel<128, 64>
+                                            : kv_cache_write_kernel<256, 64>)
+                              : (D == 64    ? kv_cache_write_kernel<64, 16>
+                                 : D == 96  ? kv_cache_write_kernel<96, 16>
+                                 : D == 128 ? kv_cache_write_kernel<128, 16>
+                                            : kv_cache_write_kernel<256, 16>);
+  return launch_kernel(kernel, grid, dim3(256), stream, k, k_st, k_sh, v, v_st, v_sh, slots,
+                       (int)T, (int)Hkv, num_pages * page_size,
+                       __builtin_ctz((unsigned)page_size), kc, vc);
 }
 
 }  // namespace flexq
