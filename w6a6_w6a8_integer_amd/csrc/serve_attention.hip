@@ -31,6 +31,8 @@ constexpr uint32_t kHead = 2, kMinShare = 8;
 // Probabilities are at most 2^kLag before the division (fp16 holds 2^15).
 constexpr float kLag = 8.0f;
 
+constexpr int kNonTemporal = 2;  // cache-policy bit of loads
+
 typedef __attribute__((address_space(1))) const void* global_ptr_t;
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef __attribute__((address_space(4))) const int32_t* scalar_ptr_t;
@@ -220,8 +222,10 @@ __device__ __forceinline__ void write_row(const AttentionArgs& a, int64_t t, int
 // from memory) and every wave reads all of them for its own rows.  S stages: the loads
 // of S - 1 steps are on their way while one is worked on, and one barrier a step tells
 // that a step has come and that the one before has been read.
-template <class E, int DT, int NT, int S>
-__global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const AttentionArgs a,
+//
+// ONE: there is one row block, nobody reads the cache's lines again, and they are not kept.
+template <class E, int DT, int NT, int S, bool ONE>
+__global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const AttentionArgs a,
                                                                      int shares, int row_blocks) {
   constexpr int D = 32 * DT;
   constexpr int OT = 2 * DT;                 // 16-wide slices of D
@@ -330,7 +334,7 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
 #pragma unroll
       for (int i = 0; i < DT; ++i)
         __builtin_amdgcn_global_load_lds((global_ptr_t)(from + i * (key_wave ? 512 : 256)),
-                                         (lds_ptr_t)(to + i * 1024), 16, 0, 0);
+                                         (lds_ptr_t)(to + i * 1024), 16, 0, ONE ? kNonTemporal : 0);
       id0 = page_of(step + 1, 0);
       id1 = page_of(step + 1, 1);
     };
@@ -429,24 +433,32 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
         poison = __ballot(bad) != 0;
       }
 
-      u32x4 hi[NT], lo[NT];
+      float top[NT];
+      bool raise = false;  // rare after a request's first step
 #pragma unroll
       for (int rt = 0; rt < NT; ++rt) {
-        float top = s[rt][0][0];
+        top[rt] = s[rt][0][0];
 #pragma unroll
-        for (int e = 1; e < 8; ++e) top = fmaxf(top, s[rt][e >> 2][e & 3]);
-        top = row_max(top);
-        if (__ballot(top > m[rt] + lag)) {  // rare after a request's first step
-          top = fmaxf(m[rt], top);
-          const float by =
-              __builtin_amdgcn_exp2f((m[rt] - (top == -INFINITY ? 0.0f : top)) * scale);
-          m[rt] = top;
+        for (int e = 1; e < 8; ++e) top[rt] = fmaxf(top[rt], s[rt][e >> 2][e & 3]);
+        top[rt] = row_max(top[rt]);
+        raise |= top[rt] > m[rt] + lag;
+      }
+      if (__ballot(raise)) {
+#pragma unroll
+        for (int rt = 0; rt < NT; ++rt) {
+          const float to = fmaxf(m[rt], top[rt]);
+          const float by = __builtin_amdgcn_exp2f((m[rt] - (to == -INFINITY ? 0.0f : to)) * scale);
+          m[rt] = to;
           l[rt] *= by;
 #pragma unroll
           for (int dt = 0; dt < OT; ++dt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[rt][dt][i] *= by;
         }
+      }
+      u32x4 hi[NT], lo[NT];
+#pragma unroll
+      for (int rt = 0; rt < NT; ++rt) {
         const float ref = m[rt] == -INFINITY ? 0.0f : -m[rt] * scale;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -457,15 +469,11 @@ __global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(const Atten
           hi[rt][i] = both[0];
           lo[rt][i] = both[1];
         }
+#pragma unroll
+        for (int dt = 0; dt < OT; ++dt) o[rt][dt] = E::mfma(f[dt], hi[rt], o[rt][dt]);
+#pragma unroll
+        for (int dt = 0; dt < OT; ++dt) o[rt][dt] = E::mfma(f[dt], lo[rt], o[rt][dt]);
       }
-
-#pragma unroll
-      for (int dt = 0; dt < OT; ++dt)
-#pragma unroll
-        for (int rt = 0; rt < NT; ++rt) {
-          o[rt][dt] = E::mfma(f[dt], hi[rt], o[rt][dt]);
-          o[rt][dt] = E::mfma(f[dt], lo[rt], o[rt][dt]);
-        }
       if (!poison) continue;
       // Infinite and NaN values reach only the rows that attend their keys: one key at a
       // time, and a row that does not attend it keeps its sum.
@@ -581,9 +589,13 @@ hipError_t launch_rows(const AttentionArgs& a, hipStream_t stream) {
   p.shares = (int)std::min<int64_t>(p.shares, std::max<int64_t>(1, a.B * room / kMinShare));
   const int64_t units = (int64_t)p.shares * a.Hkv;
   const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.row_blocks));
-  auto* kernel = tree_attention_kernel<E, DT, 1, S>;
+  const bool one = p.row_blocks == 1;
+  auto* kernel = one ? tree_attention_kernel<E, DT, 1, S, true>
+                     : tree_attention_kernel<E, DT, 1, S, false>;
   if constexpr (DT <= 4)
-    if (p.nt == 2) kernel = tree_attention_kernel<E, DT, 2, S>;
+    if (p.nt == 2)
+      kernel = one ? tree_attention_kernel<E, DT, 2, S, true>
+                   : tree_attention_kernel<E, DT, 2, S, false>;
   const hipError_t e = launch_kernel_lds(kernel, grid, dim3(64 * kWaves), S * 4 * DT * 1024,
                                          stream, a, p.shares, p.row_blocks);
   if (e != hipSuccess || p.shares == 1) return e;
