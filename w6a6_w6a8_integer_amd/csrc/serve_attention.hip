@@ -4,13 +4,16 @@
 // K and V of up to ctx + new tokens: S = scale K Q^T, P = 2^(S log2 e - m) with a running
 // maximum m per row, O = V^T P, l = sum P; out = O / l.  One pass over the cache.
 //
-// Both products are 16x16x32 MFMAs with the rows as columns, so a lane owns one row's
-// statistics: D of K Q^T gives lane l the scores of row l % 16 at four keys, and the
-// fragment of P that V^T P takes wants eight consecutive keys of that row.  The keys of
-// a 32-key step are dealt to the two score tiles so that they are the same eight: row r
-// of score tile t holds key 8 (r / 4) + 4 t + r % 4, so lane l ends up with keys
-// 8 (l / 16) .. + 7 and no exchange between lanes is needed.  K and V fragments lie in
-// the cache in the order the MFMAs take them.
+// Both products are MFMAs with the rows as columns, so a lane owns one row's statistics: a
+// wave holds 16 rows (16x16x32) or, where there are many, 32 (32x32x16: half the
+// instructions for the same rows).  D of K Q^T gives a lane the scores of its row at some
+// keys, and the fragment of P that V^T P takes wants eight consecutive keys of that row.
+// The keys of a 32-key step are dealt to the score tiles' rows so that they are the same
+// eight, and no exchange between lanes is needed:
+//   16 rows: row r of score tile t holds key 8 (r / 4) + 4 t + r % 4; lane l ends up with
+//            keys 8 (l / 16) .. + 7;
+//   32 rows: row r holds the key with bits 2 and 3 of r swapped; lane l ends up with keys
+//            16 j + 8 (l / 32) .. + 7, j = 0, 1.
 #include <algorithm>
 
 #include "kernels.h"
@@ -37,20 +40,23 @@ typedef __attribute__((address_space(1))) const void* global_ptr_t;
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef __attribute__((address_space(4))) const int32_t* scalar_ptr_t;
 
-// (max, sum) over the four lanes that hold one row (l, l ^ 16, l ^ 32, l ^ 48).  A swap of
-// x with itself gives both halves of the exchange, each in every lane.
+// (max, sum) over the lanes that hold one of RW rows (l ^ 32, and of 16 rows l ^ 16 too).  A
+// swap of x with itself gives both halves of the exchange, each in every lane.
+template <int RW>
 __device__ __forceinline__ float row_max(float x) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x);
   const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(u, u, false, false));
   const uint32_t a0 = a[0], a1 = a[1];
   const float y = fmaxf(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
+  if constexpr (RW == 32) return y;
   const uint32_t v = __builtin_bit_cast(uint32_t, y);
   const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
   const uint32_t b0 = b[0], b1 = b[1];
   return fmaxf(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
 }
+template <int RW>
 __device__ __forceinline__ float row_sum(float x) {
-  x += __shfl_xor(x, 16);
+  if constexpr (RW == 16) x += __shfl_xor(x, 16);
   return x + __shfl_xor(x, 32);
 }
 
@@ -216,7 +222,105 @@ __device__ __forceinline__ void write_row(const AttentionArgs& a, int64_t t, int
     a.lse[t * a.H + h] = total != 0.0f ? (ref + log2f(total)) * kLn2 : -INFINITY;
 }
 
-// One workgroup = one share of the cache, key head and block of 64 NT rows, 16 NT a wave.
+// A wave's products for RW rows and one 32-key step of 2 DT fragments of keys and values.
+template <class E, int DT, int RW>
+struct Products;
+
+// 16 rows: key fragments [tile t][32-wide slice of D], value fragments [16-wide slice]
+template <class E, int DT>
+struct Products<E, DT, 16> {
+  static constexpr int kGroups = 1;  // of eight keys, a lane's
+  typedef f32x4 Out;
+  static constexpr int kOuts = 2 * DT;   // tiles of O, four consecutive d a lane and quad
+  // first key of a lane's group in the step
+  static __device__ __forceinline__ int key(int lane, int) { return 8 * (lane >> 4); }
+  // the lane (of row c) and the group that hold key k
+  static __device__ __forceinline__ int lane_of(int k, int c) { return (k >> 3) * 16 + c; }
+  static __device__ __forceinline__ int group_of(int) { return 0; }
+  // first d of a lane's slice of Q for k-step i
+  static __device__ __forceinline__ int slice(int lane, int i) { return 32 * i + 8 * (lane >> 4); }
+  static constexpr int kSlices = DT;
+  // index of four consecutive d: quad g of tile t
+  static __device__ __forceinline__ int d4(int lane, int t, int) { return 4 * t + (lane >> 4); }
+  static constexpr int kQuads = 1;
+  // half of the step whose block a staged fragment's lane reads, and where in the block
+  static __device__ __forceinline__ int half(int lane, int wave) {
+    return wave < 2 ? (lane >> 3) & 1 : lane >> 5;
+  }
+  static __device__ __forceinline__ int offset(int lane, int wave) {
+    const int c = lane & 15, p = lane >> 4;
+    return wave < 2 ? (8 * ((c >> 2) & 1) + 4 * wave + (c & 3)) * 32 + 8 * p
+                    : (wave - 2) * DT * 256 + c * 16 + 8 * (p & 1);
+  }
+  static constexpr int kValueStep = 256;  // elements between a value wave's fragments
+  static __device__ __forceinline__ void scores(const u32x4* k, const u32x4 (&q)[kSlices],
+                                                float (&x)[8]) {
+    const int lane = threadIdx.x & 63;
+    u32x4 f[2 * DT];
+#pragma unroll
+    for (int i = 0; i < 2 * DT; ++i) f[i] = k[i * 64 + lane];
+    f32x4 s[2] = {};
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) s[t] = E::mfma(f[t * DT + i], q[i], s[t]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][e & 3];
+  }
+  // O += V^T P for one fragment; `group` is 0 and `t` the tile of O
+  static constexpr int kValues = 2 * DT;
+  static __device__ __forceinline__ constexpr int tile(int i) { return i; }
+  static __device__ __forceinline__ constexpr int group(int) { return 0; }
+  static __device__ __forceinline__ Out mfma(u32x4 v, u32x4 p, Out o) { return E::mfma(v, p, o); }
+};
+
+// 32 rows: keys as they lie in their two 16-token blocks (the 16-byte pieces of a
+// kilobyte placed so that a fragment's rows meet different banks: piece q of row r at slot
+// 4 r + (q ^ r / 4)), value fragments [block][32-wide slice]
+template <class E, int DT>
+struct Products<E, DT, 32> {
+  static constexpr int kGroups = 2;
+  typedef f32x16 Out;
+  static constexpr int kOuts = DT;
+  static __device__ __forceinline__ int key(int lane, int j) { return 16 * j + 8 * (lane >> 5); }
+  static __device__ __forceinline__ int lane_of(int k, int c) { return ((k >> 3) & 1) * 32 + c; }
+  static __device__ __forceinline__ int group_of(int k) { return k >> 4; }
+  static __device__ __forceinline__ int slice(int lane, int i) { return 16 * i + 8 * (lane >> 5); }
+  static constexpr int kSlices = 2 * DT;
+  static __device__ __forceinline__ int d4(int lane, int t, int g) {
+    return 8 * t + 2 * g + (lane >> 5);
+  }
+  static constexpr int kQuads = 4;
+  static __device__ __forceinline__ int half(int, int wave) { return wave & 1; }
+  static __device__ __forceinline__ int offset(int lane, int wave) {
+    const int r = lane >> 2;
+    return wave < 2 ? r * 32 + ((lane & 3) ^ (r >> 2)) * 8 : (lane & 31) * 16 + 8 * (lane >> 5);
+  }
+  static constexpr int kValueStep = 512;
+  static __device__ __forceinline__ void scores(const u32x4* k, const u32x4 (&q)[kSlices],
+                                                float (&x)[16]) {
+    const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+    const int key = (c & 19) | (c & 4) << 1 | (c & 8) >> 1, r = key & 15;
+    const u32x4* row = k + (key >> 4) * (DT * 64) + 4 * r;
+    u32x4 f[2 * DT];
+#pragma unroll
+    for (int i = 0; i < 2 * DT; ++i)
+      f[i] = row[(i >> 1) * 64 + (((i & 1) * 2 + h) ^ (r >> 2))];
+    f32x16 s = {};
+#pragma unroll
+    for (int i = 0; i < 2 * DT; ++i) s = E::mfma32(f[i], q[i], s);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = s[e];
+  }
+  static constexpr int kValues = 2 * DT;
+  static __device__ __forceinline__ constexpr int tile(int i) { return i % DT; }
+  static __device__ __forceinline__ constexpr int group(int i) { return i / DT; }
+  static __device__ __forceinline__ Out mfma(u32x4 v, u32x4 p, Out o) {
+    return E::mfma32(v, p, o);
+  }
+};
+
+// One workgroup = one share of the cache, key head and block of 4 RW rows, RW a wave.
 //
 // The four waves stage the fragments of a 32-key step in LDS (a quarter each, straight
 // from memory) and every wave reads all of them for its own rows.  S stages: the loads
@@ -224,24 +328,25 @@ __device__ __forceinline__ void write_row(const AttentionArgs& a, int64_t t, int
 // that a step has come and that the one before has been read.
 //
 // ONE: there is one row block, nobody reads the cache's lines again, and they are not kept.
-template <class E, int DT, int NT, int S, bool ONE>
+template <class E, int DT, int RW, int S, bool ONE>
 __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const AttentionArgs a,
-                                                                     int shares, int row_blocks) {
+                                                                        int shares,
+                                                                        int row_blocks) {
+  using P = Products<E, DT, RW>;
   constexpr int D = 32 * DT;
-  constexpr int OT = 2 * DT;                 // 16-wide slices of D
-  constexpr int kStage = 4 * DT * 1024;      // bytes: keys [tile][slice], values [slice]
-  constexpr int kRowsWave = 16 * NT, kRowsBlock = kWaves * kRowsWave;
+  constexpr int kStage = 4 * DT * 1024;  // bytes: 2 DT fragments of keys, 2 DT of values
+  constexpr int kKeys = 8 * P::kGroups;  // scores a lane holds
   extern __shared__ __attribute__((aligned(1024))) char lds[];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, p = lane >> 4;
+  const int c = lane & (RW - 1);
   // Workgroups 8 apart share an XCD: the row blocks that read the same keys do.
   const int id = blockIdx.x;
   const int unit = id / (8 * row_blocks) * 8 + id % 8;
   const int hk = unit % a.Hkv;
   const uint32_t share = unit / a.Hkv;
-  const int block_row0 = id / 8 % row_blocks * kRowsBlock;
+  const int block_row0 = id / 8 % row_blocks * (kWaves * RW);
   int b;
   uint32_t before;
   Window window;
@@ -262,10 +367,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
 
   // what a lane takes of a step's fragments: half of the step, and where in a block
   const bool key_wave = wave < 2;
-  const int half = key_wave ? c >> 3 : p >> 1;
-  const uint16_t* src = key_wave
-      ? a.kc + (8 * ((c >> 2) & 1) + 4 * wave + (c & 3)) * 32 + 8 * p
-      : a.vc + (wave - 2) * DT * 256 + c * 16 + 8 * (p & 1);
+  const int half = P::half(lane, wave);
+  const uint16_t* src = (key_wave ? a.kc : a.vc) + P::offset(lane, wave);
 
   for (; b < a.B && before < share_end; ++b) {
     if (b - window.base >= 64) {
@@ -289,26 +392,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
     if (block_row0 >= rows) continue;
     int end = own_end;
     if (!a.mask) {  // a chain: nothing past the last row's token
-      const int last = min(block_row0 + kRowsBlock, rows) - 1;
+      const int last = min(block_row0 + kWaves * RW, rows) - 1;
       end = min(end, (ctx + last / group + 32) >> 5);
     }
     // where the last waves have fewer rows, a compute unit's next workgroup turns them round
-    const int row0 = block_row0 + (id >> 8 & 1 ? kWaves - 1 - wave : wave) * kRowsWave;
+    const int row0 = block_row0 + (id >> 8 & 1 ? kWaves - 1 - wave : wave) * RW;
     const bool idle = row0 >= rows;  // a wave that only stages
 
-    u32x4 qf[NT][DT];
-    int tok[NT];  // the row's token in its request
+    const int row = row0 + c, tok = row / group;  // the lane's row, its token in the request
+    const int64_t tok_at = (int64_t)cu + tok;     // and that token's place in q
+    const bool in = row < rows && tok_at >= 0 && tok_at < a.T;
+    u32x4 qf[P::kSlices];
+    const uint16_t* q = a.q + tok_at * a.q_st + (int64_t)(hk * group + row % group) * a.q_sh;
 #pragma unroll
-    for (int rt = 0; rt < NT; ++rt) {
-      const int r = row0 + rt * 16 + c;
-      tok[rt] = r / group;
-      const int64_t t = (int64_t)cu + tok[rt];
-      const bool in = r < rows && t >= 0 && t < a.T;
-      const uint16_t* q = a.q + t * a.q_st + (int64_t)(hk * group + r % group) * a.q_sh + 8 * p;
-#pragma unroll
-      for (int ks = 0; ks < DT; ++ks)
-        qf[rt][ks] = in ? *reinterpret_cast<const u32x4*>(q + 32 * ks) : u32x4{};
-    }
+    for (int i = 0; i < P::kSlices; ++i)
+      qf[i] = in ? *reinterpret_cast<const u32x4*>(q + P::slice(lane, i)) : u32x4{};
 
     // Table entry of the 16 tokens at 32 step + 16 half (-1 past the request's tokens), and
     // the 16-token block of the cache it stands for (-1 where there is none).
@@ -333,19 +431,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
       char* to = lds + (step % S) * kStage + wave * (DT * 1024);
 #pragma unroll
       for (int i = 0; i < DT; ++i)
-        __builtin_amdgcn_global_load_lds((global_ptr_t)(from + i * (key_wave ? 512 : 256)),
-                                         (lds_ptr_t)(to + i * 1024), 16, 0, ONE ? kNonTemporal : 0);
+        __builtin_amdgcn_global_load_lds(
+            (global_ptr_t)(from + i * (key_wave ? 512 : P::kValueStep)),
+            (lds_ptr_t)(to + i * 1024), 16, 0, ONE ? kNonTemporal : 0);
       id0 = page_of(step + 1, 0);
       id1 = page_of(step + 1, 1);
     };
 
-    f32x4 o[NT][OT] = {};
-    float m[NT], l[NT];
-#pragma unroll
-    for (int rt = 0; rt < NT; ++rt) {
-      m[rt] = -INFINITY;
-      l[rt] = 0.0f;
-    }
+    typename P::Out o[P::kOuts] = {};
+    float m = -INFINITY, l = 0.0f;
 
     barrier();  // the stages of the request before have been read
     // S - 1 steps, the last again where there are fewer: with a fixed number of loads behind
@@ -354,12 +448,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
     for (int i = 0; i < S - 1; ++i) stage(begin + i);
     wait_vm<(S - 1) * DT>();
 #pragma unroll
-    for (int rt = 0; rt < NT; ++rt)
-#pragma unroll
-      for (int ks = 0; ks < DT; ++ks) {
-        asm volatile("" : "+v"(qf[rt][ks]));
-        qf[rt][ks] = (qf[rt][ks] & keep_q) ^ flip;
-      }
+    for (int i = 0; i < P::kSlices; ++i) {
+      asm volatile("" : "+v"(qf[i]));
+      qf[i] = (qf[i] & keep_q) ^ flip;
+    }
     for (int step = begin; step < end; ++step) {
       if (end - step >= S - 1)
         wait_vm<(S - 2) * DT>();
@@ -368,158 +460,146 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
       barrier();
       if (step + S - 1 < end) stage(step + S - 1);
       if (idle) continue;
-      const u32x4* kf = reinterpret_cast<const u32x4*>(lds + (step % S) * kStage) + lane;
-      const u32x4* vf = kf + 2 * DT * 64;
+      const u32x4* kf = reinterpret_cast<const u32x4*>(lds + (step % S) * kStage);
+      const u32x4* vf = kf + 2 * DT * 64 + lane;
 
       // S = K Q^T; then the values' fragments are on their way while P is formed
-      u32x4 f[OT];
-#pragma unroll
-      for (int i = 0; i < OT; ++i) f[i] = kf[i * 64];
-      f32x4 s[NT][2] = {};
-#pragma unroll
-      for (int ks = 0; ks < DT; ++ks)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int rt = 0; rt < NT; ++rt) s[rt][t] = E::mfma(f[t * DT + ks], qf[rt][ks], s[rt][t]);
+      float x[kKeys];
+      P::scores(kf, qf, x);
       __builtin_amdgcn_sched_barrier(0);
+      u32x4 f[P::kValues];
 #pragma unroll
-      for (int i = 0; i < OT; ++i) f[i] = vf[i * 64];
+      for (int i = 0; i < P::kValues; ++i) f[i] = vf[i * 64];
       __builtin_amdgcn_sched_barrier(0);
 
       // Keys that are no context (drafted, or none at all) or on no page: the wave masks.
       const uint32_t hole = (uint32_t)(holes >> (2 * (step & 31))) & 3u;
       const bool masked = hole != 0 || step * 32 + 32 > ctx;
-      uint32_t seen[NT];                  // attended keys among this lane's eight
-      uint32_t there = 0xFFu;             // keys that exist
-      bool poison = false;                // a value is infinite or NaN
+      uint32_t seen[P::kGroups];   // attended keys among each eight of this lane's
+      uint32_t there[P::kGroups];  // keys that exist
+      bool poison = false;         // a value is infinite or NaN
       if (masked) {
-        const int key0 = step * 32 + 8 * p;  // this lane's first key
-        const int j0 = key0 - ctx;           // its drafted index (may be negative)
-        there = (hole >> (p >> 1)) & 1u ? 0u : low_bits(len - key0);
 #pragma unroll
-        for (int rt = 0; rt < NT; ++rt) {
+        for (int j = 0; j < P::kGroups; ++j) {
+          const int key0 = P::key(lane, j);          // the group's first key in the step
+          const int j0 = step * 32 + key0 - ctx;     // its drafted index (may be negative)
+          there[j] = (hole >> (key0 >> 4)) & 1u ? 0u : low_bits(len - step * 32 - key0);
           if (a.mask) {  // the context, then the tree's bits
-            seen[rt] = low_bits(-j0);
-            const int64_t t = (int64_t)cu + tok[rt];
-            if (j0 > -8 && tok[rt] < n_new && t >= 0 && t < a.T) {
-              const int32_t* words = a.mask + t * a.mask_words;
+            seen[j] = low_bits(-j0);
+            if (j0 > -8 && in) {
+              const int32_t* words = a.mask + tok_at * a.mask_words;
               const int w = j0 >> 5;
               const uint32_t w0 = w >= 0 && w < a.mask_words ? (uint32_t)words[w] : 0u;
               const uint32_t w1 = w + 1 < a.mask_words ? (uint32_t)words[w + 1] : 0u;
-              seen[rt] |= (uint32_t)(((uint64_t)w1 << 32 | w0) >> (j0 & 31)) & 0xFFu;
+              seen[j] |= (uint32_t)(((uint64_t)w1 << 32 | w0) >> (j0 & 31)) & 0xFFu;
             }
           } else {  // a chain: the tokens up to the row's own
-            seen[rt] = low_bits(tok[rt] + 1 - j0);
+            seen[j] = low_bits(tok + 1 - j0);
           }
-          seen[rt] &= there;
+          seen[j] &= there[j];
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (!((seen[rt] >> e) & 1u)) s[rt][e >> 2][e & 3] = -INFINITY;
+            if (!((seen[j] >> e) & 1u)) x[8 * j + e] = -INFINITY;
         }
         // values of keys that do not exist are zeroed, and infinite and NaN ones for now
         bool bad = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t keep =
-              ((there >> (2 * i)) & 1u) * 0xFFFFu | ((there >> (2 * i + 1)) & 1u) * 0xFFFF0000u;
+        for (int i = 0; i < P::kValues; ++i)
 #pragma unroll
-          for (int dt = 0; dt < OT; ++dt) {
-            const uint32_t w = f[dt][i] & keep, ex = not_finite<E>(w);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t t = there[P::group(i)] >> (2 * k);
+            const uint32_t w = f[i][k] & ((t & 1u) * 0xFFFFu | (t >> 1 & 1u) * 0xFFFF0000u);
+            const uint32_t ex = not_finite<E>(w);
             bad |= ex != 0;
-            f[dt][i] = w & ~ex;
+            f[i][k] = w & ~ex;
           }
-        }
         poison = __ballot(bad) != 0;
       }
 
-      float top[NT];
-      bool raise = false;  // rare after a request's first step
+      float top = x[0];
 #pragma unroll
-      for (int rt = 0; rt < NT; ++rt) {
-        top[rt] = s[rt][0][0];
+      for (int e = 1; e < kKeys; ++e) top = fmaxf(top, x[e]);
+      top = row_max<RW>(top);
+      if (__ballot(top > m + lag)) {  // rare after a request's first step
+        top = fmaxf(m, top);
+        const float by = __builtin_amdgcn_exp2f((m - (top == -INFINITY ? 0.0f : top)) * scale);
+        m = top;
+        l *= by;
 #pragma unroll
-        for (int e = 1; e < 8; ++e) top[rt] = fmaxf(top[rt], s[rt][e >> 2][e & 3]);
-        top[rt] = row_max(top[rt]);
-        raise |= top[rt] > m[rt] + lag;
+        for (int t = 0; t < P::kOuts; ++t)
+#pragma unroll
+          for (int i = 0; i < 4 * P::kQuads; ++i) o[t][i] *= by;
       }
-      if (__ballot(raise)) {
+      const float ref = m == -INFINITY ? 0.0f : -m * scale;
+      u32x4 hi[P::kGroups], lo[P::kGroups];
 #pragma unroll
-        for (int rt = 0; rt < NT; ++rt) {
-          const float to = fmaxf(m[rt], top[rt]);
-          const float by = __builtin_amdgcn_exp2f((m[rt] - (to == -INFINITY ? 0.0f : to)) * scale);
-          m[rt] = to;
-          l[rt] *= by;
-#pragma unroll
-          for (int dt = 0; dt < OT; ++dt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[rt][dt][i] *= by;
-        }
-      }
-      u32x4 hi[NT], lo[NT];
-#pragma unroll
-      for (int rt = 0; rt < NT; ++rt) {
-        const float ref = m[rt] == -INFINITY ? 0.0f : -m[rt] * scale;
+      for (int j = 0; j < P::kGroups; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float v0 = __builtin_amdgcn_exp2f(fmaf(s[rt][i >> 1][2 * i & 3], scale, ref));
-          const float v1 = __builtin_amdgcn_exp2f(fmaf(s[rt][i >> 1][(2 * i & 3) + 1], scale, ref));
-          l[rt] += v0 + v1;
+          const float v0 = __builtin_amdgcn_exp2f(fmaf(x[8 * j + 2 * i], scale, ref));
+          const float v1 = __builtin_amdgcn_exp2f(fmaf(x[8 * j + 2 * i + 1], scale, ref));
+          l += v0 + v1;
           const u32x2 both = E::split(v0, v1);
-          hi[rt][i] = both[0];
-          lo[rt][i] = both[1];
+          hi[j][i] = both[0];
+          lo[j][i] = both[1];
         }
+
 #pragma unroll
-        for (int dt = 0; dt < OT; ++dt) o[rt][dt] = E::mfma(f[dt], hi[rt], o[rt][dt]);
+      for (int i = 0; i < P::kValues; ++i) {
+        auto& to = o[P::tile(i)];
+        to = P::mfma(f[i], hi[P::group(i)], to);
+      }
 #pragma unroll
-        for (int dt = 0; dt < OT; ++dt) o[rt][dt] = E::mfma(f[dt], lo[rt], o[rt][dt]);
+      for (int i = 0; i < P::kValues; ++i) {
+        auto& to = o[P::tile(i)];
+        to = P::mfma(f[i], lo[P::group(i)], to);
       }
       if (!poison) continue;
       // Infinite and NaN values reach only the rows that attend their keys: one key at a
       // time, and a row that does not attend it keeps its sum.
       for (int k = 0; k < 32; ++k) {
-        const int e = k & 7;
-        const bool mine = p == (k >> 3) && ((there >> e) & 1u);
+        const int e = k & 7, from = P::lane_of(k, c);
 #pragma unroll
-        for (int dt = 0; dt < OT; ++dt) {
-          const uint32_t v = mine ? reinterpret_cast<const uint16_t*>(vf + dt * 64)[e] : 0u;
-          const u32x4 one_v = {v & not_finite<E>(v), 0u, 0u, 0u};
+        for (int j = 0; j < P::kGroups; ++j) {
+          if (P::group_of(k) != j) continue;
+          const bool mine = lane == from && ((there[j] >> e) & 1u);
+          const uint32_t pair = e < 4 ? (e < 2 ? hi[j][0] : hi[j][1])
+                                      : (e < 6 ? hi[j][2] : hi[j][3]);
+          const u32x4 one_p = {mine ? (pair >> (16 * (e & 1))) & 0xFFFFu : 0u, 0u, 0u, 0u};
+          const bool attends = (__shfl((int)seen[j], from) >> e) & 1;
 #pragma unroll
-          for (int rt = 0; rt < NT; ++rt) {
-            const uint32_t pair =
-                e < 4 ? (e < 2 ? hi[rt][0] : hi[rt][1]) : (e < 6 ? hi[rt][2] : hi[rt][3]);
-            const u32x4 one_p = {mine ? (pair >> (16 * (e & 1))) & 0xFFFFu : 0u, 0u, 0u, 0u};
-            const bool attends = (__shfl((int)seen[rt], (k >> 3) * 16 + c) >> e) & 1;
-            const f32x4 with = E::mfma(one_v, one_p, o[rt][dt]);
+          for (int i = 0; i < P::kValues; ++i) {
+            if (P::group(i) != j) continue;
+            const uint32_t v = mine ? reinterpret_cast<const uint16_t*>(vf + i * 64)[e] : 0u;
+            const u32x4 one_v = {v & not_finite<E>(v), 0u, 0u, 0u};
+            auto& to = o[P::tile(i)];
+            const auto with = P::mfma(one_v, one_p, to);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[rt][dt][i] = attends ? with[i] : o[rt][dt][i];
+            for (int t = 0; t < 4 * P::kQuads; ++t) to[t] = attends ? with[t] : to[t];
           }
         }
       }
     }
 
+    const float sum = row_sum<RW>(l);
+    const float top = m == -INFINITY ? m : m * scale;
+    if (row >= rows) continue;
 #pragma unroll
-    for (int rt = 0; rt < NT; ++rt) {
-      const float sum = row_sum(l[rt]);
-      const float top = m[rt] == -INFINITY ? m[rt] : m[rt] * scale;
-      const int row = row0 + rt * 16 + c;
-      if (row >= rows) continue;
-      if (s0 != s1) {
-        const int64_t place = 2 * (int64_t)share + (share == s0 ? 1 : 0);
-        const int64_t at = (place * a.Hkv + hk) * (a.max_new * group) + row;
+    for (int t = 0; t < P::kOuts; ++t)
 #pragma unroll
-        for (int dt = 0; dt < OT; ++dt) parts.out[at * (D / 4) + 4 * dt + p] = o[rt][dt];
-        if (p == 0) parts.stat[at] = {top, sum};
-      } else {
-        const int64_t t = (int64_t)cu + tok[rt];
-        if (t >= 0 && t < a.T) {
-#pragma unroll
-          for (int dt = 0; dt < OT; ++dt)
-            write_row<E>(a, t, hk * group + row % group, 4 * dt + p, o[rt][dt],
-                         top == -INFINITY ? 0.0f : top, sum);
+      for (int g = 0; g < P::kQuads; ++g) {
+        const int d4 = P::d4(lane, t, g);
+        const f32x4 v = {o[t][4 * g], o[t][4 * g + 1], o[t][4 * g + 2], o[t][4 * g + 3]};
+        if (s0 != s1) {
+          const int64_t place = 2 * (int64_t)share + (share == s0 ? 1 : 0);
+          const int64_t at = (place * a.Hkv + hk) * (a.max_new * group) + row;
+          parts.out[at * (D / 4) + d4] = v;
+          if (d4 == 0) parts.stat[at] = {top, sum};
+        } else if (in) {
+          write_row<E>(a, tok_at, hk * group + row % group, d4, v, top == -INFINITY ? 0.0f : top,
+                       sum);
         }
       }
-    }
   }
 }
 
@@ -563,16 +643,16 @@ __global__ __launch_bounds__(256) void join_parts_kernel(const AttentionArgs a, 
 
 namespace {
 
-// How a call is laid out: 16-row tiles a wave holds, row blocks, shares of the cache
+// How a call is laid out: rows a wave holds, row blocks, shares of the cache
 struct Layout {
-  int nt, row_blocks, shares;
+  int rows, row_blocks, shares;
 };
 
 Layout layout_of(int64_t max_new, int64_t H, int64_t Hkv, int64_t D) {
   Layout p;
   const int64_t rows = max_new * (H / Hkv);
-  p.nt = rows <= 64 || D > 128 ? 1 : 2;
-  p.row_blocks = (int)((rows + 64 * p.nt - 1) / (64 * p.nt));
+  p.rows = rows <= 4 * 16 || D > 128 ? 16 : 32;
+  p.row_blocks = (int)((rows + kWaves * p.rows - 1) / (kWaves * p.rows));
   const int64_t target = kUnitsPerCu * device_cu_count();
   const int64_t units = Hkv * p.row_blocks;
   p.shares = (int)std::max<int64_t>(1, target / units);
@@ -590,12 +670,12 @@ hipError_t launch_rows(const AttentionArgs& a, hipStream_t stream) {
   const int64_t units = (int64_t)p.shares * a.Hkv;
   const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.row_blocks));
   const bool one = p.row_blocks == 1;
-  auto* kernel = one ? tree_attention_kernel<E, DT, 1, S, true>
-                     : tree_attention_kernel<E, DT, 1, S, false>;
+  auto* kernel = one ? tree_attention_kernel<E, DT, 16, S, true>
+                     : tree_attention_kernel<E, DT, 16, S, false>;
   if constexpr (DT <= 4)
-    if (p.nt == 2)
-      kernel = one ? tree_attention_kernel<E, DT, 2, S, true>
-                   : tree_attention_kernel<E, DT, 2, S, false>;
+    if (p.rows == 32)
+      kernel = one ? tree_attention_kernel<E, DT, 32, S, true>
+                   : tree_attention_kernel<E, DT, 32, S, false>;
   const hipError_t e = launch_kernel_lds(kernel, grid, dim3(64 * kWaves), S * 4 * DT * 1024,
                                          stream, a, p.shares, p.row_blocks);
   if (e != hipSuccess || p.shares == 1) return e;

@@ -12,7 +12,14 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // eight elements of k-slots 8 (l / 16) ..; D lane l holds column l % 16, rows
 // 4 (l / 16) + 0 .. 3, in fp32.  A and B agree on what k each slot stands for; the
 // kernels use that freedom to take fragments in the order memory holds them.
+//
+// 32x32x16: row and column l % 32, k-slots 8 (l / 32) ..; D lane l holds column l % 32 and, in
+// register r, row 8 (r / 4) + 4 (l / 32) + r % 4.
 struct Half {
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
   static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -29,6 +36,10 @@ struct Half {
 };
 
 struct Bfloat {
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
   static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
