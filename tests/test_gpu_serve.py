@@ -64,7 +64,11 @@ def test_pack_w4(fq, N, K, group, dtype):
 GEMV = [(1, 16, 128, 128), (1, 48, 4096, 128), (2, 80, 384, 32), (5, 208, 1152, 64),
         (13, 1040, 2176, 128), (16, 64, 256, 64), (17, 176, 896, 32), (33, 144, 640, 128),
         (64, 96, 512, 64), (65, 48, 384, 128), (130, 32, 1280, 32), (3, 16, 16512, 128),
-        (1, 12304, 256, 64), (40, 4112, 128, 128)]
+        (1, 12304, 256, 64), (40, 4112, 128, 128),
+        # two tiles an item with an odd one left, K in slices with a short last chunk, more
+        # rows than the activations' room in LDS allows the few-rows kernel
+        (2, 32784, 128, 32), (9, 272, 4224, 128), (28, 528, 3200, 32), (61, 336, 2432, 64),
+        (4, 48, 8320, 128)]
 
 
 @pytest.mark.parametrize("M,N,K,group", GEMV)
@@ -171,14 +175,15 @@ def test_w4_linear(fq):
 @pytest.mark.parametrize("B,ctx_hi,new_hi,page", [(1, 0, 1, 16), (1, 40, 1, 16), (5, 70, 9, 16),
                                                   (64, 300, 1, 32), (300, 100, 40, 16),
                                                   (700, 65, 3, 64), (4096, 30, 2, 16),
-                                                  (3, 0, 5000, 128), (9, 20, 30, 1)])
+                                                  (3, 0, 5000, 128), (9, 20, 30, 1),
+                                                  (37, 100, 36000, 16), (6, 5, 300000, 128)])
 def test_block_tables(fq, B, ctx_hi, new_hi, page):
     say("block_tables", B, ctx_hi, new_hi, page)
     r = rng(5, B, page)
     ctx, new = r.integers(0, ctx_hi + 1, B), r.integers(0, new_hi + 1, B)
     cols = int(max(1, (-(-(ctx + new) // page)).max())) + 2
     table = r.integers(0, 1 << 20, (B, cols)).astype(np.int32)
-    free = r.permutation(1 << 16).astype(np.int32)
+    free = r.permutation(1 << 17).astype(np.int32)
     most = int(new.sum()) + 37
     head = int(r.integers(0, 100))
     want = ref.block_tables(ctx, new, free, table, page, most, head)
@@ -344,6 +349,15 @@ ATTENTION = [
     ([1500], [1], 2, 1, 128, 16, False),
     ([2500, 3], [4, 9], 4, 1, 64, 32, True),
     ([700, 1, 300], [1, 1, 1], 32, 2, 128, 16, False),  # 16 heads a key head
+    # many rows of one key head (32 a wave), ragged, with masks, and over several row blocks
+    ([90, 7], [13, 17], 16, 2, 64, 16, True),
+    ([45, 300], [40, 9], 8, 2, 96, 32, True),
+    ([130, 0, 64], [33, 18, 40], 8, 1, 128, 64, True),
+    ([11], [75], 4, 2, 96, 16, False),
+    # long enough for many parts, of few rows and of many
+    ([9000], [2], 4, 2, 96, 16, False),
+    ([6000, 20], [3, 1], 16, 1, 256, 16, True),
+    ([7000], [18], 4, 1, 64, 16, True),
 ]
 
 
@@ -374,11 +388,12 @@ def test_rows_that_attend_nothing(fq, dtype):
 
 @pytest.mark.parametrize("kind", ["nan", "inf"])
 @pytest.mark.parametrize("dtype", [F16, BF16])
-def test_infinities_and_nan_in_masked_places(fq, dtype, kind):
+@pytest.mark.parametrize("H", [4, 16])
+def test_infinities_and_nan_in_masked_places(fq, dtype, kind, H):
     """A drafted token with NaN or infinite keys and values spoils the rows that attend it
-    and no other."""
+    and no other (36 rows and, in wider tiles, 144)."""
     ctx, new = [20], [9]
-    p = problem(rng(9), ctx, new, 4, 1, 128, 16, dtype, True)
+    p = problem(rng(9), ctx, new, H, 1, 128, 16, dtype, True)
     seen = p["masks"][0]
     bad = 4
     seen[:, bad] = False

@@ -27,10 +27,10 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWaves = 4;
-// Workgroups a compute unit holds.
-constexpr int kUnitsPerCu = 2;
+// Workgroups a compute unit holds: by LDS (4 stages of 2 D 64 bytes, 2 where D = 256).
+constexpr int units_per_cu(int64_t D) { return D <= 64 ? 4 : 2; }
 // What starting on a request costs, in 32-key steps, and the least share of a workgroup.
-constexpr uint32_t kHead = 2, kMinShare = 8;
+constexpr uint32_t kHead = 5, kMinShare = 8;
 // Probabilities are at most 2^kLag before the division (fp16 holds 2^15).
 constexpr float kLag = 8.0f;
 
@@ -603,42 +603,66 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
   }
 }
 
-// Joins the parts of requests that several shares hold, in order: thread = four elements
-// of one row.
-template <class E, int DT>
+// Joins the parts of requests that several shares hold, in a fixed order: D / 4 threads (four
+// elements each) take a row's parts SLICES at a time, and the slices' sums are joined
+// through LDS.
+template <class E, int DT, int SLICES>
 __global__ __launch_bounds__(256) void join_parts_kernel(const AttentionArgs a, int shares) {
   constexpr int D = 32 * DT;
-  constexpr int kRows = 256 / (D / 4);
+  constexpr int kLanes = D / 4, kRows = 256 / kLanes / SLICES;
+  __shared__ f32x4 sums[SLICES > 1 ? 256 : 1];
+  __shared__ float2 stats[SLICES > 1 ? 256 : 1];
   const int b = blockIdx.z, hk = blockIdx.y;
   const int group = a.H / a.Hkv;
-  const int row = blockIdx.x * kRows + threadIdx.x / (D / 4), d4 = threadIdx.x % (D / 4);
+  const int slot = threadIdx.x / kLanes, d4 = threadIdx.x % kLanes;
+  const int slice = slot % SLICES;
+  const int row = blockIdx.x * kRows + slot / SLICES;
   const Parts parts = parts_of(a, shares, a.max_new * group);
   const int2 plan = parts.plan[b];  // not set for a request without new tokens
   const Request request = load_request(a, b);
-  if (threadIdx.x >= kRows * (D / 4) || row >= request.n_new * group || plan.x == plan.y) return;
+  const int rows = request.n_new * group;
+  if ((int)blockIdx.x * kRows >= rows || plan.x == plan.y) return;  // the whole workgroup
+  const bool in = slot < kRows * SLICES && row < rows;
   const int64_t stride = (int64_t)a.Hkv * (a.max_new * group);
   // the first share's place is 2 i + 1, the others' 2 i
-  const int64_t at0 = (2 * (int64_t)plan.x + 1) * stride + (int64_t)hk * (a.max_new * group) + row;
-  const int64_t at1 = at0 + stride;
-  const int n = plan.y - plan.x;
-  float top = parts.stat[at0].x;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) top = fmaxf(top, parts.stat[at1 + 2 * i * stride].x);
-  const float ref = top == -INFINITY ? 0.0f : top;
-  float total = 0.0f;
+  const int64_t at0 = 2 * (int64_t)plan.x * stride + (int64_t)hk * (a.max_new * group) + row;
+  const int n = in ? plan.y - plan.x + 1 : 0;
+  float top = -INFINITY, total = 0.0f;
   f32x4 acc = {};
 #pragma unroll 4
-  for (int i = -1; i < n; ++i) {
-    const int64_t at = i < 0 ? at0 : at1 + 2 * i * stride;
+  for (int i = slice; i < n; i += SLICES) {
+    const int64_t at = at0 + (i == 0 ? 1 : 2 * (int64_t)i) * stride;
     const float2 s = parts.stat[at];
     const f32x4 o = parts.out[at * (D / 4) + d4];
-    const float by = __builtin_amdgcn_exp2f(s.x - ref);
-    total = fmaf(s.y, by, total);
+    const float to = fmaxf(top, s.x), ref = to == -INFINITY ? 0.0f : to;
+    const float old = __builtin_amdgcn_exp2f(top - ref), by = __builtin_amdgcn_exp2f(s.x - ref);
+    top = to;
+    total = fmaf(s.y, by, total * old);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = fmaf(o[k], by, acc[k]);
+    for (int k = 0; k < 4; ++k) acc[k] = fmaf(o[k], by, acc[k] * old);
+  }
+  if constexpr (SLICES > 1) {
+    sums[threadIdx.x] = acc;
+    stats[threadIdx.x] = {top, total};
+    __syncthreads();
+    if (slice != 0 || !in) return;
+    for (int j = 1; j < SLICES; ++j) top = fmaxf(top, stats[threadIdx.x + j * kLanes].x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    total = 0.0f;
+    acc = f32x4{};
+#pragma unroll
+    for (int j = 0; j < SLICES; ++j) {
+      const float2 s = stats[threadIdx.x + j * kLanes];
+      const f32x4 o = sums[threadIdx.x + j * kLanes];
+      const float by = __builtin_amdgcn_exp2f(s.x - ref);
+      total = fmaf(s.y, by, total);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] = fmaf(o[k], by, acc[k]);
+    }
   }
   const int64_t t = (int64_t)request.cu + row / group;
-  if (t >= 0 && t < a.T) write_row<E>(a, t, hk * group + row % group, d4, acc, ref, total);
+  if (in && t >= 0 && t < a.T)
+    write_row<E>(a, t, hk * group + row % group, d4, acc, top == -INFINITY ? 0.0f : top, total);
 }
 
 namespace {
@@ -653,7 +677,7 @@ Layout layout_of(int64_t max_new, int64_t H, int64_t Hkv, int64_t D) {
   const int64_t rows = max_new * (H / Hkv);
   p.rows = rows <= 4 * 16 || D > 128 ? 16 : 32;
   p.row_blocks = (int)((rows + kWaves * p.rows - 1) / (kWaves * p.rows));
-  const int64_t target = kUnitsPerCu * device_cu_count();
+  const int64_t target = units_per_cu(D) * device_cu_count();
   const int64_t units = Hkv * p.row_blocks;
   p.shares = (int)std::max<int64_t>(1, target / units);
   return p;
@@ -679,10 +703,14 @@ hipError_t launch_rows(const AttentionArgs& a, hipStream_t stream) {
   const hipError_t e = launch_kernel_lds(kernel, grid, dim3(64 * kWaves), S * 4 * DT * 1024,
                                          stream, a, p.shares, p.row_blocks);
   if (e != hipSuccess || p.shares == 1) return e;
-  const int rows = a.max_new * (a.H / a.Hkv), per = 256 / (8 * DT);
-  return launch_kernel(join_parts_kernel<E, DT>,
-                       dim3((unsigned)((rows + per - 1) / per), (unsigned)a.Hkv, (unsigned)a.B),
-                       dim3(256), stream, a, p.shares);
+  // a row's parts number about shares / B: few are taken by one thread after the other
+  constexpr int kSlots = 256 / (8 * DT);
+  const bool many = p.shares >= 8 * a.B;
+  const int rows = a.max_new * (a.H / a.Hkv), per = many ? 1 : kSlots;
+  return launch_kernel(
+      many ? join_parts_kernel<E, DT, kSlots> : join_parts_kernel<E, DT, 1>,
+      dim3((unsigned)((rows + per - 1) / per), (unsigned)a.Hkv, (unsigned)a.B), dim3(256), stream,
+      a, p.shares);
 }
 
 template <class E>
