@@ -440,35 +440,34 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
     const char* from = lds + chunk % (kAhead + 1) * kBytes;
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
-      u32x4 xf[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          xf[n][j] = *reinterpret_cast<const u32x4*>(
-              from + ((i * 2 + (j >> 1)) * kBlocks + 2 * n) * 1024 + frag_row +
-              ((((j & 1) * 4 + p) ^ row8) * 16));
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        f32x4 start[NT] = {};
+        f32x4 start[NT] = {}, dot[T][NT] = {};
 #pragma unroll
-        for (int j = g * kSteps; j < (g + 1) * kSteps; ++j)
+        for (int j = g * kSteps; j < (g + 1) * kSteps; ++j) {
+          u32x4 xf[NT];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) start[n] = E::mfma(minus24, xf[n][j], start[n]);
+          for (int n = 0; n < NT; ++n)
+            xf[n] = *reinterpret_cast<const u32x4*>(
+                from + ((i * 2 + (j >> 1)) * kBlocks + 2 * n) * 1024 + frag_row +
+                ((((j & 1) * 4 + p) ^ row8) * 16));
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-          f32x4 dot[NT];
+          for (int n = 0; n < NT; ++n) start[n] = E::mfma(minus24, xf[n], start[n]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) dot[n] = start[n];
-#pragma unroll
-          for (int j = g * kSteps; j < (g + 1) * kSteps; ++j) {
+          for (int t = 0; t < T; ++t) {
             const u32x4 a = codes_plus_24<E>(r.w[i][t][j], mask, base);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) dot[n] = E::mfma(a, xf[n][j], dot[n]);
+            for (int n = 0; n < NT; ++n) dot[t][n] = E::mfma(a, xf[n], dot[t][n]);
           }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) scale_add(acc[t][n], dot[n], r.s[i][t][g]);
         }
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) dot[t][n][k] += start[n][k];
+            scale_add(acc[t][n], dot[t][n], r.s[i][t][g]);
+          }
       }
     }
   };
@@ -535,12 +534,15 @@ __global__ __launch_bounds__(256) void join_slices_kernel(const float* __restric
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= quads) return;
   const f32x4* from = reinterpret_cast<const f32x4*>(part) + i;
-  f32x4 s = from[0];
-#pragma unroll 4
-  for (int v = 1; v < slices; ++v) {
-    const f32x4 o = from[v * quads];
+  f32x4 s = {};
+  for (int v0 = 0; v0 < slices; v0 += 8) {
+    f32x4 o[8];  // eight loads at a time
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s[k] += o[k];
+    for (int v = 0; v < 8; ++v) o[v] = v0 + v < slices ? from[(v0 + v) * quads] : f32x4{};
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += o[v][k];
   }
   store_four<E>(y + 4 * i, s);
 }
@@ -560,16 +562,22 @@ hipError_t pack_any(const uint16_t* w, int64_t N, int64_t K, int group, uint32_t
 // The few-rows kernel: two workgroups' activations and sums fit a compute unit's LDS.
 bool few_rows(int64_t M, int64_t K) { return M <= 4 && M * (K + 32) * 2 <= 48 * 1024; }
 
-// The other one: tiles a wave, and slices of K that give every compute unit two
-// workgroups of the 16 waves it holds.
+// The other one: tiles a wave, and slices of K that give every compute unit a workgroup.
+// Twice the slices only add sums to join (13 x 5120 x 13824: 22.5 us against 18.7; 64 x 8192 x
+// 8192: 34 against 26), half of them leave compute units idle (25 and 34).
 struct Cut {
   int tiles_a_wave, slices;
 };
 
 Cut cut_of(int64_t M, int64_t N, int64_t K) {
   Cut cut;
-  cut.tiles_a_wave = 1;
-  const int64_t units = (N / 16 + 7) / 8 * ((M + 63) / 64);
+  // With more than 32 rows of x its reads from LDS bound a wave; two tiles share them, and
+  // the -24 x sums, where one tile a wave would take the compute units twice (64 rows,
+  // K = 8192: N = 40960 87 us against 107, 57344 98 against 117, 131072 204 against 247; but
+  // 8192, 29 against 26).
+  cut.tiles_a_wave = M > 32 && N / 16 > 8 * device_cu_count() ? 2 : 1;
+  const int64_t per = 8 * cut.tiles_a_wave;
+  const int64_t units = (N / 16 + per - 1) / per * ((M + 63) / 64);
   const int64_t chunk = chunk_blocks(M <= 16 ? 1 : M <= 32 ? 2 : 4);
   const int64_t chunks = (K / 128 + chunk - 1) / chunk;
   const int64_t target = device_cu_count();
@@ -589,17 +597,17 @@ hipError_t gemv_launch(const uint16_t* x, int64_t x_stride, const uint32_t* w4,
                            (int)N, (int)K, (int)tiles, (int)items, y);
 }
 
-template <class E, int G, int NT>
+template <class E, int G, int NT, int T>
 hipError_t gemm_launch(const uint16_t* x, int64_t x_stride, const uint32_t* w4,
                        const uint16_t* sw, int64_t M, int64_t N, int64_t K, float* part,
                        uint16_t* y, hipStream_t stream) {
-  constexpr int T = 1;
   const Cut cut = cut_of(M, N, K);
   const int64_t tiles = N / 16;
   const dim3 grid((unsigned)((tiles + 8 * T - 1) / (8 * T) * cut.slices),
                   (unsigned)((M + 63) / 64));
   const hipError_t e =
-      launch_kernel(gemm_w4_kernel<E, G, NT, T>, grid, dim3(512), stream, x, x_stride, w4, sw, (int)M, (int)N, (int)K, (int)tiles, cut.slices, part, y);
+      launch_kernel(gemm_w4_kernel<E, G, NT, T>, grid, dim3(512), stream, x, x_stride, w4, sw,
+                    (int)M, (int)N, (int)K, (int)tiles, cut.slices, part, y);
   if (e != hipSuccess || cut.slices == 1) return e;
   const int64_t quads = M * N / 4;
   return launch_kernel(join_slices_kernel<E>, dim3((unsigned)((quads + 255) / 256)), dim3(256),
@@ -617,9 +625,11 @@ hipError_t gemv_any(const uint16_t* x, int64_t x_stride, const uint32_t* w4, con
       return gemv_launch<E, G, 2>(x, x_stride, w4, sw, M, N, K, y, stream);
     return gemv_launch<E, G, 1>(x, x_stride, w4, sw, M, N, K, y, stream);
   }
-  if (M <= 16) return gemm_launch<E, G, 1>(x, x_stride, w4, sw, M, N, K, part, y, stream);
-  if (M <= 32) return gemm_launch<E, G, 2>(x, x_stride, w4, sw, M, N, K, part, y, stream);
-  return gemm_launch<E, G, 4>(x, x_stride, w4, sw, M, N, K, part, y, stream);
+  if (M <= 16) return gemm_launch<E, G, 1, 1>(x, x_stride, w4, sw, M, N, K, part, y, stream);
+  if (M <= 32) return gemm_launch<E, G, 2, 1>(x, x_stride, w4, sw, M, N, K, part, y, stream);
+  if (cut_of(M, N, K).tiles_a_wave == 1)
+    return gemm_launch<E, G, 4, 1>(x, x_stride, w4, sw, M, N, K, part, y, stream);
+  return gemm_launch<E, G, 4, 2>(x, x_stride, w4, sw, M, N, K, part, y, stream);
 }
 
 template <class E>
