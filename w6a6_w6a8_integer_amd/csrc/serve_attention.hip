@@ -259,7 +259,6 @@ struct Products<E, DT, 16> {
     u32x4 f[2 * DT];
 #pragma unroll
     for (int i = 0; i < 2 * DT; ++i) f[i] = k[i * 64 + lane];
-    __builtin_amdgcn_sched_barrier(0);  // all of the reads are on their way together
     f32x4 s[2] = {};
 #pragma unroll
     for (int i = 0; i < DT; ++i)
@@ -307,7 +306,6 @@ struct Products<E, DT, 32> {
 #pragma unroll
     for (int i = 0; i < 2 * DT; ++i)
       f[i] = row[(i >> 1) * 64 + (((i & 1) * 2 + h) ^ (r >> 2))];
-    __builtin_amdgcn_sched_barrier(0);  // all of the reads are on their way together
     f32x16 s = {};
 #pragma unroll
     for (int i = 0; i < 2 * DT; ++i) s = E::mfma32(f[i], q[i], s);
@@ -430,7 +428,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
       const int at = 2 * (step & 31);
       holes = (holes & ~(3ull << at)) | (uint64_t)((b0 < 0 ? 1 : 0) | (b1 < 0 ? 2 : 0)) << at;
       const uint16_t* from = src + (int64_t)max(half ? b1 : b0, 0) * (16 * D);
-      char* to = lds + ((unsigned)step % S) * kStage + wave * (DT * 1024);
+      char* to = lds + (step % S) * kStage + wave * (DT * 1024);
 #pragma unroll
       for (int i = 0; i < DT; ++i)
         __builtin_amdgcn_global_load_lds(
@@ -462,7 +460,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
       barrier();
       if (step + S - 1 < end) stage(step + S - 1);
       if (idle) continue;
-      const u32x4* kf = reinterpret_cast<const u32x4*>(lds + ((unsigned)step % S) * kStage);
+      const u32x4* kf = reinterpret_cast<const u32x4*>(lds + (step % S) * kStage);
       const u32x4* vf = kf + 2 * DT * 64 + lane;
 
       // S = K Q^T; then the values' fragments are on their way while P is formed
