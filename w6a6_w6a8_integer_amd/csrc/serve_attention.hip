@@ -559,6 +559,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
       if (!poison) continue;
       // Infinite and NaN values reach only the rows that attend their keys: one key at a
       // time, and a row that does not attend it keeps its sum.
+#pragma unroll 1
       for (int k = 0; k < 32; ++k) {
         const int e = k & 7, from = P::lane_of(k, c);
 #pragma unroll
