@@ -348,7 +348,8 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
 // the 16-byte pieces are placed so that the 16 lanes of a fragment read (16 rows, one
 // piece each) meet 16 different banks: piece k of row r at slot 8 (r ^ h) + (k ^ r), h the
 // block's parity.
-constexpr int chunk_blocks(int NT) { return NT == 1 ? 4 : 2; }
+// k-blocks of a chunk (up to 16 rows, with four: 13 x 5120 x 13824 18.7 us against 16.2)
+constexpr int kChunk = 2;
 
 template <class E, int G, int NT, int T>
 __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
@@ -356,7 +357,6 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
     const uint16_t* __restrict__ sw, int M, int N, int K, int tiles, int slices,
     float* __restrict__ part, uint16_t* __restrict__ y) {
   constexpr int kGroups = 128 / G, kSteps = G / 32;
-  constexpr int kChunk = chunk_blocks(NT);             // k-blocks
   constexpr int kBlocks = 2 * NT;                      // of eight rows
   constexpr int kBytes = kChunk * 2 * kBlocks * 1024;  // of x a chunk
   constexpr int kMine = kChunk * kBlocks / 4;          // kilobytes of it a wave stages
@@ -563,8 +563,8 @@ hipError_t pack_any(const uint16_t* w, int64_t N, int64_t K, int group, uint32_t
 bool few_rows(int64_t M, int64_t K) { return M <= 4 && M * (K + 32) * 2 <= 48 * 1024; }
 
 // The other one: tiles a wave, and slices of K that give every compute unit a workgroup.
-// Twice the slices only add sums to join (13 x 5120 x 13824: 22.5 us against 18.7; 64 x 8192 x
-// 8192: 34 against 26), half of them leave compute units idle (25 and 34).
+// Twice the slices only add sums to join (13 x 5120 x 13824: 17.9 us against 16.2; 64 x 8192 x
+// 8192: 34 against 26), half of them leave compute units idle (22 and 34).
 struct Cut {
   int tiles_a_wave, slices;
 };
@@ -578,8 +578,7 @@ Cut cut_of(int64_t M, int64_t N, int64_t K) {
   cut.tiles_a_wave = M > 32 && N / 16 > 8 * device_cu_count() ? 2 : 1;
   const int64_t per = 8 * cut.tiles_a_wave;
   const int64_t units = (N / 16 + per - 1) / per * ((M + 63) / 64);
-  const int64_t chunk = chunk_blocks(M <= 16 ? 1 : M <= 32 ? 2 : 4);
-  const int64_t chunks = (K / 128 + chunk - 1) / chunk;
+  const int64_t chunks = (K / 128 + kChunk - 1) / kChunk;
   const int64_t target = device_cu_count();
   cut.slices = (int)std::clamp<int64_t>(target / units, 1, std::min<int64_t>(chunks, 16));
   return cut;
