@@ -5,6 +5,7 @@
 // code in [-8, 7] is exact in fp32, so the MFMA sums a group's products without an
 // earlier rounding and the scale is applied once per group in fp32.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "serve_device.h"
@@ -136,6 +137,24 @@ __device__ __forceinline__ void scale_add(f32x4& acc, f32x4 dot, u32x2 scales) {
     acc[i] = fmaf(half_bits_to_float((uint16_t)(scales[i >> 1] >> (16 * (i & 1)))), dot[i], acc[i]);
 }
 
+// A k-block's scales of a tile in one load: lane (c, p) has those of rows 4 p to 4 p + 3 and
+// group c % (128 / G); group g's are those of lane g of each four.
+template <int kGroups>
+__device__ __forceinline__ u32x2 group_scales(u32x2 s, int g) {
+  if constexpr (kGroups == 1) return s;
+  auto of = [&](auto lane) {
+    constexpr int kSame = decltype(lane)::value * 0x55;  // that lane's value in all four
+    return u32x2{(uint32_t)__builtin_amdgcn_mov_dpp((int)s[0], kSame, 15, 15, true),
+                 (uint32_t)__builtin_amdgcn_mov_dpp((int)s[1], kSame, 15, 15, true)};
+  };
+  switch (g) {
+    case 0: return of(std::integral_constant<int, 0>{});
+    case 1: return of(std::integral_constant<int, 1>{});
+    case 2: return of(std::integral_constant<int, 2>{});
+    default: return of(std::integral_constant<int, 3>{});
+  }
+}
+
 __device__ __forceinline__ bool not_finite(f32x4 v) {
   return fmaf(v[0], 0.0f, v[1] * 0.0f) + fmaf(v[2], 0.0f, v[3] * 0.0f) != 0.0f;
 }
@@ -204,7 +223,7 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
 
   struct Slot {
     u32x4 w[T];
-    u32x2 s[T][kGroups];
+    u32x2 s[T];
   } ring[P];
 
   // Loads of one wave step: k-block kb of item, which the offsets stand for.
@@ -214,17 +233,16 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
   const auto rs = make_rsrc(sw + first * T * 16,
                             (uint32_t)((int64_t)(K / G) * N * 2 - (int64_t)first * T * 32));
   int kb = wave;
-  uint32_t w_off = wave * 1024 + lane * 16, s_off = (uint32_t)wave * kGroups * (N * 2) + 8 * p;
-  uint32_t s_item = 0;
+  uint32_t w_off = wave * 1024 + lane * 16;
+  uint32_t s_item = (uint32_t)(wave * kGroups + c % kGroups) * (N * 2) + 8 * p;
+  uint32_t s_off = s_item;
   auto next_load = [&](Slot& r) {
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       r.w[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                              rw, w_off + t * (kbs * 1024), 0, kNonTemporal));
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-        r.s[t][g] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
-                                                  rs, s_off + g * (N * 2) + t * 32, 0, 0));
+      r.s[t] = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, s_off + t * 32, 0, 0));
     }
     kb += W;
     w_off += W * 1024;
@@ -233,7 +251,7 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
       kb = wave;
       w_off += (T * kbs - rounds * W) * 1024;
       s_item += T * 32;
-      s_off = (uint32_t)wave * kGroups * (N * 2) + s_item + 8 * p;
+      s_off = s_item;
     }
   };
 
@@ -262,7 +280,7 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
 #pragma unroll
         for (int j = g * kSteps; j < (g + 1) * kSteps; ++j)
           dot = E::mfma(codes_plus_24<E>(r.w[t][j], mask, base), xf[j], dot);
-        scale_add(acc[t], dot, r.s[t][g]);
+        scale_add(acc[t], dot, group_scales<kGroups>(r.s[t], g));
       }
     }
   };
@@ -398,7 +416,7 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
 
   struct Chunk {
     u32x4 w[kChunk][T];
-    u32x2 s[kChunk][T][kGroups];
+    u32x2 s[kChunk][T];
   } ring[kAhead];
   const char* w0 = reinterpret_cast<const char*>(w4) + (int64_t)tile0 * kbs * 1024;
   const uint32_t w_bytes = (uint32_t)(max(0, min(T, tiles - tile0)) * kbs) * 1024u;
@@ -409,7 +427,7 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
     const auto rw = make_rsrc(w0, chunk < last ? w_bytes : 0u);
     const auto rs = make_rsrc(sw + tile0 * 16, chunk < last ? s_bytes : 0u);
     const uint32_t w_off = chunk * (kChunk * 1024) + lane * 16;
-    uint32_t s_off = (uint32_t)chunk * (kChunk * kGroups) * (N * 2) + 8 * p;
+    const uint32_t s_off = (uint32_t)(chunk * (kChunk * kGroups) + c % kGroups) * (N * 2) + 8 * p;
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
 #pragma unroll
@@ -418,13 +436,10 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
                                                   rw, w_off + t * (kbs * 1024) + i * 1024, 0,
                                                   kNonTemporal));
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-          r.s[i][t][g] = __builtin_bit_cast(
-              u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, s_off + t * 32, 0, 0));
-        s_off += N * 2;
-      }
+      for (int t = 0; t < T; ++t)
+        r.s[i][t] = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                       rs, s_off + (uint32_t)i * kGroups * (N * 2) + t * 32, 0, 0));
     }
   };
 
@@ -461,20 +476,22 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
           }
         }
 #pragma unroll
-        for (int t = 0; t < T; ++t)
+        for (int t = 0; t < T; ++t) {
+          const u32x2 scales = group_scales<kGroups>(r.s[i][t], g);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) dot[t][n][k] += start[n][k];
-            scale_add(acc[t][n], dot[t][n], r.s[i][t][g]);
+            scale_add(acc[t][n], dot[t][n], scales);
           }
+        }
       }
     }
   };
 
   // A chunk's loads: kMine of x, then the weights' and scales'.  Those of chunks past the
   // slice are issued too (the waits count on them) but go nowhere.
-  constexpr int kLoads = kMine + kChunk * T * (1 + kGroups);
+  constexpr int kLoads = kMine + kChunk * T * 2;
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
     stage(first + i);
@@ -560,6 +577,8 @@ hipError_t pack_any(const uint16_t* w, int64_t N, int64_t K, int group, uint32_t
 }
 
 // The few-rows kernel: two workgroups' activations and sums fit a compute unit's LDS.
+// One row of 4096 x 4096 takes 5.0 us with it and 7.2 with the other, of 57344 x 8192 45 and
+// 51; four of 5120 x 5120 (groups of 32) 10.9 and 10.2.
 bool few_rows(int64_t M, int64_t K) { return M <= 4 && M * (K + 32) * 2 <= 48 * 1024; }
 
 // The other one: tiles a wave, and slices of K that give every compute unit a workgroup.
@@ -588,12 +607,18 @@ template <class E, int G, int T>
 hipError_t gemv_launch(const uint16_t* x, int64_t x_stride, const uint32_t* w4,
                        const uint16_t* sw, int64_t M, int64_t N, int64_t K, uint16_t* y,
                        hipStream_t stream) {
-  constexpr int W = 8, P = T == 2 && G == 32 ? 3 : 4;
-  const int64_t tiles = N / 16, items = (tiles + T - 1) / T;
-  const int64_t most = device_cu_count() * (16 / W);  // 16 waves a compute unit
-  return launch_kernel_lds(gemv_w4_kernel<E, G, T, W, P>, dim3((unsigned)std::min(items, most)),
-                           dim3(64 * W), M * (K + 32) * 2, stream, x, x_stride, w4, sw, (int)M,
-                           (int)N, (int)K, (int)tiles, (int)items, y);
+  constexpr int W = 8, P = 4;
+  const int64_t tiles = N / 16, items = (tiles + T - 1) / T, cus = device_cu_count();
+  const int64_t x_bytes = M * (K + 32) * 2;
+  // Two workgroups a compute unit, or three if registers and LDS hold them and the last round
+  // of items is fuller for it (10240 x 8192, 640 items: 15.1 us against 17.1; but 14336 x
+  // 4096, 896 items: 11.1 against 10.3).
+  auto cost = [&](int64_t held) { return (items + held * cus - 1) / (held * cus) * held; };
+  const int64_t held = T == 1 && x_bytes <= 32 * 1024 && cost(3) < cost(2) ? 3 : 2;
+  return launch_kernel_lds(gemv_w4_kernel<E, G, T, W, P>,
+                           dim3((unsigned)std::min(items, held * cus)), dim3(64 * W), x_bytes,
+                           stream, x, x_stride, w4, sw, (int)M, (int)N, (int)K, (int)tiles,
+                           (int)items, y);
 }
 
 template <class E, int G, int NT, int T>
@@ -619,7 +644,8 @@ hipError_t gemv_any(const uint16_t* x, int64_t x_stride, const uint32_t* w4, con
                     hipStream_t stream) {
   if (few_rows(M, K)) {
     // two tiles an item halve the reads of x and the steps' overhead, one tile leaves the
-    // workgroups' shares more even
+    // workgroups' shares more even (57344 x 8192: 46.7 us against 50.0; 28672 x 8192: 29.2
+    // against 27.6)
     if (N / 16 >= 4 * 2 * device_cu_count())
       return gemv_launch<E, G, 2>(x, x_stride, w4, sw, M, N, K, y, stream);
     return gemv_launch<E, G, 1>(x, x_stride, w4, sw, M, N, K, y, stream);
