@@ -2,12 +2,12 @@
 // and step (gemv_w4, block_tables, kv_cache_write, tree_attention): the argument checks,
 // output allocation and C call of serve.py's functions without the interpreter between
 // them.  A step's smallest calls take 4 to 10 us on the GPU; checked in Python they took
-// 11 to 22 us of the host's time, here 4 to 8.
+// 11 to 22 us of the host's time, here 5 to 11.
 //
 // The C functions are those of the library that the package has loaded: bind() takes
-// their addresses.  Every other function takes all of its arguments by position (serve.py has the signatures and
-// their documentation), raises TypeError or ValueError before the C ABI sees a pointer,
-// and FlexqError for a status it returns.
+// their addresses.  Every other function takes all of its arguments by position (serve.py
+// has the signatures and their documentation), raises TypeError or ValueError before the C
+// ABI sees a pointer, and FlexqError for a status it returns.
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/hip/HIPFunctions.h>

@@ -57,7 +57,8 @@ __device__ __forceinline__ int find(const int* start, int n, int v) {
 // Every workgroup forms the prefix sums of all requests in LDS (at most 32 KB, from
 // L2), then takes its share of the new pages and of the slot map; a slot
 // on a new page reads the free list, not the table another workgroup may be writing, so
-// one launch does.
+// one launch does.  Bound by its latencies (launch, the lengths, the scan, the page looked up,
+// each after the other): 4.5 us for 16 requests, 9.3 for 512 prompts and 8.7 MB.
 template <int PER>
 __global__ __launch_bounds__(kScanThreads) void block_tables_kernel(
     const int* __restrict__ ctx_lens, const int* __restrict__ new_lens, int B,
@@ -156,7 +157,9 @@ __global__ __launch_bounds__(kScanThreads) void block_tables_kernel(
   }
 }
 
-// New keys and values into the cache, a copy bound by HBM (read and written once).
+// New keys and values into the cache, a copy bound by HBM (read and written once): prompts of
+// 180 MB take 36 to 37 us, 4.9 TB/s, what a plain copy reaches; the loads and stores are not
+// kept in the caches (43 us when they were).
 //
 // In the cache the keys of a token are 64-byte pieces and the values have the token
 // innermost, eight tokens of one d in 16 bytes (half a 16-token block).  So tokens whose
@@ -256,14 +259,16 @@ hipError_t launch_block_tables(const int32_t* ctx, const int32_t* add, int64_t B
                                int64_t max_tokens, int32_t* slots, int32_t* cu, int32_t* counts,
                                hipStream_t stream) {
   // One slot a thread while those threads fit the GPU twice over; then eight, which share
-  // the search and most page lookups.
+  // the search and most page lookups (16 requests of a token: 4.5 us against 7.0 with eight;
+  // 2.1 million slots: 9.3 against 13.9 with one).
   const int64_t most = 8 * device_cu_count();
   const int per = max_tokens <= most * kScanThreads / 4 ? 1 : 8;
   const int64_t work = std::max<int64_t>((max_tokens + per - 1) / per, B);
   const int64_t grid = std::min<int64_t>(work / kScanThreads + 1, most);
   const size_t lds = (size_t)(B + 1) * 2 * sizeof(int);
-  return launch_kernel_lds(per == 1 ? block_tables_kernel<1> : block_tables_kernel<8>, dim3((unsigned)grid), dim3(kScanThreads), lds,
-                           stream, ctx, add, (int)B, free_pages, (int)num_free, head,
+  auto* kernel = per == 1 ? block_tables_kernel<1> : block_tables_kernel<8>;
+  return launch_kernel_lds(kernel, dim3((unsigned)grid), dim3(kScanThreads), lds, stream, ctx,
+                           add, (int)B, free_pages, (int)num_free, head,
                            __builtin_ctz((unsigned)page_size), table, (int)max_blocks,
                            (int)max_tokens, slots, cu, counts);
 }
@@ -274,6 +279,7 @@ hipError_t launch_kv_cache_write(const uint16_t* k, int64_t k_st, int64_t k_sh,
                                  int64_t num_pages, int page_size, uint16_t* kc, uint16_t* vc,
                                  hipStream_t stream) {
   // sixteen tokens a workgroup where that is what it takes to have two for a compute unit
+  // (80 tokens: 4.8 us against 8.5 with 64; prompts: 40 us with 16 against 37 with 64)
   const int tokens = (T + 63) / 64 * Hkv >= 2 * device_cu_count() ? 64 : 16;
   const dim3 grid((unsigned)((T + tokens - 1) / tokens), (unsigned)Hkv);
   auto* kernel = tokens == 64 ? (D == 64    ? kv_cache_write_kernel<64, 64>
