@@ -90,6 +90,27 @@ def test_gemv_w4(fq, M, N, K, group, dtype):
     assert torch.equal(y, fq.gemv_w4(x.to(DEV), w4, sw, N))
 
 
+@pytest.mark.parametrize("M,N,K,group", [(40, 32816, 256, 128), (64, 32816, 384, 64),
+                                         (70, 32816, 384, 32), (3, 32816, 384, 32),
+                                         (2, 9616, 1152, 64), (4, 9616, 384, 128)])
+def test_gemv_w4_wide_weights(fq, M, N, K, group):
+    """Weights with more tiles than workgroups, odd numbers of them; one row is infinite."""
+    say("gemv_w4, wide", M, N, K, group)
+    r = rng(61, M, N, K, group)
+    q = r.integers(-7, 8, (N, K))
+    s = (r.random((N, K // group)) * 0.01).astype(np.float16)
+    x = normal(r, (M, K), F16)
+    x[M - 1, 37] = float("inf")
+    w4 = torch.from_numpy(ref.pack_w4(q).view(np.int32)).to(DEV)
+    y = fq.gemv_w4(x.to(DEV), w4, torch.from_numpy(np.ascontiguousarray(s.T)).to(DEV), N)
+    y = y.double().cpu().numpy()
+    want, sums = ref.gemv(x[:M - 1].double().numpy(), q, s, group)
+    assert (np.abs(y[:M - 1] - want) <= ref.gemv_tolerance(want, sums, F16)).all()
+    code = np.where(s[:, 37 // group] == 0, 0, q[:, 37])
+    assert np.array_equal(y[M - 1], np.where(code == 0, NAN, np.where(code > 0, np.inf, -np.inf)),
+                          equal_nan=True)
+
+
 def test_gemv_w4_strided_rows_guards_and_stream(fq):
     """Rows of a wider tensor, an output between guards, a stream of its own."""
     r = rng(3)
