@@ -1,0 +1,97 @@
+"""GPU numerics of tree_attention where one fp32 pass can lose them: the two 16-bit parts of
+a probability, small probabilities behind a large one, and infinite values of attended
+keys.  Bounds come from the definition (softmax in 64 bits) and from what the header says of
+the probabilities, not from how the kernel forms them.
+"""
+import numpy as np
+import pytest
+
+import serve_reference as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+DEV = "cuda:0"
+F16, BF16 = torch.float16, torch.bfloat16
+U = 2.0 ** -23
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def fq():
+    import w6a6_w6a8_integer_amd as fq
+    fq.lib()
+    return fq
+
+
+def i32(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)
+
+
+def cache_of(fq, keys, values, page):
+    """The paged cache of requests' keys and values [len][Hkv][D] (in page order), and its
+    block table."""
+    Hkv, D = keys[0].shape[1:]
+    need = [-(-k.shape[0] // page) for k in keys]
+    kc, vc = fq.kv_cache(sum(need), Hkv, D, page, keys[0].dtype, "cpu")
+    table = np.full((len(keys), max(need)), -1, np.int32)
+    h, d = np.arange(Hkv)[:, None], np.arange(D)
+    at = 0
+    for b, (k, v) in enumerate(zip(keys, values)):
+        table[b, :need[b]] = np.arange(at, at + need[b])
+        slot = at * page + np.arange(k.shape[0])[:, None, None]
+        ik, iv = ref.cache_index(slot, h, d, Hkv, D, page)
+        kc.view(-1)[torch.from_numpy(ik)] = k
+        vc.view(-1)[torch.from_numpy(iv)] = v
+        at += need[b]
+    return kc.to(DEV), vc.to(DEV), i32(table)
+
+
+def attend(fq, q, keys, values, new, page=16, scale=1.0, mask=None):
+    """(out, lse) of requests with new[b] drafted tokens each, in float64 on the CPU."""
+    kc, vc, table = cache_of(fq, keys, values, page)
+    ctx = [k.shape[0] - n for k, n in zip(keys, new)]
+    out, lse = fq.tree_attention(q.to(DEV), kc, vc, table, i32(ctx),
+                                 i32(np.concatenate(([0], np.cumsum(new)))), tree_mask=mask,
+                                 max_new=max(new), scale=scale, return_lse=True)
+    return out.double().cpu(), lse.double().cpu()
+
+
+@pytest.mark.parametrize("rows", [1, 5])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_parts_of_a_probability(fq, dtype, rows):
+    """Each probability as two 16-bit parts is within 2^-17 of itself.  One key of probability
+    p and value 1, a few of probability 1 whose values add up to p's first sixteen bits: what
+    is left of p has to be right to 2^-17 p (and the fp32 score, exponential and the three
+    sums of a handful of terms to 16 u).  The p are those whose bits from the seventeenth on
+    are nearly all ones.  With 16 rows a wave and, from 65 rows on, 32."""
+    a = torch.arange(1, 2816).to(torch.float64) / 512
+    a = a[a == a.to(dtype).double()]
+    p = torch.exp(-a)
+    unit = 2.0 ** (torch.floor(torch.log2(p)) - 15)
+    worst = torch.argsort(p / unit - torch.floor(p / unit), descending=True)[:24]
+    a, p, unit = a[worst], p[worst], unit[worst]
+    B, L, D, H = len(a), 32, 64, 16
+    keys, values = [], []
+    for i in range(B):
+        k, v = torch.zeros(L, 1, D, dtype=dtype), torch.zeros(L, 1, D, dtype=dtype)
+        k[3, 0, 0], v[3] = -a[i], 256
+        left = float(torch.floor(p[i] / unit[i]) * unit[i])
+        for j in (7, 8, 20):                  # to at most eight bits each, exact in both types
+            part = float(torch.tensor(left, dtype=torch.float64).to(BF16))
+            v[j], left = -256 * part, left - part
+        assert left == 0
+        keys.append(k), values.append(v)
+    # the last tokens are the drafted ones; their keys are zero, so a chain changes l only
+    q = torch.zeros(B * rows, H, D, dtype=dtype)
+    q[:, :, 0] = 1
+    out, _ = attend(fq, q, keys, values, [rows] * B)
+    for b in range(B):
+        for t in range(rows):
+            total = L - rows + t + float(p[b])
+            want = 256 * float(p[b] - torch.floor(p[b] / unit[b]) * unit[b]) / total
+            tol = (2.0 ** -17 + 16 * U) * 256 * float(p[b]) / total + ref.OUT_EPS[dtype] * want \
+                + ref.OUT_ABS[dtype]
+            err = (out[b * rows + t] - want).abs().max()
+            assert float(err) <= tol, (b, t, float(err) / tol)

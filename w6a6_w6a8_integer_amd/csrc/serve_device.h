@@ -50,13 +50,17 @@ struct Bfloat {
   static __device__ __forceinline__ float value(uint16_t h) {
     return __builtin_bit_cast(float, (uint32_t)h << 16);
   }
+  // Two fp32 values each as the sum of two parts, both rounded to nearest: within 2^-17 of the
+  // value and to either side of it.  (Cut to 16 bits instead they are up to 2^-15 too small,
+  // all to one side, which an average over many keys keeps.)
   static __device__ __forceinline__ u32x2 split(float x, float y) {
-    const uint32_t a = __builtin_bit_cast(uint32_t, x), b = __builtin_bit_cast(uint32_t, y);
-    const float ax = __builtin_bit_cast(float, a & 0xFFFF0000u);
-    const float by = __builtin_bit_cast(float, b & 0xFFFF0000u);
-    return u32x2{__builtin_amdgcn_perm(b, a, 0x07060302u),
-                 __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, y - by),
-                                       __builtin_bit_cast(uint32_t, x - ax), 0x07060302u)};
+    typedef float pair __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t h =
+        __builtin_bit_cast(uint32_t, __builtin_convertvector((pair{x, y}), bf16x2));
+    const pair left = {x - __builtin_bit_cast(float, h << 16),
+                       y - __builtin_bit_cast(float, h & 0xFFFF0000u)};
+    return u32x2{h, __builtin_bit_cast(uint32_t, __builtin_convertvector(left, bf16x2))};
   }
   static constexpr uint32_t kExponent = 0x7F80u;
 };
