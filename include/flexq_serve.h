@@ -141,7 +141,8 @@ flexq_status flexq_kv_cache_write(const uint16_t* k, int64_t k_stride_t, int64_t
      s_j = scale * (q . k_j);  out = sum_j softmax(s)_j v_j;  lse = ln sum_j exp(s_j)
    over the attended j; a row that attends nothing gives out = 0, lse = -inf.  Scores,
    statistics and sums are fp32; the probabilities enter the product with the values as
-   the sum of two 16-bit parts (at least 16 significant bits); out is rounded once.
+   the sum of two 16-bit parts, within 2^-17 of themselves or, for fp16, 2^-34 of the row's
+   largest, whichever is more; out is rounded once.
    What masked places, unused slots and pages hold does not matter, NaN and infinities
    included.  Tokens on a page outside [0, num_pages) are left out.
      q          element (t, h, d) at t * q_stride_t + h * q_stride_h + d, t < T

@@ -95,3 +95,36 @@ def test_parts_of_a_probability(fq, dtype, rows):
                 + ref.OUT_ABS[dtype]
             err = (out[b * rows + t] - want).abs().max()
             assert float(err) <= tol, (b, t, float(err) / tol)
+
+
+@pytest.mark.parametrize("nats", [6, 10, 12, 14, 17, 20])
+@pytest.mark.parametrize("L,new,H", [(256, 1, 4), (255, 9, 16), (4096, 2, 4)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_small_probabilities_behind_a_large_one(fq, dtype, L, new, H, nats):
+    """An early key far above all others, of value zero: the output is the others' alone.  The
+    header's bound holds for each probability: 2^-17 of itself, in fp16 or 2^-34 of the row's
+    largest, whichever is more.  All the other scores are alike (the errors of their
+    probabilities all have one sign), and spread over a nat."""
+    D = 64
+    for spread in (0.0, 1.0):
+        r = np.random.default_rng([L, new, nats, int(spread)])
+        k = torch.zeros(L, 1, D, dtype=dtype)
+        k[:, 0, 0] = torch.from_numpy(-nats - spread * r.random(L)).to(dtype)
+        k[2, 0, 0] = 0
+        v = torch.from_numpy(64 * r.random((L, 1, D)) + 32).to(dtype)
+        v[2] = 0
+        q = torch.zeros(new, H, D, dtype=dtype)
+        q[:, :, 0] = 1
+        out, lse = attend(fq, q, [k], [v], [new])
+        for t in range(new):
+            n = L - new + t + 1
+            s = k[:n, 0, 0].double()
+            p = torch.exp(s - s.max())
+            want = (p @ v[:n, 0].double()) / p.sum()
+            each = torch.maximum(2.0 ** -17 * p, torch.full_like(p, 2.0 ** -34)) \
+                if dtype is F16 else 2.0 ** -17 * p
+            tol = (each + (n / 32 + 96) * U * p) @ v[:n, 0].double() / p.sum()
+            tol = tol + ref.OUT_EPS[dtype] * want * (1 + 2.0 ** -7) + ref.OUT_ABS[dtype]
+            err = (out[t] - want).abs()
+            assert bool((err <= tol).all()), (spread, t, float((err / tol).max()))
+            assert float((lse[t] - p.sum().log() - s.max()).abs().max()) <= (n / 32 + 96) * U

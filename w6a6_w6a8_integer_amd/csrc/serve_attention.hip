@@ -1,8 +1,8 @@
 // serve_attention.hip -- attention of drafted tokens over the paged cache.
 //
 // For the rows of one request and key head (new tokens x query heads of the group), with
-// K and V of up to ctx + new tokens: S = scale K Q^T, P = 2^(S log2 e - m) with a running
-// maximum m per row, O = V^T P, l = sum P; out = O / l.  One pass over the cache.
+// K and V of up to ctx + new tokens: S = scale K Q^T, P = 2^(S log2 e - m + c) with a running
+// maximum m per row and a constant c, O = V^T P, l = sum P; out = O / l.  One pass over the cache.
 //
 // Both products are MFMAs with the rows as columns, so a lane owns one row's statistics: a
 // wave holds 16 rows (16x16x32) or, where there are many, 32 (32x32x16: half the
@@ -40,8 +40,6 @@ constexpr int units_per_cu(int64_t D, int rows) { return D > 64 ? 2 : rows == 16
 // (counting no start: 32 single tokens over 4k 64 us against 57; shares down to one step: a
 // single token over 37 10.1 us, as then there is a join, against 8.1).
 constexpr uint32_t kHead = 5, kMinShare = 8;
-// Probabilities are at most 2^kLag before the division (fp16 holds 2^15).
-constexpr float kLag = 8.0f;
 
 constexpr int kNonTemporal = 2;  // cache-policy bit of loads
 
@@ -369,9 +367,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
   // A negative scale goes into the queries' signs and a zero one into the queries, so that
   // the scores' order is the scaled ones'.  The reference m a row's probabilities are
   // taken against is kept unscaled and raised only where a score exceeds it by a factor of
-  // 2^kLag: l and O are in proportion to 2^-m whatever m is.
+  // 2^E::kLag: l and O are in proportion to 2^(E::kTop - m) whatever m is.
   const float scale = a.scale != 0.0f ? fabsf(a.scale) * kLog2e : 1.0f;
-  const float lag = fminf(kLag / scale, 3e38f);
+  const float lag = fminf(E::kLag / scale, 3e38f);
+  // what is added to a row's scaled scores (m = -inf: nothing attended yet)
+  auto reference = [&](float m) { return m == -INFINITY ? 0.0f : E::kTop - m * scale; };
   const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
   const uint32_t keep_q = a.scale != 0.0f ? 0xFFFFFFFFu : 0u;
 
@@ -540,7 +540,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
 #pragma unroll
           for (int i = 0; i < 4 * P::kQuads; ++i) o[t][i] *= by;
       }
-      const float ref = m == -INFINITY ? 0.0f : -m * scale;
+      const float ref = reference(m);
       u32x4 hi[P::kGroups], lo[P::kGroups];
 #pragma unroll
       for (int j = 0; j < P::kGroups; ++j)
@@ -593,7 +593,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
     }
 
     const float sum = row_sum<RW>(l);
-    const float top = m == -INFINITY ? m : m * scale;
+    const float top = m == -INFINITY ? m : -reference(m);
     if (row >= rows) continue;
 #pragma unroll
     for (int t = 0; t < P::kOuts; ++t)

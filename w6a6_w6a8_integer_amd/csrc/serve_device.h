@@ -26,13 +26,17 @@ struct Half {
   }
   static __device__ __forceinline__ uint16_t bits(float f) { return float_to_half_bits(f); }
   static __device__ __forceinline__ float value(uint16_t h) { return half_bits_to_float(h); }
-  // Two fp32 values in [0, 1] each as the sum of two halves: cut, then what was cut off
+  // Two fp32 values in [0, 2^15] each as the sum of two halves: cut, then what was cut off.  The
+  // sum is less than 2^-20 of the value, or 2^-24 (half's least step), below it.
   static __device__ __forceinline__ u32x2 split(float x, float y) {
     const auto h = __builtin_amdgcn_cvt_pkrtz(x, y);
     const auto l = __builtin_amdgcn_cvt_pkrtz(fmaf(-(float)h[0], 1.0f, x), fmaf(-(float)h[1], 1.0f, y));
     return u32x2{__builtin_bit_cast(uint32_t, h), __builtin_bit_cast(uint32_t, l)};
   }
   static constexpr uint32_t kExponent = 0x7C00u;  // all ones: infinity or NaN
+  // A row's largest probability is held as 2^kTop to 2^(kTop + kLag): half's range reaches no
+  // further up, and down to 2^-24, so that small ones keep their bits.
+  static constexpr float kTop = 11.0f, kLag = 4.0f;
 };
 
 struct Bfloat {
@@ -63,6 +67,7 @@ struct Bfloat {
     return u32x2{h, __builtin_bit_cast(uint32_t, __builtin_convertvector(left, bf16x2))};
   }
   static constexpr uint32_t kExponent = 0x7F80u;
+  static constexpr float kTop = 0.0f, kLag = 8.0f;  // (fp32's exponents: any will do)
 };
 
 }  // namespace flexq
