@@ -83,7 +83,11 @@ __device__ __forceinline__ void wait_vm() {
 // x, known to be the same in every lane (so that it and what follows from it is scalar)
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+// A barrier that the wave's own LDS accesses have come before: a stage may be overwritten behind
+// it.  Loads from memory stay in flight.
+__device__ __forceinline__ void barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 
 }  // namespace
 
