@@ -128,3 +128,63 @@ def test_small_probabilities_behind_a_large_one(fq, dtype, L, new, H, nats):
             err = (out[t] - want).abs()
             assert bool((err <= tol).all()), (spread, t, float((err / tol).max()))
             assert float((lse[t] - p.sum().log() - s.max()).abs().max()) <= (n / 32 + 96) * U
+
+
+@pytest.mark.parametrize("new,H,Hkv,D", [(1, 4, 2, 64), (3, 16, 1, 128), (9, 16, 1, 128),
+                                         (30, 4, 2, 96), (5, 8, 1, 256)])
+@pytest.mark.parametrize("ctx", [100, 1500])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_infinite_values_of_attended_keys(fq, dtype, ctx, new, H, Hkv, D):
+    """An infinite value of an attended key gives an infinity of its sign, wherever the key
+    lies and whatever its (positive) probability is; two of opposite signs, or a NaN, give
+    NaN; the other columns keep their results.  With a mask, a drafted key's value reaches
+    only the rows that attend it."""
+    r = np.random.default_rng([ctx, new, H, D])
+    L = ctx + new
+    k = torch.from_numpy(r.standard_normal((L, Hkv, D)).astype(np.float32)).to(dtype)
+    v = torch.from_numpy(r.standard_normal((L, Hkv, D)).astype(np.float32)).to(dtype)
+    q = torch.from_numpy(r.standard_normal((new, H, D)).astype(np.float32)).to(dtype)
+    k[5] = 4 * q[0, 0]                          # probabilities of all sizes
+    seen = np.tril(np.ones((new, new), bool))
+    for t in range(new):
+        seen[t, :t] &= r.random(t) < 0.5
+    words = torch.zeros(new, 1, dtype=torch.int64)
+    for t, j in zip(*np.nonzero(seen)):
+        words[t, 0] |= 1 << int(j)
+    mask = (words - (words >= 1 << 31) * (1 << 32)).to(torch.int32).to(DEV)
+    clean, clean_lse = attend(fq, q, [k], [v], [new], scale=D ** -0.5, mask=mask)
+    bad = [(5, 0, INF), (5, 1, -INF), (17, 2, INF), (40, 3, -INF), (64, 4, INF), (70, 5, -INF),
+           (33, 6, INF), (34, 6, INF), (20, 7, INF), (90, 7, -INF), (50, 8, NAN),
+           (ctx - 1, 9, INF), (0, 10, -INF), (ctx + new // 2, 11, INF), (ctx - 40, 12, INF)]
+    for key, col, value in bad:
+        v[key, :, col] = value
+    out, lse = attend(fq, q, [k], [v], [new], scale=D ** -0.5, mask=mask)
+    assert torch.equal(lse, clean_lse)
+    want = clean.clone()
+    for col in {c for _, c, _ in bad}:
+        for t in range(new):
+            hit = [x for key, c, x in bad if c == col and (key < ctx or seen[t, key - ctx])]
+            if hit:
+                want[t, :, col] = sum(hit)
+    assert torch.equal(out.nan_to_num(nan=7e9, posinf=8e9, neginf=9e9),
+                       want.nan_to_num(nan=7e9, posinf=8e9, neginf=9e9))
+
+
+@pytest.mark.parametrize("L", [96, 3000])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_infinite_values_far_below_the_maximum(fq, dtype, L):
+    """The same where the infinite value's key is 300 nats below the row's maximum, before and
+    after it: below fp32's range, and still a positive probability."""
+    k, v = torch.zeros(L, 1, 64, dtype=dtype), torch.ones(L, 1, 64, dtype=dtype)
+    q = torch.zeros(1, 2, 64, dtype=dtype)
+    q[:, :, 0] = 1
+    k[3, 0, 0], v[3, 0, 9] = -300, INF
+    k[L - 5, 0, 0], v[L - 5, 0, 10] = -300, -INF
+    if dtype is BF16:
+        v[5, 0, 11], k[5, 0, 0] = 1e38, -300    # finite, and no more than 1e38 e^-600
+    k[L // 2, 0, 0] = 300
+    k[:L // 2, 0, 0] -= 1
+    out, _ = attend(fq, q, [k], [v], [1])
+    assert bool((out[..., 9] == INF).all()) and bool((out[..., 10] == -INF).all())
+    keep = [c for c in range(64) if c not in (9, 10)]
+    assert bool((out[..., keep] == 1).all())

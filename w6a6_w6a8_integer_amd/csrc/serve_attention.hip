@@ -212,6 +212,11 @@ __device__ __forceinline__ Parts parts_of(const AttentionArgs& a, int shares, in
   return w;
 }
 
+// 2^n x for a whole n of any size: an infinite x stays.
+__device__ __forceinline__ float scaled(float x, float n) {
+  return __builtin_ldexpf(x, (int)fminf(fmaxf(n, -1e4f), 1e4f));
+}
+
 // 0xFFFF in each 16-bit half of v that is infinite or NaN.
 template <class E>
 __device__ __forceinline__ uint32_t not_finite(uint32_t v) {
@@ -349,6 +354,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
   constexpr int kStage = 4 * DT * 1024;  // bytes: 2 DT fragments of keys, 2 DT of values
   constexpr int kKeys = 8 * P::kGroups;  // scores a lane holds
   extern __shared__ __attribute__((aligned(1024))) char lds[];
+  int& again = *reinterpret_cast<int*>(lds + S * kStage);  // (behind the stages)
+  if (threadIdx.x == 0) again = 0;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -369,13 +376,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
   const Parts parts = parts_of(a, shares, a.max_new * group);
   const int per_page = 1 << (a.page_shift - 4);  // 16-token blocks of a page
   // A negative scale goes into the queries' signs and a zero one into the queries, so that
-  // the scores' order is the scaled ones'.  The reference m a row's probabilities are
-  // taken against is kept unscaled and raised only where a score exceeds it by a factor of
-  // 2^E::kLag: l and O are in proportion to 2^(E::kTop - m) whatever m is.
+  // the scores' order is the scaled ones'.  A row's reference m is a whole number, the
+  // scores' maximum rounded up, and raised only where a score exceeds it by E::kLag: l and O are
+  // in proportion to 2^(E::kTop - m) whatever m is, and change by powers of 2.
   const float scale = a.scale != 0.0f ? fabsf(a.scale) * kLog2e : 1.0f;
-  const float lag = fminf(E::kLag / scale, 3e38f);
   // what is added to a row's scaled scores (m = -inf: nothing attended yet)
-  auto reference = [&](float m) { return m == -INFINITY ? 0.0f : E::kTop - m * scale; };
+  auto reference = [&](float m) { return m == -INFINITY ? 0.0f : E::kTop - m; };
   const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
   const uint32_t keep_q = a.scale != 0.0f ? 0xFFFFFFFFu : 0u;
 
@@ -384,237 +390,253 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
   const int half = P::half(lane, wave);
   const uint16_t* src = (key_wave ? a.kc : a.vc) + P::offset(lane, wave);
 
-  for (; b < a.B && before < share_end; ++b) {
-    if (b - window.base >= 64) {
-      window.base = b;
-      window.mine = load_request(a, b + lane);
-    }
-    const Request r = window.at(b);
-    const uint32_t weight = r.weight();
-    if (weight == 0) continue;
-    const int cu = r.cu, n_new = r.n_new, ctx = r.ctx, len = r.len, steps = (int)r.steps();
-    // this share's steps of the request
-    const uint32_t first_step = before + kHead;
-    const int begin = share_begin > first_step ? (int)(share_begin - first_step) : 0;
-    const int own_end = min(steps, (int)(share_end - first_step));
-    before += weight;
-    if (own_end <= begin) continue;
-    const uint32_t s0 = plan.share_of(first_step), s1 = plan.share_of(first_step + steps - 1);
-    if (threadIdx.x == 0 && hk == 0 && block_row0 == 0 && share == s0)
-      parts.plan[b] = {(int)s0, (int)s1};
-    const int rows = n_new * group;
-    if (block_row0 >= rows) continue;
-    int end = own_end;
-    if (!a.mask) {  // a chain: nothing past the last row's token
-      const int last = min(block_row0 + kWaves * RW, rows) - 1;
-      end = min(end, (ctx + last / group + 32) >> 5);
-    }
-    // where the last waves have fewer rows, a compute unit's next workgroup turns them round
-    const int row0 = block_row0 + (id >> 8 & 1 ? kWaves - 1 - wave : wave) * RW;
-    const bool idle = row0 >= rows;  // a wave that only stages
+  // Once; and where some sum is not finite a second time, with infinite and NaN values taken
+  // out of every step and given to the rows that attend them.  (The first time they meet both
+  // parts of a probability, and where one is 0 an infinity makes NaN.)
+  const int first_b = b;
+  const uint32_t first_before = before;
+  for (bool careful = false;; careful = true) {
+    for (b = first_b, before = first_before; b < a.B && before < share_end; ++b) {
+      if ((uint32_t)(b - window.base) >= 64u) {
+        window.base = b;
+        window.mine = load_request(a, b + lane);
+      }
+      const Request r = window.at(b);
+      const uint32_t weight = r.weight();
+      if (weight == 0) continue;
+      const int cu = r.cu, n_new = r.n_new, ctx = r.ctx, len = r.len, steps = (int)r.steps();
+      // this share's steps of the request
+      const uint32_t first_step = before + kHead;
+      const int begin = share_begin > first_step ? (int)(share_begin - first_step) : 0;
+      const int own_end = min(steps, (int)(share_end - first_step));
+      before += weight;
+      if (own_end <= begin) continue;
+      const uint32_t s0 = plan.share_of(first_step), s1 = plan.share_of(first_step + steps - 1);
+      if (threadIdx.x == 0 && hk == 0 && block_row0 == 0 && share == s0)
+        parts.plan[b] = {(int)s0, (int)s1};
+      const int rows = n_new * group;
+      if (block_row0 >= rows) continue;
+      int end = own_end;
+      if (!a.mask) {  // a chain: nothing past the last row's token
+        const int last = min(block_row0 + kWaves * RW, rows) - 1;
+        end = min(end, (ctx + last / group + 32) >> 5);
+      }
+      // where the last waves have fewer rows, a compute unit's next workgroup turns them round
+      const int row0 = block_row0 + (id >> 8 & 1 ? kWaves - 1 - wave : wave) * RW;
+      const bool idle = row0 >= rows;  // a wave that only stages
 
-    const int row = row0 + c, tok = row / group;  // the lane's row, its token in the request
-    const int64_t tok_at = (int64_t)cu + tok;     // and that token's place in q
-    const bool in = row < rows && tok_at >= 0 && tok_at < a.T;
-    u32x4 qf[P::kSlices];
-    const uint16_t* q = a.q + tok_at * a.q_st + (int64_t)(hk * group + row % group) * a.q_sh;
+      const int row = row0 + c, tok = row / group;  // the lane's row, its token in the request
+      const int64_t tok_at = (int64_t)cu + tok;     // and that token's place in q
+      const bool in = row < rows && tok_at >= 0 && tok_at < a.T;
+      u32x4 qf[P::kSlices];
+      const uint16_t* q = a.q + tok_at * a.q_st + (int64_t)(hk * group + row % group) * a.q_sh;
 #pragma unroll
-    for (int i = 0; i < P::kSlices; ++i)
-      qf[i] = in ? *reinterpret_cast<const u32x4*>(q + P::slice(lane, i)) : u32x4{};
+      for (int i = 0; i < P::kSlices; ++i)
+        qf[i] = in ? *reinterpret_cast<const u32x4*>(q + P::slice(lane, i)) : u32x4{};
 
-    // Table entry of the 16 tokens at 32 step + 16 half (-1 past the request's tokens), and
-    // the 16-token block of the cache it stands for (-1 where there is none).
-    const scalar_ptr_t table = (scalar_ptr_t)(a.table + (int64_t)b * a.max_blocks);
-    auto page_of = [&](int step, int half) {
-      const int pos = min(step, end - 1) * 32 + half * 16;
-      return pos < len ? table[pos >> a.page_shift] : -1;
-    };
-    auto block_of = [&](int id, int step, int half) {
-      if ((unsigned)id >= (unsigned)a.num_pages) return -1;
-      return (id * a.Hkv + hk) * per_page + ((step * 2 + half) & (per_page - 1));
-    };
-    // Stages a step whose table entries are in id0, id1, and fetches the next step's.
-    // holes: bit 2 (step % 32) + half where there is no block.
-    int id0 = page_of(begin, 0), id1 = page_of(begin, 1);
-    uint64_t holes = 0;
-    auto stage = [&](int step) {
-      const int b0 = block_of(id0, step, 0), b1 = block_of(id1, step, 1);
-      const int at = 2 * (step & 31);
-      holes = (holes & ~(3ull << at)) | (uint64_t)((b0 < 0 ? 1 : 0) | (b1 < 0 ? 2 : 0)) << at;
-      const uint16_t* from = src + (int64_t)max(half ? b1 : b0, 0) * (16 * D);
-      char* to = lds + (step % S) * kStage + wave * (DT * 1024);
+      // Table entry of the 16 tokens at 32 step + 16 half (-1 past the request's tokens), and
+      // the 16-token block of the cache it stands for (-1 where there is none).
+      const scalar_ptr_t table = (scalar_ptr_t)(a.table + (int64_t)b * a.max_blocks);
+      auto page_of = [&](int step, int half) {
+        const int pos = min(step, end - 1) * 32 + half * 16;
+        return pos < len ? table[pos >> a.page_shift] : -1;
+      };
+      auto block_of = [&](int id, int step, int half) {
+        if ((unsigned)id >= (unsigned)a.num_pages) return -1;
+        return (id * a.Hkv + hk) * per_page + ((step * 2 + half) & (per_page - 1));
+      };
+      // Stages a step whose table entries are in id0, id1, and fetches the next step's.
+      // holes: bit 2 (step % 32) + half where there is no block.
+      int id0 = page_of(begin, 0), id1 = page_of(begin, 1);
+      uint64_t holes = 0;
+      auto stage = [&](int step) {
+        const int b0 = block_of(id0, step, 0), b1 = block_of(id1, step, 1);
+        const int at = 2 * (step & 31);
+        holes = (holes & ~(3ull << at)) | (uint64_t)((b0 < 0 ? 1 : 0) | (b1 < 0 ? 2 : 0)) << at;
+        const uint16_t* from = src + (int64_t)max(half ? b1 : b0, 0) * (16 * D);
+        char* to = lds + (step % S) * kStage + wave * (DT * 1024);
 #pragma unroll
-      for (int i = 0; i < DT; ++i)
-        __builtin_amdgcn_global_load_lds(
-            (global_ptr_t)(from + i * (key_wave ? 512 : P::kValueStep)),
-            (lds_ptr_t)(to + i * 1024), 16, 0, ONE ? kNonTemporal : 0);
-      id0 = page_of(step + 1, 0);
-      id1 = page_of(step + 1, 1);
-    };
+        for (int i = 0; i < DT; ++i)
+          __builtin_amdgcn_global_load_lds(
+              (global_ptr_t)(from + i * (key_wave ? 512 : P::kValueStep)),
+              (lds_ptr_t)(to + i * 1024), 16, 0, ONE ? kNonTemporal : 0);
+        id0 = page_of(step + 1, 0);
+        id1 = page_of(step + 1, 1);
+      };
 
-    typename P::Out o[P::kOuts] = {};
-    float m = -INFINITY, l = 0.0f;
+      typename P::Out o[P::kOuts] = {};
+      float m = -INFINITY, l = 0.0f;
 
-    barrier();  // the stages of the request before have been read
-    // S - 1 steps, the last again where there are fewer: with a fixed number of loads behind
-    // it the wait for q (before the loop, not in it) leaves them in flight.
+      barrier();  // the stages of the request before have been read
+      // S - 1 steps, the last again where there are fewer: with a fixed number of loads behind
+      // it the wait for q (before the loop, not in it) leaves them in flight.
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) stage(begin + i);
-    wait_vm<(S - 1) * DT>();
+      for (int i = 0; i < S - 1; ++i) stage(begin + i);
+      wait_vm<(S - 1) * DT>();
 #pragma unroll
-    for (int i = 0; i < P::kSlices; ++i) {
-      asm volatile("" : "+v"(qf[i]));
-      qf[i] = (qf[i] & keep_q) ^ flip;
-    }
-    for (int step = begin; step < end; ++step) {
-      if (end - step >= S - 1)
-        wait_vm<(S - 2) * DT>();
-      else
-        wait_vm<0>();
-      barrier();
-      if (step + S - 1 < end) stage(step + S - 1);
-      if (idle) continue;
-      const u32x4* kf = reinterpret_cast<const u32x4*>(lds + (step % S) * kStage);
-      const u32x4* vf = kf + 2 * DT * 64 + lane;
+      for (int i = 0; i < P::kSlices; ++i) {
+        asm volatile("" : "+v"(qf[i]));
+        qf[i] = (qf[i] & keep_q) ^ flip;
+      }
+      for (int step = begin; step < end; ++step) {
+        if (end - step >= S - 1)
+          wait_vm<(S - 2) * DT>();
+        else
+          wait_vm<0>();
+        barrier();
+        if (step + S - 1 < end) stage(step + S - 1);
+        if (idle) continue;
+        const u32x4* kf = reinterpret_cast<const u32x4*>(lds + (step % S) * kStage);
+        const u32x4* vf = kf + 2 * DT * 64 + lane;
 
-      // S = K Q^T; then the values' fragments are on their way while P is formed
-      float x[kKeys];
-      P::scores(kf, qf, x);
-      __builtin_amdgcn_sched_barrier(0);
-      u32x4 f[P::kValues];
+        // S = K Q^T; then the values' fragments are on their way while P is formed
+        float x[kKeys];
+        P::scores(kf, qf, x);
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 f[P::kValues];
 #pragma unroll
-      for (int i = 0; i < P::kValues; ++i) f[i] = vf[i * 64];
-      __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < P::kValues; ++i) f[i] = vf[i * 64];
+        __builtin_amdgcn_sched_barrier(0);
 
-      // Keys that are no context (drafted, or none at all) or on no page: the wave masks.
-      const uint32_t hole = (uint32_t)(holes >> (2 * (step & 31))) & 3u;
-      const bool masked = hole != 0 || step * 32 + 32 > ctx;
-      uint32_t seen[P::kGroups];   // attended keys among each eight of this lane's
-      uint32_t there[P::kGroups];  // keys that exist
-      bool poison = false;         // a value is infinite or NaN
-      if (masked) {
+        // Keys that are no context (drafted, or none at all) or on no page: the wave masks.
+        const uint32_t hole = (uint32_t)(holes >> (2 * (step & 31))) & 3u;
+        const bool masked = careful || hole != 0 || step * 32 + 32 > ctx;
+        uint32_t seen[P::kGroups];   // attended keys among each eight of this lane's
+        uint32_t there[P::kGroups];  // keys that exist
+        bool poison = false;         // a value is infinite or NaN
+        if (masked) {
 #pragma unroll
-        for (int j = 0; j < P::kGroups; ++j) {
-          const int key0 = P::key(lane, j);          // the group's first key in the step
-          const int j0 = step * 32 + key0 - ctx;     // its drafted index (may be negative)
-          there[j] = (hole >> (key0 >> 4)) & 1u ? 0u : low_bits(len - step * 32 - key0);
-          if (a.mask) {  // the context, then the tree's bits
-            seen[j] = low_bits(-j0);
-            if (j0 > -8 && in) {
-              const int32_t* words = a.mask + tok_at * a.mask_words;
-              const int w = j0 >> 5;
-              const uint32_t w0 = w >= 0 && w < a.mask_words ? (uint32_t)words[w] : 0u;
-              const uint32_t w1 = w + 1 < a.mask_words ? (uint32_t)words[w + 1] : 0u;
-              seen[j] |= (uint32_t)(((uint64_t)w1 << 32 | w0) >> (j0 & 31)) & 0xFFu;
+          for (int j = 0; j < P::kGroups; ++j) {
+            const int key0 = P::key(lane, j);          // the group's first key in the step
+            const int j0 = step * 32 + key0 - ctx;     // its drafted index (may be negative)
+            there[j] = (hole >> (key0 >> 4)) & 1u ? 0u : low_bits(len - step * 32 - key0);
+            if (a.mask) {  // the context, then the tree's bits
+              seen[j] = low_bits(-j0);
+              if (j0 > -8 && in) {
+                const int32_t* words = a.mask + tok_at * a.mask_words;
+                const int w = j0 >> 5;
+                const uint32_t w0 = w >= 0 && w < a.mask_words ? (uint32_t)words[w] : 0u;
+                const uint32_t w1 = w + 1 < a.mask_words ? (uint32_t)words[w + 1] : 0u;
+                seen[j] |= (uint32_t)(((uint64_t)w1 << 32 | w0) >> (j0 & 31)) & 0xFFu;
+              }
+            } else {  // a chain: the tokens up to the row's own
+              seen[j] = low_bits(tok + 1 - j0);
             }
-          } else {  // a chain: the tokens up to the row's own
-            seen[j] = low_bits(tok + 1 - j0);
+            seen[j] &= there[j];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (!((seen[j] >> e) & 1u)) x[8 * j + e] = -INFINITY;
           }
-          seen[j] &= there[j];
+          // values of keys that do not exist are zeroed, and infinite and NaN ones for now
+          bool bad = false;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (!((seen[j] >> e) & 1u)) x[8 * j + e] = -INFINITY;
-        }
-        // values of keys that do not exist are zeroed, and infinite and NaN ones for now
-        bool bad = false;
+          for (int i = 0; i < P::kValues; ++i)
 #pragma unroll
-        for (int i = 0; i < P::kValues; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t t = there[P::group(i)] >> (2 * k);
-            const uint32_t w = f[i][k] & ((t & 1u) * 0xFFFFu | (t >> 1 & 1u) * 0xFFFF0000u);
-            const uint32_t ex = not_finite<E>(w);
-            bad |= ex != 0;
-            f[i][k] = w & ~ex;
-          }
-        poison = __ballot(bad) != 0;
-      }
-
-      float top = x[0];
-#pragma unroll
-      for (int e = 1; e < kKeys; ++e) top = fmaxf(top, x[e]);
-      top = row_max<RW>(top);
-      if (__ballot(top > m + lag)) {  // rare after a request's first step
-        top = fmaxf(m, top);
-        const float by = __builtin_amdgcn_exp2f((m - (top == -INFINITY ? 0.0f : top)) * scale);
-        m = top;
-        l *= by;
-#pragma unroll
-        for (int t = 0; t < P::kOuts; ++t)
-#pragma unroll
-          for (int i = 0; i < 4 * P::kQuads; ++i) o[t][i] *= by;
-      }
-      const float ref = reference(m);
-      u32x4 hi[P::kGroups], lo[P::kGroups];
-#pragma unroll
-      for (int j = 0; j < P::kGroups; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v0 = __builtin_amdgcn_exp2f(fmaf(x[8 * j + 2 * i], scale, ref));
-          const float v1 = __builtin_amdgcn_exp2f(fmaf(x[8 * j + 2 * i + 1], scale, ref));
-          l += v0 + v1;
-          const u32x2 both = E::split(v0, v1);
-          hi[j][i] = both[0];
-          lo[j][i] = both[1];
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t t = there[P::group(i)] >> (2 * k);
+              const uint32_t w = f[i][k] & ((t & 1u) * 0xFFFFu | (t >> 1 & 1u) * 0xFFFF0000u);
+              const uint32_t ex = not_finite<E>(w);
+              bad |= ex != 0;
+              f[i][k] = w & ~ex;
+            }
+          poison = __ballot(bad) != 0;
         }
 
+        float top = x[0];
 #pragma unroll
-      for (int i = 0; i < P::kValues; ++i) {
-        auto& to = o[P::tile(i)];
-        to = P::mfma(f[i], hi[P::group(i)], to);
-      }
+        for (int e = 1; e < kKeys; ++e) top = fmaxf(top, x[e]);
+        top = row_max<RW>(top);
+        top *= scale;
+        if (__ballot(top > m + E::kLag)) {  // rare after a request's first step
+          top = fmaxf(m, ceilf(top));
+          const float by = m - (top == -INFINITY ? 0.0f : top);
+          m = top;
+          l = scaled(l, by);
 #pragma unroll
-      for (int i = 0; i < P::kValues; ++i) {
-        auto& to = o[P::tile(i)];
-        to = P::mfma(f[i], lo[P::group(i)], to);
-      }
-      if (!poison) continue;
-      // Infinite and NaN values reach only the rows that attend their keys: one key at a
-      // time, and a row that does not attend it keeps its sum.
+          for (int t = 0; t < P::kOuts; ++t)
+#pragma unroll
+            for (int i = 0; i < 4 * P::kQuads; ++i) o[t][i] = scaled(o[t][i], by);
+        }
+        const float ref = reference(m);
+        u32x4 hi[P::kGroups], lo[P::kGroups];
+#pragma unroll
+        for (int j = 0; j < P::kGroups; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float v0 = __builtin_amdgcn_exp2f(fmaf(x[8 * j + 2 * i], scale, ref));
+            const float v1 = __builtin_amdgcn_exp2f(fmaf(x[8 * j + 2 * i + 1], scale, ref));
+            l += v0 + v1;
+            const u32x2 both = E::split(v0, v1);
+            hi[j][i] = both[0];
+            lo[j][i] = both[1];
+          }
+
+#pragma unroll
+        for (int i = 0; i < P::kValues; ++i) {
+          auto& to = o[P::tile(i)];
+          to = P::mfma(f[i], hi[P::group(i)], to);
+        }
+#pragma unroll
+        for (int i = 0; i < P::kValues; ++i) {
+          auto& to = o[P::tile(i)];
+          to = P::mfma(f[i], lo[P::group(i)], to);
+        }
+        if (!poison) continue;
+        // Infinite and NaN values reach only the rows that attend their keys: one key at a
+        // time, and a row that does not attend it keeps its sum.
 #pragma unroll 1
-      for (int k = 0; k < 32; ++k) {
-        const int e = k & 7, from = P::lane_of(k, c);
+        for (int k = 0; k < 32; ++k) {
+          const int e = k & 7, from = P::lane_of(k, c);
 #pragma unroll
-        for (int j = 0; j < P::kGroups; ++j) {
-          if (P::group_of(k) != j) continue;
-          const bool mine = lane == from && ((there[j] >> e) & 1u);
-          const uint32_t pair = e < 4 ? (e < 2 ? hi[j][0] : hi[j][1])
-                                      : (e < 6 ? hi[j][2] : hi[j][3]);
-          const u32x4 one_p = {mine ? (pair >> (16 * (e & 1))) & 0xFFFFu : 0u, 0u, 0u, 0u};
-          const bool attends = (__shfl((int)seen[j], from) >> e) & 1;
+          for (int j = 0; j < P::kGroups; ++j) {
+            if (P::group_of(k) != j) continue;
+            const bool mine = lane == from && ((there[j] >> e) & 1u);
+            // (any attended key's probability is positive, also one too small for fp32)
+            const u32x4 one_p = {mine ? E::kOne : 0u, 0u, 0u, 0u};
+            const bool attends = (__shfl((int)seen[j], from) >> e) & 1;
 #pragma unroll
-          for (int i = 0; i < P::kValues; ++i) {
-            if (P::group(i) != j) continue;
-            const uint32_t v = mine ? reinterpret_cast<const uint16_t*>(vf + i * 64)[e] : 0u;
-            const u32x4 one_v = {v & not_finite<E>(v), 0u, 0u, 0u};
-            auto& to = o[P::tile(i)];
-            const auto with = P::mfma(one_v, one_p, to);
+            for (int i = 0; i < P::kValues; ++i) {
+              if (P::group(i) != j) continue;
+              const uint32_t v = mine ? reinterpret_cast<const uint16_t*>(vf + i * 64)[e] : 0u;
+              const u32x4 one_v = {v & not_finite<E>(v), 0u, 0u, 0u};
+              auto& to = o[P::tile(i)];
+              const auto with = P::mfma(one_v, one_p, to);
 #pragma unroll
-            for (int t = 0; t < 4 * P::kQuads; ++t) to[t] = attends ? with[t] : to[t];
+              for (int t = 0; t < 4 * P::kQuads; ++t) to[t] = attends ? with[t] : to[t];
+            }
           }
         }
       }
-    }
+      f32x4 finite = {};  // or NaN
+#pragma unroll
+      for (int t = 0; t < P::kOuts; ++t)
+#pragma unroll
+        for (int i = 0; i < 4 * P::kQuads; ++i)
+          finite[i & 3] = fmaf(o[t][i], 0.0f, finite[i & 3]);
+      if (__ballot(finite[0] + finite[1] + finite[2] + finite[3] != 0.0f)) again = 1;
 
-    const float sum = row_sum<RW>(l);
-    const float top = m == -INFINITY ? m : -reference(m);
-    if (row >= rows) continue;
+      const float sum = row_sum<RW>(l);
+      const float top = m == -INFINITY ? m : -reference(m);
+      if (row >= rows) continue;
 #pragma unroll
-    for (int t = 0; t < P::kOuts; ++t)
+      for (int t = 0; t < P::kOuts; ++t)
 #pragma unroll
-      for (int g = 0; g < P::kQuads; ++g) {
-        const int d4 = P::d4(lane, t, g);
-        const f32x4 v = {o[t][4 * g], o[t][4 * g + 1], o[t][4 * g + 2], o[t][4 * g + 3]};
-        if (s0 != s1) {
-          const int64_t place = 2 * (int64_t)share + (share == s0 ? 1 : 0);
-          const int64_t at = (place * a.Hkv + hk) * (a.max_new * group) + row;
-          parts.out[at * (D / 4) + d4] = v;
-          if (d4 == 0) parts.stat[at] = {top, sum};
-        } else if (in) {
-          write_row<E>(a, tok_at, hk * group + row % group, d4, v, top == -INFINITY ? 0.0f : top,
-                       sum);
+        for (int g = 0; g < P::kQuads; ++g) {
+          const int d4 = P::d4(lane, t, g);
+          const f32x4 v = {o[t][4 * g], o[t][4 * g + 1], o[t][4 * g + 2], o[t][4 * g + 3]};
+          if (s0 != s1) {
+            const int64_t place = 2 * (int64_t)share + (share == s0 ? 1 : 0);
+            const int64_t at = (place * a.Hkv + hk) * (a.max_new * group) + row;
+            parts.out[at * (D / 4) + d4] = v;
+            if (d4 == 0) parts.stat[at] = {top, sum};
+          } else if (in) {
+            write_row<E>(a, tok_at, hk * group + row % group, d4, v, top == -INFINITY ? 0.0f : top,
+                         sum);
+          }
         }
-      }
+    }
+    barrier();
+    if (careful || again == 0) break;
   }
 }
 
@@ -650,11 +672,11 @@ __global__ __launch_bounds__(256) void join_parts_kernel(const AttentionArgs a, 
     const float2 s = parts.stat[at];
     const f32x4 o = parts.out[at * (D / 4) + d4];
     const float to = fmaxf(top, s.x), ref = to == -INFINITY ? 0.0f : to;
-    const float old = __builtin_amdgcn_exp2f(top - ref), by = __builtin_amdgcn_exp2f(s.x - ref);
+    const float old = top - ref, by = s.x - ref;
     top = to;
-    total = fmaf(s.y, by, total * old);
+    total = scaled(s.y, by) + scaled(total, old);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = fmaf(o[k], by, acc[k] * old);
+    for (int k = 0; k < 4; ++k) acc[k] = scaled(o[k], by) + scaled(acc[k], old);
   }
   if constexpr (SLICES > 1) {
     sums[threadIdx.x] = acc;
@@ -669,10 +691,10 @@ __global__ __launch_bounds__(256) void join_parts_kernel(const AttentionArgs a, 
     for (int j = 0; j < SLICES; ++j) {
       const float2 s = stats[threadIdx.x + j * kLanes];
       const f32x4 o = sums[threadIdx.x + j * kLanes];
-      const float by = __builtin_amdgcn_exp2f(s.x - ref);
-      total = fmaf(s.y, by, total);
+      const float by = s.x - ref;
+      total += scaled(s.y, by);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[k] = fmaf(o[k], by, acc[k]);
+      for (int k = 0; k < 4; ++k) acc[k] += scaled(o[k], by);
     }
   }
   const int64_t t = (int64_t)request.cu + row / group;
@@ -718,7 +740,7 @@ hipError_t launch_rows(const AttentionArgs& a, hipStream_t stream) {
     if (p.rows == 32)
       kernel = one ? tree_attention_kernel<E, DT, 32, S, true>
                    : tree_attention_kernel<E, DT, 32, S, false>;
-  const hipError_t e = launch_kernel_lds(kernel, grid, dim3(64 * kWaves), S * 4 * DT * 1024,
+  const hipError_t e = launch_kernel_lds(kernel, grid, dim3(64 * kWaves), S * 4 * DT * 1024 + 16,
                                          stream, a, p.shares, p.row_blocks);
   if (e != hipSuccess || p.shares == 1) return e;
   // a row's parts number about shares / B: few are taken by one thread after the other

@@ -34,8 +34,9 @@ struct Half {
     return u32x2{__builtin_bit_cast(uint32_t, h), __builtin_bit_cast(uint32_t, l)};
   }
   static constexpr uint32_t kExponent = 0x7C00u;  // all ones: infinity or NaN
-  // A row's largest probability is held as 2^kTop to 2^(kTop + kLag): half's range reaches no
-  // further up, and down to 2^-24, so that small ones keep their bits.
+  static constexpr uint32_t kOne = 0x3C00u;
+  // A row's largest probability is held as 2^(kTop - 1) to 2^(kTop + kLag): half's range reaches
+  // no further up, and down to 2^-24, so that small ones keep their bits.
   static constexpr float kTop = 11.0f, kLag = 4.0f;
 };
 
@@ -67,6 +68,7 @@ struct Bfloat {
     return u32x2{h, __builtin_bit_cast(uint32_t, __builtin_convertvector(left, bf16x2))};
   }
   static constexpr uint32_t kExponent = 0x7F80u;
+  static constexpr uint32_t kOne = 0x3F80u;
   static constexpr float kTop = 0.0f, kLag = 8.0f;  // (fp32's exponents: any will do)
 };
 
