@@ -88,50 +88,63 @@ __global__ __launch_bounds__(256) void pack_w4_kernel(const uint16_t* __restrict
 // launch and one load after the other), more rows the LDS reads of x and the MFMAs (64 rows
 // of 57344 x 8192: 101 us, 600 TFLOP/s).
 //
-// A code u = q + 8 becomes a 16-bit float with its four bits as the top of the mantissa
-// of 16 + u = q + 24: two bit operations for two codes, and the sum over a group starts
-// from -24 sum x, which one more MFMA (a constant matrix) forms for all T tiles.  The
-// products are exact in fp32 and at most 31 |x|, so the sums lose up to three bits of
-// fp32 against those of q itself, far below the output's rounding.  With an infinite or NaN
-// activation, or near the top of the range, that difference is not a number where the
-// definition may be one; such a group is taken again with the codes' own values.
+// Eight codes as the MFMA's 16-bit floats of their own values, so that a sum errs in
+// proportion to what it adds: a large activation whose code is 0 adds 0, also where it is
+// infinite only NaN, as the definition has it.
 template <class E>
-struct Code;
+struct Codes;
+
+// u = q + 8 as the low mantissa bits of 1024 + u or, four bits further up, 1024 + 16 u; then one
+// packed add or fma: nine operations for eight codes.  The constants are held in registers so
+// that a pair's bits take one and-or.
 template <>
-struct Code<Half> {
-  static constexpr int kShift = 6;  // of u in the mantissa
-  static constexpr uint32_t kBase = 0x4C004C00u, kMinus24 = 0xCE00CE00u;
-};
-template <>
-struct Code<Bfloat> {
-  static constexpr int kShift = 3;
-  static constexpr uint32_t kBase = 0x41804180u, kMinus24 = 0xC1C0C1C0u;
+struct Codes<Half> {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  static constexpr float kScale = 1.0f;  // what the value is still to be multiplied by
+  uint32_t low = 0x000F000Fu, high = 0x00F000F0u, base = 0x64006400u;
+  __device__ __forceinline__ Codes() {
+    asm("" : "+s"(low));
+    asm("" : "+s"(high));
+    asm("" : "+v"(base));
+  }
+  __device__ __forceinline__ u32x4 operator()(uint32_t d) const {
+    const f16x2 minus1032 = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+    const f16x2 by = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const f16x2 minus72 = {(_Float16)-72.0f, (_Float16)-72.0f};
+    u32x4 a;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t bits = ((i < 2 ? d : d >> 8) & (i % 2 ? high : low)) | base;
+      const f16x2 v = __builtin_bit_cast(f16x2, bits);
+      a[i] = __builtin_bit_cast(
+          uint32_t, i % 2 ? __builtin_elementwise_fma(v, by, minus72) : v + minus1032);
+    }
+    return a;
+  }
 };
 
-// Eight codes as q + 24.  mask and base are Code<E>'s, held in a scalar and a vector
-// register so that each pair is a shift and one and-or (a literal apiece would not fit).
-template <class E>
-__device__ __forceinline__ u32x4 codes_plus_24(uint32_t d, uint32_t mask, uint32_t base) {
-  u32x4 a;
+// Two's complement codes (q + 8 with the top bit turned) go through the conversion that makes
+// q / 16 of four bits; packing two is exact.  Fourteen operations for eight codes.
+template <>
+struct Codes<Bfloat> {
+  static constexpr float kScale = 16.0f;
+  __device__ __forceinline__ u32x4 operator()(uint32_t d) const {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t even = d ^ 0x88888888u;
+    uint32_t odd = even >> 4;  // codes in the low halves of the bytes, which the
+    asm("" : "+v"(odd));       // conversion can take by itself
+    u32x4 a;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int up = Code<E>::kShift - 4 * i;
-    a[i] = ((up >= 0 ? d << up : d >> -up) & mask) | base;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t from = i % 2 ? odd : even;
+      const f32x2 v = {__builtin_amdgcn_cvt_off_f32_i4((int)((from >> (8 * (i / 2))) & 255u)),
+                       __builtin_amdgcn_cvt_off_f32_i4((int)((from >> (8 * (i / 2) + 16)) & 255u))};
+      a[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    }
+    return a;
   }
-  return a;
-}
-
-// eight codes as q
-template <class E>
-__device__ __forceinline__ u32x4 codes(uint32_t d) {
-  u32x4 a;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int lo = (int)((d >> (4 * i)) & 15u) - 8, hi = (int)((d >> (4 * i + 16)) & 15u) - 8;
-    a[i] = E::bits((float)lo) | (uint32_t)E::bits((float)hi) << 16;
-  }
-  return a;
-}
+};
 
 // acc += scale * dot, four consecutive weight rows
 __device__ __forceinline__ void scale_add(f32x4& acc, f32x4 dot, u32x2 scales) {
@@ -158,39 +171,12 @@ __device__ __forceinline__ u32x2 group_scales(u32x2 s, int g) {
   }
 }
 
-__device__ __forceinline__ bool not_finite(f32x4 v) {
-  return fmaf(v[0], 0.0f, v[1] * 0.0f) + fmaf(v[2], 0.0f, v[3] * 0.0f) != 0.0f;
-}
-
 template <class E>
 __device__ __forceinline__ void store_four(uint16_t* to, f32x4 v) {
   u32x2 o;
   o[0] = E::bits(v[0]) | (uint32_t)E::bits(v[1]) << 16;
   o[1] = E::bits(v[2]) | (uint32_t)E::bits(v[3]) << 16;
   *reinterpret_cast<u32x2*>(to) = o;
-}
-
-// acc[n] += k-block kb of a tile with the codes' own values, straight from memory
-template <class E, int G, int NT>
-__device__ __forceinline__ void exact_block(f32x4* acc, const uint32_t* w4, const uint16_t* sw,
-                                            const uint16_t* x, int64_t x_stride, int rows, int N,
-                                            int kbs, int tile, int kb) {
-  const int lane = threadIdx.x & 63, c = lane & 15, p = lane >> 4;
-  const u32x4 w = reinterpret_cast<const u32x4*>(w4)[((int64_t)tile * kbs + kb) * 64 + lane];
-#pragma unroll
-  for (int g = 0; g < 128 / G; ++g) {
-    const u32x2 scales = *reinterpret_cast<const u32x2*>(
-        sw + (int64_t)(kb * (128 / G) + g) * N + tile * 16 + 4 * p);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint16_t* row = x + (int64_t)min(n * 16 + c, rows - 1) * x_stride + kb * 128 + p * 8;
-      f32x4 dot = {};
-#pragma unroll
-      for (int j = g * (G / 32); j < (g + 1) * (G / 32); ++j)
-        dot = E::mfma(codes<E>(w[j]), *reinterpret_cast<const u32x4*>(row + j * 32), dot);
-      scale_add(acc[n], dot, scales);
-    }
-  }
 }
 
 // Up to four rows.  An item is T adjacent 16-row tiles of the weight; a persistent
@@ -215,7 +201,6 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
   constexpr int kSteps = G / 32;    // MFMAs of a group
   extern __shared__ __attribute__((aligned(16))) uint16_t lds_x[];
   __shared__ f32x4 part[2][W][T][64];
-  __shared__ int again;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, p = lane >> 4;
@@ -258,37 +243,31 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
     }
   };
 
-  uint32_t mask = 0x000F000Fu << Code<E>::kShift, base = Code<E>::kBase;
-  asm("" : "+s"(mask));
-  asm("" : "+v"(base));
-  const uint32_t m24 = Code<E>::kMinus24;
-  const u32x4 minus24 = {m24, m24, m24, m24};
+  const Codes<E> codes;
   const uint16_t* lds_row = lds_x + min(c, M - 1) * (K + 32) + p * 8;
+  const uint16_t* lds_zeros = lds_x + M * (K + 32) + p * 8;
 
   f32x4 acc[T] = {};
   auto work = [&](const Slot& r, int round) {
-    // past K the scales are zero, and any activations will do that are a row's
-    const uint16_t* at = lds_row + min(round * W + wave, kbs - 1) * 128;
+    const int kb_now = round * W + wave;  // past K zeros: other activations may be infinite
+    const uint16_t* at = kb_now < kbs ? lds_row + kb_now * 128 : lds_zeros;
     u32x4 xf[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) xf[j] = *reinterpret_cast<const u32x4*>(at + j * 32);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      f32x4 start = {};
-#pragma unroll
-      for (int j = g * kSteps; j < (g + 1) * kSteps; ++j) start = E::mfma(minus24, xf[j], start);
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        f32x4 dot = start;
+        f32x4 dot = {};
 #pragma unroll
         for (int j = g * kSteps; j < (g + 1) * kSteps; ++j)
-          dot = E::mfma(codes_plus_24<E>(r.w[t][j], mask, base), xf[j], dot);
+          dot = E::mfma(codes(r.w[t][j]), xf[j], dot);
         scale_add(acc[t], dot, group_scales<kGroups>(r.s[t], g));
       }
     }
   };
 
-  // the waves' sums, in order; a sum that is not finite is formed again at the end
+  // the waves' sums, in order
   auto finish = [&](int item) {
     f32x4(*to)[T][64] = part[item & 1];
 #pragma unroll
@@ -306,20 +285,18 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[k] += o[k];
       }
-      if (c < M) {
-        if (not_finite(s)) again = 1;
-        store_four<E>(y + (int64_t)c * N + tile * 16 + 4 * p, s);
-      }
+      if (c < M)
+        store_four<E>(y + (int64_t)c * N + tile * 16 + 4 * p, s * Codes<E>::kScale);
     }
   };
 
-  if (threadIdx.x == 0) again = 0;
   const int pieces = K / 8;  // 16 bytes each
   for (int i = threadIdx.x; i < M * pieces; i += 64 * W) {
     const int row = i / pieces, k8 = i % pieces;
     *reinterpret_cast<u32x4*>(lds_x + row * (K + 32) + k8 * 8) =
         *reinterpret_cast<const u32x4*>(x + row * x_stride + k8 * 8);
   }
+  if (threadIdx.x < 16) *reinterpret_cast<u32x4*>(lds_x + M * (K + 32) + threadIdx.x * 8) = u32x4{};
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     next_load(ring[i]);
@@ -342,20 +319,6 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
         ++item;
       }
     }
-  }
-
-  lds_barrier();
-  if (again == 0) return;
-  // Rare: the codes' own values, a k-block at a time.
-  for (item = first; item < last; ++item) {
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      acc[t] = f32x4{};  // the steps past the run left something here
-      const int tile = min(item * T + t, tiles - 1);
-      for (kb = wave; kb < kbs; kb += W)
-        exact_block<E, G, 1>(&acc[t], w4, sw, x, x_stride, M, N, kbs, tile, kb);
-    }
-    finish(item);
   }
 }
 
@@ -446,11 +409,7 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
     }
   };
 
-  uint32_t mask = 0x000F000Fu << Code<E>::kShift, base = Code<E>::kBase;
-  asm("" : "+s"(mask));
-  asm("" : "+v"(base));
-  const uint32_t m24 = Code<E>::kMinus24;
-  const u32x4 minus24 = {m24, m24, m24, m24};
+  const Codes<E> codes;
   const int row8 = c & 7, h = c >> 3;
   const int frag_row = h * 1024 + ((row8 ^ h) * 8) * 16;
   f32x4 acc[T][NT] = {};
@@ -460,7 +419,7 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
     for (int i = 0; i < kChunk; ++i) {
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        f32x4 start[NT] = {}, dot[T][NT] = {};
+        f32x4 dot[T][NT] = {};
 #pragma unroll
         for (int j = g * kSteps; j < (g + 1) * kSteps; ++j) {
           u32x4 xf[NT];
@@ -470,10 +429,8 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
                 from + ((i * 2 + (j >> 1)) * kBlocks + 2 * n) * 1024 + frag_row +
                 ((((j & 1) * 4 + p) ^ row8) * 16));
 #pragma unroll
-          for (int n = 0; n < NT; ++n) start[n] = E::mfma(minus24, xf[n], start[n]);
-#pragma unroll
           for (int t = 0; t < T; ++t) {
-            const u32x4 a = codes_plus_24<E>(r.w[i][t][j], mask, base);
+            const u32x4 a = codes(r.w[i][t][j]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) dot[t][n] = E::mfma(a, xf[n], dot[t][n]);
           }
@@ -482,11 +439,7 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
         for (int t = 0; t < T; ++t) {
           const u32x2 scales = group_scales<kGroups>(r.s[i][t], g);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) dot[t][n][k] += start[n][k];
-            scale_add(acc[t][n], dot[t][n], scales);
-          }
+          for (int n = 0; n < NT; ++n) scale_add(acc[t][n], dot[t][n], scales);
         }
       }
     }
@@ -518,22 +471,10 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
     }
   }
 
-  bool bad = false;
-#pragma unroll
-  for (int t = 0; t < T; ++t)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) bad |= not_finite(acc[t][n]);
-  const bool again = __ballot(bad) != 0;
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     const int tile = tile0 + t;
     if (tile >= tiles) continue;
-    if (again) {  // rare: the codes' own values
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[t][n] = f32x4{};
-      for (int kb = first * kChunk; kb < min(last * kChunk, kbs); ++kb)
-        exact_block<E, G, NT>(acc[t], w4, sw, x0, x_stride, rows, N, kbs, tile, kb);
-    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (n * 16 + c >= rows) continue;
@@ -541,7 +482,7 @@ __global__ __launch_bounds__(512, NT <= 2 ? 4 : 2) void gemm_w4_kernel(
       if (slices > 1)
         *reinterpret_cast<f32x4*>(part + (int64_t)slice * M * N + at) = acc[t][n];
       else
-        store_four<E>(y + at, acc[t][n]);
+        store_four<E>(y + at, acc[t][n] * Codes<E>::kScale);
     }
   }
 }
@@ -564,7 +505,7 @@ __global__ __launch_bounds__(256) void join_slices_kernel(const float* __restric
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[k] += o[v][k];
   }
-  store_four<E>(y + 4 * i, s);
+  store_four<E>(y + 4 * i, s * Codes<E>::kScale);
 }
 
 namespace {
@@ -582,7 +523,8 @@ hipError_t pack_any(const uint16_t* w, int64_t N, int64_t K, int group, uint32_t
 // The few-rows kernel: two workgroups' activations and sums fit a compute unit's LDS.
 // One row of 4096 x 4096 takes 5.0 us with it and 7.2 with the other, of 57344 x 8192 45 and
 // 51; four of 5120 x 5120 (groups of 32) 10.9 and 10.2.
-bool few_rows(int64_t M, int64_t K) { return M <= 4 && M * (K + 32) * 2 <= 48 * 1024; }
+int64_t x_lds_bytes(int64_t M, int64_t K) { return (M * (K + 32) + 128) * 2; }
+bool few_rows(int64_t M, int64_t K) { return M <= 4 && x_lds_bytes(M, K) <= 48 * 1024; }
 
 // The other one: tiles a wave, and slices of K that give every compute unit a workgroup.
 // Twice the slices only add sums to join (13 x 5120 x 13824: 17.9 us against 16.2; 64 x 8192 x
@@ -612,7 +554,7 @@ hipError_t gemv_launch(const uint16_t* x, int64_t x_stride, const uint32_t* w4,
                        hipStream_t stream) {
   constexpr int W = 8, P = 4;
   const int64_t tiles = N / 16, items = (tiles + T - 1) / T, cus = device_cu_count();
-  const int64_t x_bytes = M * (K + 32) * 2;
+  const int64_t x_bytes = x_lds_bytes(M, K);
   // Two workgroups a compute unit, or three if registers and LDS hold them and the last round
   // of items is fuller for it (10240 x 8192, 640 items: 15.1 us against 17.1; but 14336 x
   // 4096, 896 items: 11.1 against 10.3).
