@@ -80,9 +80,6 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
 
-// x, known to be the same in every lane (so that it and what follows from it is scalar)
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
 // A barrier that the wave's own LDS accesses have come before: a stage may be overwritten behind
 // it.  Loads from memory stay in flight.
 __device__ __forceinline__ void barrier() {
@@ -734,12 +731,13 @@ hipError_t launch_rows(const AttentionArgs& a, hipStream_t stream) {
   const int64_t units = (int64_t)p.shares * a.Hkv;
   const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.row_blocks));
   const bool one = p.row_blocks == 1;
-  auto* kernel = one ? tree_attention_kernel<E, DT, 16, S, true>
-                     : tree_attention_kernel<E, DT, 16, S, false>;
-  if constexpr (DT <= 4)
-    if (p.rows == 32)
-      kernel = one ? tree_attention_kernel<E, DT, 32, S, true>
-                   : tree_attention_kernel<E, DT, 32, S, false>;
+  auto* kernel = tree_attention_kernel<E, DT, 16, S, true>;
+  if constexpr (DT > 4) {
+    if (!one) kernel = tree_attention_kernel<E, DT, 16, S, false>;
+  } else if (p.rows == 32) {  // (16 rows a wave are one row block)
+    kernel = one ? tree_attention_kernel<E, DT, 32, S, true>
+                 : tree_attention_kernel<E, DT, 32, S, false>;
+  }
   const hipError_t e = launch_kernel_lds(kernel, grid, dim3(64 * kWaves), S * 4 * DT * 1024 + 16,
                                          stream, a, p.shares, p.row_blocks);
   if (e != hipSuccess || p.shares == 1) return e;
