@@ -32,8 +32,7 @@
  *             + (d / 32) * 512 + (r % 16) * 32 + d % 32
  *   values  the same block offset + d * 16 + r % 16
  * (keys in 32-wide slices of D, values with the token innermost: each is the order an
- * MFMA fragment takes, so the attention reads whole cache lines straight into
- * registers).  As torch tensors: keys [pages][Hkv][page_size/16][D/32][16][32], values
+ * MFMA fragment takes, so the attention stages whole cache lines in LDS as they are).  As torch tensors: keys [pages][Hkv][page_size/16][D/32][16][32], values
  * [pages][Hkv][page_size/16][D][16].  D is 64, 96, 128 or 256.
  * block_table[b][i] is the page of request b's tokens i * page_size ...
  */
