@@ -3,6 +3,7 @@ and _serve.so, the Python binding of the decoding-step calls, with the host comp
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -37,13 +38,26 @@ FLAGS = [
 BINDING = os.path.join(PKG, "_serve.so")
 
 
-def binding_command(out: str) -> list[str]:
-    import torch
-    from torch.utils import cpp_extension
+class NoBinding(Exception):
+    """What the binding needs and this host lacks."""
 
+
+def binding_command(out: str) -> list[str]:
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError as e:
+        raise NoBinding(f"torch cannot be imported ({e})") from e
+
+    cxx = os.environ.get("CXX", "g++")
+    if shutil.which(cxx) is None:
+        raise NoBinding(f"there is no host compiler {cxx}")
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     include = [*cpp_extension.include_paths("cuda"), sysconfig.get_paths()["include"]]
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    for header in ("torch/csrc/autograd/python_variable.h", "c10/hip/HIPStream.h", "Python.h"):
+        if not any(os.path.exists(os.path.join(p, header)) for p in include):
+            raise NoBinding(f"there is no {header}")
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
             # what torch's own headers ask for on ROCm
             "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -53,13 +67,21 @@ def binding_command(out: str) -> list[str]:
 
 
 def build(verbose: bool = False, jobs: int | None = None) -> str:
+    """Builds both.  The library needs hipcc alone: where the host lacks what the binding
+    needs, it is left out (the calls that need it say so), and where the binding does not
+    compile, the library is there before the error is raised."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs, procs = [], []
-    cmd = binding_command(BINDING + ".tmp")
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    procs.append(("serve_binding.cpp",
-                  subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    try:
+        cmd = binding_command(BINDING + ".tmp")
+    except NoBinding as e:
+        binding = None
+        print(f"{os.path.basename(BINDING)} is not built: {e}", file=sys.stderr)
+    else:
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        binding = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        procs.append(("serve_binding.cpp", binding))
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
         cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -77,15 +99,20 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
             print(f"[{src}]\n" + "\n".join(lines), file=sys.stderr)
         if p.returncode:
             failed.append(src)
-    if failed:
+    if set(failed) - {"serve_binding.cpp"}:
         raise RuntimeError(f"the compiler failed for {failed}")
-    os.replace(BINDING + ".tmp", BINDING)
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
+    if os.path.exists(BINDING):
+        os.remove(BINDING)  # none is left that was built for another library
     os.replace(tmp, LIB)
+    if failed:
+        raise RuntimeError(f"the compiler failed for {failed}; {LIB} is built")
+    if binding is not None:
+        os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 
