@@ -51,36 +51,37 @@ __device__ __forceinline__ int64_t w4_dword(int64_t n, int kb, int j, int p, int
 }  // namespace
 
 // One thread = 8 consecutive codes (one dword); the G / 8 threads of a group are adjacent
-// lanes.  blockIdx.x = row, blockIdx.y = chunk of 2048 columns.
+// lanes.  blockIdx.x = row (and those gridDim.x apart), blockIdx.y = chunk of 2048 columns.
 template <class E, int G>
 __global__ __launch_bounds__(256) void pack_w4_kernel(const uint16_t* __restrict__ w, int N,
                                                       int K, uint32_t* __restrict__ w4,
                                                       uint16_t* __restrict__ sw) {
-  const int64_t n = blockIdx.x;
   const int k0 = (blockIdx.y * 256 + threadIdx.x) * 8;
   if (k0 >= K) return;  // whole 16-lane rows drop out together (K % 128 == 0)
-  const u32x4 h = *reinterpret_cast<const u32x4*>(w + n * K + k0);
-  float v[8];
-  float amax = 0.0f;
+  for (int64_t n = blockIdx.x; n < N; n += gridDim.x) {
+    const u32x4 h = *reinterpret_cast<const u32x4*>(w + n * K + k0);
+    float v[8];
+    float amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = E::value((uint16_t)(h[i] & 0xFFFFu));
-    v[2 * i + 1] = E::value((uint16_t)(h[i] >> 16));
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = E::value((uint16_t)(h[i] & 0xFFFFu));
+      v[2 * i + 1] = E::value((uint16_t)(h[i] >> 16));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+    for (int o = 1; o < G / 8; o *= 2) amax = fmaxf(amax, __shfl_xor(amax, o));
+    const uint16_t s16 = float_to_half_bits(amax / 7.0f);
+    const float s = half_bits_to_float(s16);
+    uint32_t d = 0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float r = s != 0.0f ? fminf(fmaxf(rintf(v[c] / s), -7.0f), 7.0f) : 0.0f;
+      d |= (uint32_t)((int)r + 8) << (4 * (c >> 1) + 16 * (c & 1));
+    }
+    w4[w4_dword(n, k0 >> 7, (k0 >> 5) & 3, (k0 >> 3) & 3, K >> 7)] = d;
+    if ((k0 & (G - 1)) == 0) sw[(int64_t)(k0 / G) * N + n] = s16;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-#pragma unroll
-  for (int o = 1; o < G / 8; o *= 2) amax = fmaxf(amax, __shfl_xor(amax, o));
-  const uint16_t s16 = float_to_half_bits(amax / 7.0f);
-  const float s = half_bits_to_float(s16);
-  uint32_t d = 0;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const float r = s != 0.0f ? fminf(fmaxf(rintf(v[c] / s), -7.0f), 7.0f) : 0.0f;
-    d |= (uint32_t)((int)r + 8) << (4 * (c >> 1) + 16 * (c & 1));
-  }
-  w4[w4_dword(n, k0 >> 7, (k0 >> 5) & 3, (k0 >> 3) & 3, K >> 7)] = d;
-  if ((k0 & (G - 1)) == 0) sw[(int64_t)(k0 / G) * N + n] = s16;
 }
 
 // Both kernels below are bound by HBM (0.5 byte a weight) where the weight is large: one row
@@ -513,7 +514,8 @@ namespace {
 template <class E>
 hipError_t pack_any(const uint16_t* w, int64_t N, int64_t K, int group, uint32_t* w4,
                     uint16_t* sw, hipStream_t stream) {
-  const dim3 grid((unsigned)N, (unsigned)((K + 2047) / 2048));
+  // (a launch holds fewer than 2^32 threads in a direction)
+  const dim3 grid((unsigned)std::min<int64_t>(N, 1 << 23), (unsigned)((K + 2047) / 2048));
   auto* kernel = group == 32   ? pack_w4_kernel<E, 32>
                  : group == 64 ? pack_w4_kernel<E, 64>
                                : pack_w4_kernel<E, 128>;
