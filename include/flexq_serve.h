@@ -32,7 +32,8 @@
  *             + (d / 32) * 512 + (r % 16) * 32 + d % 32
  *   values  the same block offset + d * 16 + r % 16
  * (keys in 32-wide slices of D, values with the token innermost: each is the order an
- * MFMA fragment takes, so the attention stages whole cache lines in LDS as they are).  As torch tensors: keys [pages][Hkv][page_size/16][D/32][16][32], values
+ * MFMA fragment takes, so the attention stages whole cache lines in LDS as they are).
+ * As torch tensors: keys [pages][Hkv][page_size/16][D/32][16][32], values
  * [pages][Hkv][page_size/16][D][16].  D is 64, 96, 128 or 256.
  * block_table[b][i] is the page of request b's tokens i * page_size ...
  */
@@ -120,7 +121,8 @@ flexq_status flexq_block_tables(const int32_t* ctx_lens, const int32_t* new_lens
    a slot outside [0, num_pages * page_size) (such as -1) drops the token.  Two tokens
    with one slot leave either's value.  A copy of 16-bit elements of either dtype.
      k, v      element (t, h, d) at t * stride_t + h * stride_h + d (strides in
-               elements, the tensors' own), 16-byte aligned rows
+               elements, the tensors' own; that of an axis of length one plays no
+               part), 16-byte aligned rows
      slot_map  int32[T]      k_cache, v_cache  the layouts above, 16-byte aligned
    T == 0 is a no-op.  Errors: INVALID_VALUE (null, negative size, negative stride, a
    cache overlapping another argument), UNSUPPORTED (D, page_size, strides % 8, Hkv >
@@ -144,7 +146,8 @@ flexq_status flexq_kv_cache_write(const uint16_t* k, int64_t k_stride_t, int64_t
    largest, whichever is more; out is rounded once.
    What masked places, unused slots and pages hold does not matter, NaN and infinities
    included; an infinite value of an attended key gives an infinity of its sign.  Tokens on a page outside [0, num_pages) are left out.
-     q          element (t, h, d) at t * q_stride_t + h * q_stride_h + d, t < T
+     q          element (t, h, d) at t * q_stride_t + h * q_stride_h + d, t < T (the
+                stride of an axis of length one plays no part)
      tree_mask  int32[T][mask_words] or NULL; bits past mask_words are 0
      out        [T][H][D] of dtype, 16-byte aligned     lse  fp32[T][H] or NULL
      max_new    no request has more drafted tokens (further ones are not computed)

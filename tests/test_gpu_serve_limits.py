@@ -40,6 +40,34 @@ def gather(cache_k, cache_v, slots, page):
     return k.reshape(len(s), cache_k.shape[1], -1), cache_v[at, :, block, :, r]
 
 
+def test_strides_of_axes_of_length_one(fq):
+    """A single token, and a single head, from a tensor whose rows are no multiple of eight
+    elements apart: the stride of an axis of length one is never used."""
+    D, page = 64, 16
+    g = torch.Generator(device=DEV).manual_seed(1)
+    wide = torch.randn(2, 3 * 2 * D + 4, generator=g, device=DEV).half()
+    one = wide[:, :6 * D].unflatten(1, (6, D))[:1]       # [1][6][D], 388 elements a token
+    assert one.stride(0) % 8 and one.data_ptr() % 16 == 0
+    kc, vc = fq.kv_cache(2, 2, D, page, F16, DEV)
+    kc.zero_(), vc.zero_()
+    fq.kv_cache_write(one[:, 2:4], one[:, 4:], i32([17]), kc, vc)
+    k, v = gather(kc, vc, [17], page)
+    assert torch.equal(k, one[:, 2:4]) and torch.equal(v, one[:, 4:])
+    args = (kc, vc, i32([[1, 0]]), i32([1]), i32([0, 1]))
+    got = fq.tree_attention(one[:, :2], *args)
+    assert torch.equal(got, fq.tree_attention(one[:, :2].contiguous(), *args))
+    # one head, four elements from the next of a tensor that has no other
+    head = torch.randn(3, D, generator=g, device=DEV).half().as_strided((3, 1, D), (D, 4, 1))
+    kc, vc = fq.kv_cache(2, 1, D, page, F16, DEV)
+    kc.zero_(), vc.zero_()
+    fq.kv_cache_write(head, head, i32([3, 18, 19]), kc, vc)
+    k, v = gather(kc, vc, [3, 18, 19], page)
+    assert torch.equal(k, head) and torch.equal(v, head)
+    args = (kc, vc, i32([[0, 1]]), i32([17]), i32([0, 3]))
+    assert torch.equal(fq.tree_attention(head, *args),
+                       fq.tree_attention(head.reshape(3, D).view(3, 1, D), *args))
+
+
 def test_pack_w4_of_the_most_rows(fq):
     """2^24 rows, as many as are accepted: the last ones, the first, and some between."""
     N, K, group = 1 << 24, 128, 128

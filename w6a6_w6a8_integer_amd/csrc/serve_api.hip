@@ -181,6 +181,8 @@ flexq_status flexq_kv_cache_write(const uint16_t* k, int64_t k_stride_t, int64_t
   if (T == 0) return FLEXQ_SUCCESS;
   if (!k || !v || !slot_map || (num_pages > 0 && (!k_cache || !v_cache)))
     return FLEXQ_ERROR_INVALID_VALUE;
+  if (T == 1) k_stride_t = v_stride_t = 0;  // (never used)
+  if (Hkv == 1) k_stride_h = v_stride_h = 0;
   if (k_stride_t % 8 || k_stride_h % 8 || v_stride_t % 8 || v_stride_h % 8 ||
       k_stride_t > kMaxStride || k_stride_h > kMaxStride || v_stride_t > kMaxStride ||
       v_stride_h > kMaxStride)
@@ -231,6 +233,8 @@ flexq_status flexq_tree_attention(const uint16_t* q, int32_t dtype, int64_t q_st
     return FLEXQ_ERROR_INVALID_VALUE;
   if (workspace_bytes < flexq::attention_workspace_bytes(B, max_new, H, Hkv, D))
     return FLEXQ_ERROR_INVALID_VALUE;
+  if (T == 1) q_stride_t = 0;  // (never used)
+  if (H == 1) q_stride_h = 0;
   if (q_stride_t % 8 || q_stride_h % 8 || q_stride_t > kMaxStride || q_stride_h > kMaxStride)
     return FLEXQ_ERROR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
