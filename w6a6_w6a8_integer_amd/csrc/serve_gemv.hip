@@ -180,10 +180,10 @@ __device__ __forceinline__ void store_four(uint16_t* to, f32x4 v) {
   *reinterpret_cast<u32x2*>(to) = o;
 }
 
-// Up to four rows.  An item is T adjacent 16-row tiles of the weight; a persistent
-// workgroup owns a run of items, its W waves take the 128-deep k-blocks of an item in turn
-// (a wave's part of a tile and k-block is 1 KB in one piece), and the waves' sums are added
-// in wave order through LDS.  P steps of loads are in flight, on into the next item.
+// Up to four rows.  A persistent workgroup owns a run of 16-row tiles of the weight, its W
+// waves take the 128-deep k-blocks of a tile in turn (1 KB in one piece each), and the waves'
+// sums are added in wave order through LDS.  P steps of loads are in flight, on into the next
+// tile.
 //
 // All loads are buffer loads and no branch is around one, so that the waits count exactly
 // the steps in flight.  The addresses only ever grow by constants (the scalar unit is
@@ -193,54 +193,49 @@ __device__ __forceinline__ void store_four(uint16_t* to, f32x4 v) {
 // The activations are in LDS, rows K + 32 elements apart, so that only the weights and
 // scales take registers in flight; lanes without a row read the last one's (their columns
 // are not stored).
-template <class E, int G, int T, int W, int P>
+template <class E, int G, int W, int P>
 __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
     const uint16_t* __restrict__ x, int64_t x_stride, const uint32_t* __restrict__ w4,
-    const uint16_t* __restrict__ sw, int M, int N, int K, int tiles, int items,
-    uint16_t* __restrict__ y) {
+    const uint16_t* __restrict__ sw, int M, int N, int K, int tiles, uint16_t* __restrict__ y) {
   constexpr int kGroups = 128 / G;  // of a k-block
   constexpr int kSteps = G / 32;    // MFMAs of a group
   extern __shared__ __attribute__((aligned(16))) uint16_t lds_x[];
-  __shared__ f32x4 part[2][W][T][64];
+  __shared__ f32x4 part[2][W][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, p = lane >> 4;
   const int kbs = K >> 7;
   const int rounds = (kbs + W - 1) / W;
-  const int first = (int)((int64_t)items * blockIdx.x / gridDim.x);
-  const int last = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
+  const int first = (int)((int64_t)tiles * blockIdx.x / gridDim.x);
+  const int last = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
 
   struct Slot {
-    u32x4 w[T];
-    u32x2 s[T];
+    u32x4 w;
+    u32x2 s;
   } ring[P];
 
-  // Loads of one wave step: k-block kb of item, which the offsets stand for.
-  const int64_t run = (int64_t)first * T * kbs * 1024;
+  // Loads of one wave step: k-block kb of a tile, which the offsets stand for.
+  const int64_t run = (int64_t)first * kbs * 1024;
   const auto rw = make_rsrc(reinterpret_cast<const char*>(w4) + run,
-                            (uint32_t)((int64_t)min(last * T, tiles) * kbs * 1024 - run));
-  const auto rs = make_rsrc(sw + first * T * 16,
-                            (uint32_t)((int64_t)(K / G) * N * 2 - (int64_t)first * T * 32));
+                            (uint32_t)((int64_t)last * kbs * 1024 - run));
+  const auto rs = make_rsrc(sw + first * 16,
+                            (uint32_t)((int64_t)(K / G) * N * 2 - (int64_t)first * 32));
   int kb = wave;
   uint32_t w_off = wave * 1024 + lane * 16;
-  uint32_t s_item = (uint32_t)(wave * kGroups + c % kGroups) * (N * 2) + 8 * p;
-  uint32_t s_off = s_item;
+  uint32_t s_tile = (uint32_t)(wave * kGroups + c % kGroups) * (N * 2) + 8 * p;
+  uint32_t s_off = s_tile;
   auto next_load = [&](Slot& r) {
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      r.w[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             rw, w_off + t * (kbs * 1024), 0, kNonTemporal));
-      r.s[t] = __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, s_off + t * 32, 0, 0));
-    }
+    r.w = __builtin_bit_cast(
+        u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, w_off, 0, kNonTemporal));
+    r.s = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, s_off, 0, 0));
     kb += W;
     w_off += W * 1024;
     s_off += W * kGroups * (N * 2);
-    if (kb >= rounds * W) {  // the next item
+    if (kb >= rounds * W) {  // the next tile
       kb = wave;
-      w_off += (T * kbs - rounds * W) * 1024;
-      s_item += T * 32;
-      s_off = s_item;
+      w_off += (kbs - rounds * W) * 1024;
+      s_tile += 32;
+      s_off = s_tile;
     }
   };
 
@@ -248,7 +243,7 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
   const uint16_t* lds_row = lds_x + min(c, M - 1) * (K + 32) + p * 8;
   const uint16_t* lds_zeros = lds_x + M * (K + 32) + p * 8;
 
-  f32x4 acc[T] = {};
+  f32x4 acc = {};
   auto work = [&](const Slot& r, int round) {
     const int kb_now = round * W + wave;  // past K zeros: other activations may be infinite
     const uint16_t* at = kb_now < kbs ? lds_row + kb_now * 128 : lds_zeros;
@@ -257,38 +252,29 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
     for (int j = 0; j < 4; ++j) xf[j] = *reinterpret_cast<const u32x4*>(at + j * 32);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
+      f32x4 dot = {};
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
-        f32x4 dot = {};
-#pragma unroll
-        for (int j = g * kSteps; j < (g + 1) * kSteps; ++j)
-          dot = E::mfma(codes(r.w[t][j]), xf[j], dot);
-        scale_add(acc[t], dot, group_scales<kGroups>(r.s[t], g));
-      }
+      for (int j = g * kSteps; j < (g + 1) * kSteps; ++j)
+        dot = E::mfma(codes(r.w[j]), xf[j], dot);
+      scale_add(acc, dot, group_scales<kGroups>(r.s, g));
     }
   };
 
   // the waves' sums, in order
-  auto finish = [&](int item) {
-    f32x4(*to)[T][64] = part[item & 1];
+  auto finish = [&](int tile) {
+    f32x4(*to)[64] = part[tile & 1];
+    to[wave][lane] = acc;
+    acc = f32x4{};
+    lds_barrier();  // (the next tile's sums go to the other half)
+    if ((wave + tile) % W != 0) return;
+    f32x4 s = to[0][lane];
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      to[wave][t][lane] = acc[t];
-      acc[t] = f32x4{};
+    for (int v = 1; v < W; ++v) {
+      const f32x4 o = to[v][lane];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += o[k];
     }
-    lds_barrier();  // (the next item's sums go to the other half)
-    const int t = (wave + item) % W, tile = item * T + t;
-    if (t < T && tile < tiles) {
-      f32x4 s = to[0][t][lane];
-#pragma unroll
-      for (int v = 1; v < W; ++v) {
-        const f32x4 o = to[v][t][lane];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[k] += o[k];
-      }
-      if (c < M)
-        store_four<E>(y + (int64_t)c * N + tile * 16 + 4 * p, s * Codes<E>::kScale);
-    }
+    if (c < M) store_four<E>(y + (int64_t)c * N + tile * 16 + 4 * p, s * Codes<E>::kScale);
   };
 
   const int pieces = K / 8;  // 16 bytes each
@@ -304,9 +290,9 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
     __builtin_amdgcn_sched_barrier(0);  // the waits count on the steps' order
   }
   lds_barrier();  // the activations are there
-  int item = first, round = 0;
+  int tile = first, round = 0;
   const int steps = (last - first) * rounds;
-  for (int step = 0; item < last; step += P) {
+  for (int step = 0; tile < last; step += P) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       if (step + i >= steps) break;
@@ -315,9 +301,9 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
       next_load(ring[i]);
       __builtin_amdgcn_sched_barrier(0);
       if (++round == rounds) {
-        finish(item);
+        finish(tile);
         round = 0;
-        ++item;
+        ++tile;
       }
     }
   }
@@ -550,22 +536,23 @@ Cut cut_of(int64_t M, int64_t N, int64_t K) {
   return cut;
 }
 
-template <class E, int G, int T>
+template <class E, int G>
 hipError_t gemv_launch(const uint16_t* x, int64_t x_stride, const uint32_t* w4,
                        const uint16_t* sw, int64_t M, int64_t N, int64_t K, uint16_t* y,
                        hipStream_t stream) {
   constexpr int W = 8, P = 4;
-  const int64_t tiles = N / 16, items = (tiles + T - 1) / T, cus = device_cu_count();
+  const int64_t tiles = N / 16, cus = device_cu_count();
   const int64_t x_bytes = x_lds_bytes(M, K);
   // Two workgroups a compute unit, or three if registers and LDS hold them and the last round
-  // of items is fuller for it (10240 x 8192, 640 items: 15.1 us against 17.1; but 14336 x
-  // 4096, 896 items: 11.1 against 10.3).
-  auto cost = [&](int64_t held) { return (items + held * cus - 1) / (held * cus) * held; };
-  const int64_t held = T == 1 && x_bytes <= 32 * 1024 && cost(3) < cost(2) ? 3 : 2;
-  return launch_kernel_lds(gemv_w4_kernel<E, G, T, W, P>,
-                           dim3((unsigned)std::min(items, held * cus)), dim3(64 * W), x_bytes,
-                           stream, x, x_stride, w4, sw, (int)M, (int)N, (int)K, (int)tiles,
-                           (int)items, y);
+  // of tiles is fuller for it (10240 x 8192, 640 tiles: 11.0 us against 12.3; but 14336 x
+  // 4096, 896 tiles: 8.5 against 8.1).  (Two tiles at a time share x's fragments and leave the
+  // workgroups' shares less even: 32768 x 4096 14.4 us against 13.6, 57344 x 8192 43.5 against
+  // 41.4, 131072 x 4096 46.8 against 47.6.)
+  auto cost = [&](int64_t held) { return (tiles + held * cus - 1) / (held * cus) * held; };
+  const int64_t held = x_bytes <= 32 * 1024 && cost(3) < cost(2) ? 3 : 2;
+  return launch_kernel_lds(gemv_w4_kernel<E, G, W, P>,
+                           dim3((unsigned)std::min(tiles, held * cus)), dim3(64 * W), x_bytes,
+                           stream, x, x_stride, w4, sw, (int)M, (int)N, (int)K, (int)tiles, y);
 }
 
 template <class E, int G, int NT, int T>
@@ -589,14 +576,7 @@ template <class E, int G>
 hipError_t gemv_any(const uint16_t* x, int64_t x_stride, const uint32_t* w4, const uint16_t* sw,
                     int64_t M, int64_t N, int64_t K, float* part, uint16_t* y,
                     hipStream_t stream) {
-  if (few_rows(M, K)) {
-    // two tiles an item halve the reads of x and the steps' overhead, one tile leaves the
-    // workgroups' shares more even (57344 x 8192: 46.7 us against 50.0; 28672 x 8192: 29.2
-    // against 27.6)
-    if (N / 16 >= 4 * 2 * device_cu_count())
-      return gemv_launch<E, G, 2>(x, x_stride, w4, sw, M, N, K, y, stream);
-    return gemv_launch<E, G, 1>(x, x_stride, w4, sw, M, N, K, y, stream);
-  }
+  if (few_rows(M, K)) return gemv_launch<E, G>(x, x_stride, w4, sw, M, N, K, y, stream);
   if (M <= 16) return gemm_launch<E, G, 1, 1>(x, x_stride, w4, sw, M, N, K, part, y, stream);
   if (M <= 32) return gemm_launch<E, G, 2, 1>(x, x_stride, w4, sw, M, N, K, part, y, stream);
   if (cut_of(M, N, K).tiles_a_wave == 1)
