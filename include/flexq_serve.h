@@ -150,7 +150,8 @@ flexq_status flexq_kv_cache_write(const uint16_t* k, int64_t k_stride_t, int64_t
                 stride of an axis of length one plays no part)
      tree_mask  int32[T][mask_words] or NULL; bits past mask_words are 0
      out        [T][H][D] of dtype, 16-byte aligned     lse  fp32[T][H] or NULL
-     max_new    no request has more drafted tokens (further ones are not computed)
+     max_new    no request has more drafted tokens (further ones are not computed); the
+                work and the workspace are laid out for that many rows a request
      workspace  flexq_tree_attention_workspace_bytes(B, max_new, H, Hkv, D) bytes, 16-byte
                 aligned, overwritten; not to be used by other work until this call's
                 kernels have run

@@ -335,7 +335,7 @@ PyObject* tree_attention(PyObject* const* a) {
   const int64_t B = table.size(0), max_blocks = table.size(1);
   const Tensor& ctx = exact(tensor(a[4], "ctx_lens"), at::kInt, "ctx_lens", {B});
   const Tensor& cu = exact(tensor(a[5], "cu_new"), at::kInt, "cu_new", {B + 1});
-  const int64_t max_new = given(a[8]) ? integer(a[8], "max_new") : T;
+  int64_t max_new = given(a[8]) ? integer(a[8], "max_new") : T;
   Tensor mask, out, lse, ws;
   int64_t words = 0;
   if (given(a[6])) {
@@ -343,6 +343,8 @@ PyObject* tree_attention(PyObject* const* a) {
     dims_check(mask, 2, "tree_mask");
     words = mask.size(1);
     exact(mask, at::kInt, "tree_mask", {T, words});
+    // a mask's bits are as many as one request's tokens may be
+    if (!given(a[8])) max_new = std::min(T, 32 * words);
     value_check(max_new <= 32 * words, "tree_mask has ", 32 * words, " bits a token; max_new = ",
                 max_new);
   }
