@@ -41,10 +41,7 @@ constexpr int units_per_cu(int64_t D, int rows) { return D > 64 ? 2 : rows == 16
 // single token over 37 10.1 us, as then there is a join, against 8.1).
 constexpr uint32_t kHead = 5, kMinShare = 8;
 
-constexpr int kNonTemporal = 2;  // cache-policy bit of loads
-
 typedef __attribute__((address_space(1))) const void* global_ptr_t;
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef __attribute__((address_space(4))) const int32_t* scalar_ptr_t;
 
 // (max, sum) over the lanes that hold one of RW rows (l ^ 32, and of 16 rows l ^ 16 too).  A
@@ -70,20 +67,6 @@ __device__ __forceinline__ float row_sum(float x) {
 // the low n bits, n clamped to 0 .. 8
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : (n >= 8 ? 0xFFu : (1u << n) - 1u);
-}
-
-// s_waitcnt vmcnt(N) alone (gfx9 encoding: vmcnt[3:0], expcnt[6:4], lgkmcnt[11:8],
-// vmcnt[5:4] in [15:14]).
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
-}
-
-// A barrier that the wave's own LDS accesses have come before: a stage may be overwritten behind
-// it.  Loads from memory stay in flight.
-__device__ __forceinline__ void barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 }  // namespace
@@ -464,7 +447,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
       typename P::Out o[P::kOuts] = {};
       float m = -INFINITY, l = 0.0f;
 
-      barrier();  // the stages of the request before have been read
+      lds_barrier();  // the stages of the request before have been read
       // S - 1 steps, the last again where there are fewer: with a fixed number of loads behind
       // it the wait for q (before the loop, not in it) leaves them in flight.
 #pragma unroll
@@ -480,7 +463,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
           wait_vm<(S - 2) * DT>();
         else
           wait_vm<0>();
-        barrier();
+        lds_barrier();
         if (step + S - 1 < end) stage(step + S - 1);
         if (idle) continue;
         const u32x4* kf = reinterpret_cast<const u32x4*>(lds + (step % S) * kStage);
@@ -632,7 +615,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const At
           }
         }
     }
-    barrier();
+    lds_barrier();
     if (careful || again == 0) break;
   }
 }

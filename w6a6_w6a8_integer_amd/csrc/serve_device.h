@@ -1,5 +1,5 @@
 // serve_device.h -- gfx950 device helpers of the decoding-step kernels: 16-bit element
-// types and their MFMAs.
+// types and their MFMAs, waits and barriers.
 #pragma once
 #include "w6_device.h"
 
@@ -7,6 +7,24 @@ namespace flexq {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kNonTemporal = 2;  // cache-policy bit of loads
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+// s_waitcnt vmcnt(N) alone (gfx9 encoding: vmcnt[3:0], expcnt[6:4], lgkmcnt[11:8],
+// vmcnt[5:4] in [15:14]).
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+// A barrier that the wave's own LDS accesses have come before (a stage may be overwritten
+// behind it).  Loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 
 // 16x16x32 MFMA on 16-bit elements: lane l supplies A row l % 16 and B column l % 16, the
 // eight elements of k-slots 8 (l / 16) ..; D lane l holds column l % 16, rows

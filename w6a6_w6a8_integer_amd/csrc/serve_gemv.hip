@@ -16,31 +16,15 @@ namespace flexq {
 namespace {
 
 constexpr uint32_t kRsrcWord3 = 0x00020000u;  // raw 32-bit dword buffer, gfx9 style
-constexpr int kNonTemporal = 2;                // cache-policy bit of buffer loads
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes,
                                            kRsrcWord3);
 }
 
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-
-// s_waitcnt vmcnt(N) alone (gfx9 encoding: vmcnt[3:0], expcnt[6:4], lgkmcnt[11:8],
-// vmcnt[5:4] in [15:14]).
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
-}
-
 // 16 bytes a lane from memory to LDS: lane l's at `to` + 16 l, zeros past the buffer.
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, char* to, uint32_t off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr_t)to, 16, off, 0, 0, 0);
-}
-
-// A barrier for what went through LDS alone: loads from memory stay in flight.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // dword of row n, column k = 128 kb + 32 j + 8 p (+ c)
