@@ -145,7 +145,8 @@ flexq_status flexq_kv_cache_write(const uint16_t* k, int64_t k_stride_t, int64_t
    the sum of two 16-bit parts, within 2^-17 of themselves or, for fp16, 2^-34 of the row's
    largest, whichever is more; out is rounded once.
    What masked places, unused slots and pages hold does not matter, NaN and infinities
-   included; an infinite value of an attended key gives an infinity of its sign.  Tokens on a page outside [0, num_pages) are left out.
+   included; an infinite value of an attended key gives an infinity of its sign.  Tokens on
+   a page outside [0, num_pages) are left out.
      q          element (t, h, d) at t * q_stride_t + h * q_stride_h + d, t < T (the
                 stride of an axis of length one plays no part)
      tree_mask  int32[T][mask_words] or NULL; bits past mask_words are 0

@@ -17,8 +17,8 @@
 //
 // Bound by HBM's reads of the cache, for many rows nearly as much by the MFMAs and the
 // exponentials beside them.  Measured (8 key heads of 128, 64 heads): 32 single tokens over
-// up to 4k tokens 53 us, 5.3 TB/s; 24 requests of up to 13 over 8k 95 us, 5.0 TB/s; 2 of up to
-// 9 over 128k 182 us, 5.1 TB/s and 350 TFLOP/s.
+// up to 4k tokens 54 us, 5.3 TB/s; 24 requests of up to 13 over 8k 95 us, 4.9 TB/s; 2 of up to
+// 9 over 128k 184 us, 5.0 TB/s and 344 TFLOP/s.
 #include <algorithm>
 
 #include "kernels.h"
@@ -33,12 +33,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWaves = 4;
 // Workgroups a compute unit holds: two by LDS (4 stages of 2 D 64 bytes, 2 where D = 256),
-// on 64-wide heads as many as registers allow (48 rows of 40 heads: 31 us against 34 with two;
-// 110 rows, three: 52 against 53, and 62 with a fourth that waits for the others).
+// on 64-wide heads as many as registers allow (48 rows of 40 heads: 30 us against 32 with two;
+// 110 rows, three: 45 against 49, and 55 with a fourth that waits for the others).
 constexpr int units_per_cu(int64_t D, int rows) { return D > 64 ? 2 : rows == 16 ? 4 : 3; }
 // What starting on a request costs, in 32-key steps, and the least share of a workgroup
-// (counting no start: 32 single tokens over 4k 64 us against 57; shares down to one step: a
-// single token over 37 10.1 us, as then there is a join, against 8.1).
+// (counting no start: 32 single tokens over 4k 57 us against 54; shares down to one step: a
+// single token over 37 10.1 us, as then there is a join, against 8.2).
 constexpr uint32_t kHead = 5, kMinShare = 8;
 
 typedef __attribute__((address_space(1))) const void* global_ptr_t;
@@ -324,7 +324,8 @@ struct Products<E, DT, 32> {
 // that a step has come and that the one before has been read.
 //
 // ONE: there is one row block, nobody reads the cache's lines again, and they are not kept
-// (32 single tokens over 4k: 57 us against 63 when they are, 2 of 9 over 128k 203 and 216).
+// (32 single tokens over 4k: 54 us against 62 when they are, 24 of 13 over 8k 96 and 110, 2 of 9
+// over 128k 189 and 193; but 8 of 48 over 2k, 40 heads of 64, 29.6 and 28.1).
 template <class E, int DT, int RW, int S, bool ONE>
 __global__ __launch_bounds__(64 * kWaves, 2) void tree_attention_kernel(const AttentionArgs a,
                                                                         int shares,
@@ -693,8 +694,8 @@ Layout layout_of(int64_t max_new, int64_t H, int64_t Hkv, int64_t D) {
   Layout p;
   const int64_t rows = max_new * (H / Hkv);
   // 32 rows a wave halve the LDS reads and MFMAs for many rows, and are half empty for few (up
-  // to 104 rows: 111 us against 116 with 16; 72 rows over 128k: 203 against 240; but 48 rows:
-  // 37 us against 31, one row 9.1 against 8.1).  256-wide heads have no registers for them.
+  // to 104 rows: 97 us against 126 with 16; 72 rows over 128k: 189 against 227; but 48 rows:
+  // 32 us against 30, one row 9.0 against 8.2).  256-wide heads have no registers for them.
   p.rows = rows <= 4 * 16 || D > 128 ? 16 : 32;
   p.row_blocks = (int)((rows + kWaves * p.rows - 1) / (kWaves * p.rows));
   const int64_t target = units_per_cu(D, p.rows) * device_cu_count();

@@ -69,9 +69,9 @@ __global__ __launch_bounds__(256) void pack_w4_kernel(const uint16_t* __restrict
 }
 
 // Both kernels below are bound by HBM (0.5 byte a weight) where the weight is large: one row
-// of 57344 x 8192 takes 44 us, 5.6 TB/s.  Smaller weights are latency (4096 x 4096: 5 us, a
-// launch and one load after the other), more rows the LDS reads of x and the MFMAs (64 rows
-// of 57344 x 8192: 101 us, 600 TFLOP/s).
+// of 57344 x 8192 takes 41 us, 5.9 TB/s, in bfloat16, whose codes take more to convert, 47.
+// Smaller weights are latency (4096 x 4096: 5 us, a launch and one load after the other), more
+// rows the LDS reads of x and the MFMAs (64 rows of 57344 x 8192: 78 us, 770 TFLOP/s).
 //
 // Eight codes as the MFMA's 16-bit floats of their own values, so that a sum errs in
 // proportion to what it adds: a large activation whose code is 0 adds 0, also where it is
@@ -303,7 +303,8 @@ __global__ __launch_bounds__(64 * W, 4) void gemv_w4_kernel(
 // the 16-byte pieces are placed so that the 16 lanes of a fragment read (16 rows, one
 // piece each) meet 16 different banks: piece k of row r at slot 8 (r ^ h) + (k ^ r), h the
 // block's parity.
-// k-blocks of a chunk (up to 16 rows, with four: 13 x 5120 x 13824 18.7 us against 16.2)
+// k-blocks of a chunk (up to 16 rows, with four: 13 x 5120 x 13824 15.4 us against 13.7, 16 x
+// 57344 x 8192 50.8 against 49.1)
 constexpr int kChunk = 2;
 
 template <class E, int G, int NT, int T>
@@ -492,25 +493,25 @@ hipError_t pack_any(const uint16_t* w, int64_t N, int64_t K, int group, uint32_t
   return launch_kernel(kernel, grid, dim3(256), stream, w, (int)N, (int)K, w4, sw);
 }
 
-// The few-rows kernel: two workgroups' activations and sums fit a compute unit's LDS.
-// One row of 4096 x 4096 takes 5.0 us with it and 7.2 with the other, of 57344 x 8192 45 and
-// 51; four of 5120 x 5120 (groups of 32) 10.9 and 10.2.
+// The few-rows kernel, for activations that every workgroup can hold in LDS.  One row of 4096 x 4096 takes 5.4 us with it and 7.8 with
+// the other, of 10240 x 8192 11.0 and 13.0, of 57344 x 8192 41 and 47; four of 5120 x 5120 (groups
+// of 32) 9.1 and 8.7; one of 8192 x 28672, past the bound on LDS, 25.5 and 24.3.
 int64_t x_lds_bytes(int64_t M, int64_t K) { return (M * (K + 32) + 128) * 2; }
 bool few_rows(int64_t M, int64_t K) { return M <= 4 && x_lds_bytes(M, K) <= 48 * 1024; }
 
 // The other one: tiles a wave, and slices of K that give every compute unit a workgroup.
-// Twice the slices only add sums to join (13 x 5120 x 13824: 17.9 us against 16.2; 64 x 8192 x
-// 8192: 34 against 26), half of them leave compute units idle (22 and 34).
+// Twice the slices only add sums to join (13 x 5120 x 13824: 15.4 us against 13.7; 64 x 8192 x
+// 8192: 31 against 21), half of them leave compute units idle (20 and 28).
 struct Cut {
   int tiles_a_wave, slices;
 };
 
 Cut cut_of(int64_t M, int64_t N, int64_t K) {
   Cut cut;
-  // With more than 32 rows of x its reads from LDS bound a wave; two tiles share them, and
-  // the -24 x sums, where one tile a wave would take the compute units twice (64 rows,
-  // K = 8192: N = 40960 87 us against 107, 57344 98 against 117, 131072 204 against 247; but
-  // 8192, 29 against 26).
+  // With more than 32 rows of x its reads from LDS bound a wave; two tiles share them where
+  // one tile a wave would take the compute units twice (64 rows, K = 8192: N = 40960 66 us
+  // against 86, 57344 78 against 94, 131072 167 against 200; but 8192, 24 against 21, and 48 x
+  // 22016 x 4096 29 against 24).
   cut.tiles_a_wave = M > 32 && N / 16 > 8 * device_cu_count() ? 2 : 1;
   const int64_t per = 8 * cut.tiles_a_wave;
   const int64_t units = (N / 16 + per - 1) / per * ((M + 63) / 64);
