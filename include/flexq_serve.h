@@ -100,7 +100,8 @@ size_t flexq_gemv_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
      slot_map[t] = -1 for cu_new[B] <= t < max_tokens
      counts = {cu_new[B], sum of add, head + sum of add}  (the last: the next step's head)
    Where the free list or a table row ends too soon, the table gets -1 (or nothing past
-   its row) and such tokens the slot -1; tokens past max_tokens get no slot.  The caller
+   its row) and such tokens the slot -1, as tokens do whose slot int32 does not hold; tokens
+   past max_tokens get no slot.  The caller
    sees it in counts.  A negative length counts as 0.  Other table entries are kept.
      ctx_lens, new_lens int32[B]       free_pages int32[num_free]     free_head int32[1]
      block_table int32[B][max_blocks]  (in, out)

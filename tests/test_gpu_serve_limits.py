@@ -87,6 +87,18 @@ def test_pack_w4_of_the_most_rows(fq):
     assert int((w4 == 0x08080808 * 17 - (1 << 32)).sum()) >= N * K // 8 - len(rows) * 2 * K
 
 
+def test_block_tables_slots_past_32_bits(fq):
+    """A slot that int32 does not hold is -1, not another request's."""
+    page = 65536
+    table = i32([[32767, 32768, 65536, 65537], [1, -1, -1, -1]])
+    slots, cu, counts = fq.block_tables(i32([page - 2, 0]), i32([3 * page, 2]), i32([70000]), table,
+                                        page, 3 * page + 2)
+    want = torch.full((3 * page + 2,), -1, dtype=torch.int32, device=DEV)
+    want[:2] = i32([32767 * page + page - 2, 32767 * page + page - 1])
+    assert torch.equal(slots[:3 * page], want[:3 * page])
+    assert table[0].tolist() == [32767, 70000, -1, -1] and counts.tolist() == [3 * page + 2, 4, 4]
+
+
 @pytest.mark.parametrize("T,Hkv,D,page", [(2100, 16, 64, 16), (1089, 32, 96, 32),
                                           (4131, 8, 128, 64), (1025, 40, 256, 128),
                                           (700, 64, 128, 16)])

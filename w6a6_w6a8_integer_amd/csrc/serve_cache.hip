@@ -140,7 +140,8 @@ __global__ __launch_bounds__(kScanThreads) void block_tables_kernel(
             id = free_pages[f];
         }
       }
-      if (id >= 0) slot[j] = (int)(((int64_t)id << shift) + (pos & (page - 1)));
+      const int64_t at = ((int64_t)id << shift) + (pos & (page - 1));
+      if (id >= 0 && at <= INT32_MAX) slot[j] = (int)at;
     }
     if constexpr (PER % 4 == 0) {
       if (t0 + PER <= max_tokens && wide) {
