@@ -139,9 +139,9 @@ __global__ __launch_bounds__(kScanThreads) void block_tables_kernel(
           else if (f >= 0 && f < num_free)
             id = free_pages[f];
         }
+        if (id > INT32_MAX >> shift) id = -1;  // its slots are no int32
       }
-      const int64_t at = ((int64_t)id << shift) + (pos & (page - 1));
-      if (id >= 0 && at <= INT32_MAX) slot[j] = (int)at;
+      if (id >= 0) slot[j] = (id << shift) + (int)(pos & (page - 1));
     }
     if constexpr (PER % 4 == 0) {
       if (t0 + PER <= max_tokens && wide) {
