@@ -31,6 +31,11 @@ hipError_t launch_kv_cache_write(const uint16_t* k, int64_t k_st, int64_t k_sh,
 
 // What a tree attention call works on (flexq_serve.h has the meaning of each).
 struct AttentionArgs {
+  // What starting on a request costs, in 32-key steps, and the least share of a workgroup
+  // (counting no start: 32 single tokens over 4k 57 us against 54; shares down to one step: a
+  // single token over 37 10.1 us, as then there is a join, against 8.2).
+  static constexpr uint32_t kHead = 5, kMinShare = 8;
+  static constexpr bool kWindowed = false;
   const uint16_t* q;
   int64_t q_st, q_sh;
   const uint16_t* kc;
@@ -51,5 +56,50 @@ struct AttentionArgs {
 
 size_t attention_workspace_bytes(int64_t B, int64_t max_new, int64_t H, int64_t Hkv, int64_t D);
 hipError_t launch_tree_attention(const AttentionArgs& a, bool bf16, hipStream_t stream);
+
+// The same over a 4-bit cache: kc and vc hold codes, and keys of the context before the last
+// `window` of a token's positions are left out, but for the first `sinks` (window 0: none are).
+struct Kv4AttentionArgs : AttentionArgs {
+  static constexpr uint32_t kHead = 5, kMinShare = 8;
+  static constexpr bool kWindowed = true;
+  bool bf16;
+  const uint16_t* scales;
+  int32_t window, sinks;
+};
+
+size_t kv4_attention_workspace_bytes(int64_t B, int64_t max_new, int64_t H, int64_t Hkv,
+                                     int64_t D);
+hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t stream);
+
+hipError_t launch_kv4_cache_write(const uint16_t* k, int64_t k_st, int64_t k_sh,
+                                  const uint16_t* v, int64_t v_st, int64_t v_sh, bool bf16,
+                                  const int32_t* slots, int64_t T, int64_t Hkv, int64_t D,
+                                  int64_t num_pages, int page_size, uint32_t* kc, uint32_t* vc,
+                                  uint16_t* scales, hipStream_t stream);
+hipError_t launch_kv4_cache_read(const uint32_t* kc, const uint32_t* vc, const uint16_t* scales,
+                                 const int32_t* slots, int64_t T, int64_t Hkv, int64_t D,
+                                 int64_t num_pages, int page_size, bool bf16, uint16_t* k,
+                                 uint16_t* v, hipStream_t stream);
+
+// What a lora_add call works on; h is the workspace, fp32 [slices][T][R padded].
+struct LoraArgs {
+  const uint16_t* x;
+  int64_t x_st;
+  const uint16_t* y;
+  int64_t y_st;
+  const int32_t* adapters;
+  const uint16_t* a;
+  const uint16_t* b;
+  const int32_t* ranks;
+  const float* scales;
+  int64_t T;
+  int32_t N, K, R, L;
+  float* h;
+  uint16_t* out;
+  int64_t out_st;
+};
+
+size_t lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L);
+hipError_t launch_lora(const LoraArgs& a, bool bf16, hipStream_t stream);
 
 }  // namespace flexq
