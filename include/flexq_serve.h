@@ -10,6 +10,11 @@
  *                                    request lengths
  *   flexq_kv_cache_write             new keys and values into the paged cache
  *   flexq_tree_attention             attention of drafted tokens over the paged cache
+ *   flexq_kv4_cache_write, flexq_kv4_cache_read, flexq_kv4_attention
+ *                                    the same over a paged cache of 4-bit codes, with an
+ *                                    optional sliding window whose first tokens stay visible
+ *   flexq_lora_add                   low-rank adapters of many requests at once, added to a
+ *                                    shared projection's output
  *
  * Element type: `dtype` says whether 16-bit tensors hold IEEE half (FLEXQ_FP16) or
  * bfloat16 (FLEXQ_BF16).  Lengths, tables and slot maps are int32.  A step's lengths
@@ -36,6 +41,23 @@
  * As torch tensors: keys [pages][Hkv][page_size/16][D/32][16][32], values
  * [pages][Hkv][page_size/16][D][16].  D is 64, 96, 128 or 256.
  * block_table[b][i] is the page of request b's tokens i * page_size ...
+ *
+ * 4-bit cache: pages, slots and tables as above, (D + 8) bytes a token and head instead of
+ * 4 D.  A row x[0 .. D) of a token and head is held as x = b + s c:
+ *   b = fp16(min x);  s = fp16((max x - min x) / 15);
+ *   c = clamp(rint((x - b) / s), 0, 15), 0 where s = 0
+ *   (IEEE binary32 before the roundings to fp16, which are to nearest, ties to even, as rint)
+ * for fp16 and bfloat16 rows alike.  A row with a NaN, or whose b or s is not finite, has NaN for
+ * both and so reads as NaN.  Of the token at slot page * page_size + r, with block =
+ * (page * Hkv + h) * (page_size / 16) + r / 16,
+ *   keys    code of d at dword block * 2 D + (r % 16) * (D / 8) + d / 8,
+ *           bits 4 (d % 8 / 2) + 16 (d % 2) ..
+ *   values  code of d in dword block * 2 D + (r % 16 / 8) * D + d / 2 * 2 + r % 8 / 4,
+ *           byte 0, 2, 1, 3 for r % 4 = 0 .. 3, bits 4 (d % 2) .. of it
+ *   scales  fp16 at block * 64 + r % 16: s of the key, + 16 its b, + 32 s of the value, + 48 its b
+ * (keys in the order a score's MFMA takes, values with tokens in bytes that can be written alone).
+ * As torch tensors: k_codes int32 [pages][Hkv][page_size/16][16][D/8], v_codes int32
+ * [pages][Hkv][page_size/16][2][D/2][2], scales fp16 [pages][Hkv][page_size/16][4][16].
  */
 #ifndef FLEXQ_SERVE_H
 #define FLEXQ_SERVE_H
@@ -178,6 +200,93 @@ flexq_status flexq_tree_attention(const uint16_t* q, int32_t dtype, int64_t q_st
    that it refuses or that makes it a no-op. */
 size_t flexq_tree_attention_workspace_bytes(int64_t B, int64_t max_new, int64_t H, int64_t Hkv,
                                             int64_t D);
+
+/* Keys and values of T tokens into the 4-bit cache: token t's go to slot slot_map[t]; a
+   slot outside [0, num_pages * page_size) (such as -1) drops the token.  No other token's place
+   is written, also where two calls write neighbouring slots at once.  The slots of a call
+   should differ: of two tokens with one slot that slot holds a mixture afterwards.
+     k, v      of dtype, as in flexq_kv_cache_write       slot_map  int32[T]
+     k_codes, v_codes, scales  the layouts above, 16-byte aligned (output)
+   T == 0 is a no-op.  Errors: as flexq_kv_cache_write, and INVALID_VALUE for dtype. */
+flexq_status flexq_kv4_cache_write(const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h,
+                                   const uint16_t* v, int64_t v_stride_t, int64_t v_stride_h,
+                                   int32_t dtype, const int32_t* slot_map, int64_t T, int64_t Hkv,
+                                   int64_t D, int64_t num_pages, int32_t page_size,
+                                   uint32_t* k_codes, uint32_t* v_codes, uint16_t* scales,
+                                   void* stream);
+
+/* The tokens at slots slot_map[0 .. T) of the 4-bit cache as rows of dtype, b + s c rounded
+   once: what attention over the cache sees of them.  A slot outside the cache reads as 0.
+     k, v      [T][Hkv][D] of dtype, 16-byte aligned (output)
+   T == 0 is a no-op.  Errors: INVALID_VALUE (null, negative size, dtype, overlap), UNSUPPORTED
+   (D, page_size, sizes as flexq_kv_cache_write, alignment). */
+flexq_status flexq_kv4_cache_read(const uint32_t* k_codes, const uint32_t* v_codes,
+                                  const uint16_t* scales, const int32_t* slot_map, int64_t T,
+                                  int64_t Hkv, int64_t D, int64_t num_pages, int32_t page_size,
+                                  int32_t dtype, uint16_t* k, uint16_t* v, void* stream);
+
+/* Attention of drafted tokens over the 4-bit cache: flexq_tree_attention's with the keys and
+   values that the codes stand for, b + s c.
+   window  0, or how many positions a token sees, itself among them: of the context token t (in
+           its request) attends the keys from ctx_lens[b] + n_t - window on, n_t the
+           request's drafted tokens that it attends (t + 1 in a chain), and of a chain's
+           drafted tokens those from there on too; a tree's bits hold whatever the window.
+   sinks   with a window, the first `sinks` tokens of the request stay visible; without one it
+           plays no part.
+   Keys that no token's window holds are not read.  Scores, statistics and sums are fp32; the
+   queries enter with 11 bits or more down to 2^-28 of a row's largest; probabilities times the
+   values' scales enter their product as two fp16 parts, within 2^-22 of themselves or 2^-35 of
+   the row's largest, whichever is more; out is rounded once.  What masked places, unused
+   slots and pages hold does not matter.  A row that attends a NaN key or value is NaN.
+   All else (arguments, masks, rows that attend nothing, rows past cu_new[B], workspace, limits,
+   errors) as flexq_tree_attention, with the workspace of the function below; INVALID_VALUE also
+   for a negative window or negative sinks. */
+flexq_status flexq_kv4_attention(const uint16_t* q, int32_t dtype, int64_t q_stride_t,
+                                 int64_t q_stride_h, const uint32_t* k_codes,
+                                 const uint32_t* v_codes, const uint16_t* scales,
+                                 int64_t num_pages, int32_t page_size, const int32_t* block_table,
+                                 int64_t max_blocks, const int32_t* ctx_lens,
+                                 const int32_t* cu_new, int64_t B, int64_t T, int64_t max_new,
+                                 int64_t H, int64_t Hkv, int64_t D, const int32_t* tree_mask,
+                                 int64_t mask_words, int64_t window, int64_t sinks, float scale,
+                                 void* workspace, size_t workspace_bytes, uint16_t* out,
+                                 float* lse, void* stream);
+
+/* Bytes of workspace flexq_kv4_attention needs on the current device.  0 for a size that it
+   refuses or that makes it a no-op. */
+size_t flexq_kv4_attention_workspace_bytes(int64_t B, int64_t max_new, int64_t H, int64_t Hkv,
+                                           int64_t D);
+
+/* Low-rank adapters beside a projection shared by many requests:
+     out[t] = y[t] + scales[i] * B_i (A_i x[t]),  i = adapters[t]
+   with the first ranks[i] rows of A_i and columns of B_i (ranks between 0 and R; what A and B
+   hold past them does not matter).  A token whose adapter is outside [0, L) (such as -1) has
+   out[t] = y[t].  Both products sum in fp32; A x enters the second one as two 16-bit parts, within
+   2^-17 of itself (fp16: 2^-22, or 2^-39 of the token's largest, whichever is more); the sum
+   with y is rounded once to dtype.
+     x         [T][K], y and out [T][N] of dtype, rows their stride apart, 16-byte aligned rows;
+               out may be y itself, with the same stride
+     adapters  int32[T], in any order       ranks  int32[L] or NULL (all R)
+     a         [L][R][K], b [L][N][R] of dtype, 16-byte aligned
+     scales    fp32[L] or NULL (all 1)
+     workspace  flexq_lora_add_workspace_bytes(T, N, K, R, L) bytes, 16-byte aligned (NULL
+               where that is 0), overwritten; not to be used by other work until this call's
+               kernels have run
+   Adapters are read once per 64 consecutive tokens.  The result does not depend on the order
+   in which workgroups run.  T == 0 or N == 0 is a no-op.  Errors: INVALID_VALUE (null, negative
+   size, dtype, a stride less than a row with T > 1, workspace too small, an output or the
+   workspace overlapping another argument), UNSUPPORTED (K % 128, N % 16, R % 8, R > 256, K > 2^22,
+   N > 2^24, L > 2^20, T > 4,194,240, strides % 8, alignment). */
+flexq_status flexq_lora_add(const uint16_t* x, int32_t dtype, int64_t x_stride, const uint16_t* y,
+                            int64_t y_stride, const int32_t* adapters, const uint16_t* a,
+                            const uint16_t* b, const int32_t* ranks, const float* scales,
+                            int64_t T, int64_t N, int64_t K, int64_t R, int64_t L,
+                            void* workspace, size_t workspace_bytes, uint16_t* out,
+                            int64_t out_stride, void* stream);
+
+/* Bytes of workspace flexq_lora_add needs on the current device: fp32 sums of slices of K.  0 for
+   a size that it refuses or that makes it a no-op. */
+size_t flexq_lora_add_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L);
 
 #ifdef __cplusplus
 }

@@ -551,5 +551,7 @@ class W6AxLinear:
 
 from .serve import SIGNATURES as SERVE_SIGNATURES  # noqa: E402  (needs the checks above)
 from .serve import (W4Linear, block_tables, gemv_w4, gemv_w4_workspace_bytes,  # noqa: E402,F401
-                    kv_cache, kv_cache_write, pack_w4, tree_attention,
+                    kv4_attention, kv4_attention_workspace_bytes, kv4_cache, kv4_cache_read,
+                    kv4_cache_write, kv_cache, kv_cache_write, lora_add,
+                    lora_add_workspace_bytes, pack_w4, tree_attention,
                     tree_attention_workspace_bytes)

@@ -16,7 +16,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.hip", "pack_quant.hip", "gemm_decode.hip", "gemm_prefill.hip", "group_dots.hip",
            "peaks.hip", "gemm_prefill_ws.hip", "serve_api.hip", "serve_gemv.hip",
-           "serve_cache.hip", "serve_attention.hip"]
+           "serve_cache.hip", "serve_attention.hip", "serve_kv4_cache.hip",
+           "serve_kv4_attention.hip", "serve_lora.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,5 +1,5 @@
 // serve_binding.cpp -- the Python side of the decoding-step calls that run once a layer
-// and step (gemv_w4, block_tables, kv_cache_write, tree_attention): the argument checks,
+// and step (all of serve.py's but pack_w4): the argument checks,
 // output allocation and C call of serve.py's functions without the interpreter between
 // them.  A step's smallest calls take 4 to 10 us on the GPU; checked in Python they took
 // 11 to 22 us of the host's time, here 5 to 11.
@@ -12,13 +12,17 @@
 #include <ATen/ops/empty.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <optional>
 #include <sstream>
 #include <string>
+#include <utility>
 
 #include "../../include/flexq_serve.h"
 
@@ -33,6 +37,12 @@ struct {
   decltype(&flexq_kv_cache_write) kv_cache_write;
   decltype(&flexq_tree_attention) tree_attention;
   decltype(&flexq_tree_attention_workspace_bytes) tree_attention_workspace_bytes;
+  decltype(&flexq_kv4_cache_write) kv4_cache_write;
+  decltype(&flexq_kv4_cache_read) kv4_cache_read;
+  decltype(&flexq_kv4_attention) kv4_attention;
+  decltype(&flexq_kv4_attention_workspace_bytes) kv4_attention_workspace_bytes;
+  decltype(&flexq_lora_add) lora_add;
+  decltype(&flexq_lora_add_workspace_bytes) lora_add_workspace_bytes;
 } library;
 
 // A refused argument, on its way to the interpreter.
@@ -319,79 +329,278 @@ PyObject* kv_cache_write(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
+// The arguments that the attention calls share, checked but for the cache's own: q, the block
+// table and lengths, the masks and the outputs.
+struct Attention {
+  Tensor q, table, ctx, cu, mask, out, lse, ws;
+  int32_t type;
+  at::ScalarType dtype;
+  int64_t T, H, D, B, max_blocks, max_new, words = 0;
+  double scale;
+  bool want_lse;
+
+  Attention(PyObject* query, PyObject* block_table, PyObject* ctx_lens, PyObject* cu_new,
+            PyObject* tree_mask, PyObject* scale_or_none, PyObject* most_new, PyObject* out_or_none,
+            PyObject* lse_or_none, PyObject* return_lse, const Cache& cache) {
+    q = tensor(query, "q");
+    type = half_type(q, "q");
+    dtype = q.scalar_type();
+    rows(q, dtype, "q", 3);
+    T = q.size(0), H = q.size(1), D = q.size(2);
+    value_check(cache.width == D && cache.heads > 0 && H > 0 && H % cache.heads == 0, "q [", T, "][",
+                H, "][", D, "] does not fit a cache of ", cache.heads, " heads of ", cache.width);
+    table = tensor(block_table, "block_table");
+    dims_check(table, 2, "block_table");
+    exact(table, at::kInt, "block_table", table.sizes());
+    B = table.size(0), max_blocks = table.size(1);
+    ctx = exact(tensor(ctx_lens, "ctx_lens"), at::kInt, "ctx_lens", {B});
+    cu = exact(tensor(cu_new, "cu_new"), at::kInt, "cu_new", {B + 1});
+    max_new = given(most_new) ? integer(most_new, "max_new") : T;
+    if (given(tree_mask)) {
+      mask = tensor(tree_mask, "tree_mask");
+      dims_check(mask, 2, "tree_mask");
+      words = mask.size(1);
+      exact(mask, at::kInt, "tree_mask", {T, words});
+      // a mask's bits are as many as one request's tokens may be
+      if (!given(most_new)) max_new = std::min(T, 32 * words);
+      value_check(max_new <= 32 * words, "tree_mask has ", 32 * words, " bits a token; max_new = ",
+                  max_new);
+    }
+    scale = 1.0 / std::sqrt((double)D);
+    if (given(scale_or_none)) {
+      scale = PyFloat_AsDouble(scale_or_none);
+      if (scale == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse(PyExc_TypeError, "scale must be a number, got ", Py_TYPE(scale_or_none)->tp_name);
+      }
+    }
+    if (given(out_or_none)) out = exact(tensor(out_or_none, "out"), dtype, "out", {T, H, D});
+    if (given(lse_or_none)) lse = exact(tensor(lse_or_none, "lse"), at::kFloat, "lse", {T, H});
+    const int truth = PyObject_IsTrue(return_lse);
+    if (truth < 0) {
+      PyErr_Clear();
+      refuse(PyExc_TypeError, "return_lse has no truth value");
+    }
+    want_lse = truth != 0;
+  }
+
+  // Every tensor on one GPU; outputs and the workspace made where the caller brings none.
+  void place(OneGpu& gpu, std::initializer_list<std::pair<const Tensor*, const char*>> cache,
+             PyObject* workspace, int64_t need) {
+    if (given(workspace)) ws = flat(tensor(workspace, "workspace"), at::kByte, "workspace", need);
+    gpu.add(q, "q");
+    for (const auto& c : cache) gpu.add(*c.first, c.second);
+    gpu.add(table, "block_table");
+    gpu.add(ctx, "ctx_lens");
+    gpu.add(cu, "cu_new");
+    if (mask.defined()) gpu.add(mask, "tree_mask");
+    if (!out.defined()) out = make({T, H, D}, dtype, q);
+    gpu.add(out, "out");
+    if (!lse.defined() && want_lse) lse = make({T, H}, at::kFloat, q);
+    if (lse.defined()) gpu.add(lse, "lse");
+    if (!ws.defined()) ws = make({std::max<int64_t>(16, need)}, at::kByte, q);
+    gpu.add(ws, "workspace");
+  }
+
+  const int32_t* mask_data() const { return mask.defined() ? (const int32_t*)data(mask) : nullptr; }
+  float* lse_data() const { return lse.defined() ? (float*)lse.mutable_data_ptr() : nullptr; }
+
+  PyObject* result() const {
+    if (!lse.defined()) return THPVariable_Wrap(out);
+    PyObject* both = PyTuple_New(2);
+    if (!both) return nullptr;
+    PyTuple_SET_ITEM(both, 0, THPVariable_Wrap(out));
+    PyTuple_SET_ITEM(both, 1, THPVariable_Wrap(lse));
+    return both;
+  }
+};
+
 PyObject* tree_attention(PyObject* const* a) {
   const Tensor& q = tensor(a[0], "q");
-  const int32_t type = half_type(q, "q");
-  const at::ScalarType dtype = q.scalar_type();
-  rows(q, dtype, "q", 3);
-  const int64_t T = q.size(0), H = q.size(1), D = q.size(2);
+  half_type(q, "q");
+  rows(q, q.scalar_type(), "q", 3);
   const Tensor &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache");
-  const Cache cache = cache_of(kc, vc, dtype);
-  value_check(cache.width == D && cache.heads > 0 && H > 0 && H % cache.heads == 0, "q [", T, "][",
-              H, "][", D, "] does not fit a cache of ", cache.heads, " heads of ", cache.width);
-  const Tensor& table = tensor(a[3], "block_table");
-  dims_check(table, 2, "block_table");
-  exact(table, at::kInt, "block_table", table.sizes());
-  const int64_t B = table.size(0), max_blocks = table.size(1);
-  const Tensor& ctx = exact(tensor(a[4], "ctx_lens"), at::kInt, "ctx_lens", {B});
-  const Tensor& cu = exact(tensor(a[5], "cu_new"), at::kInt, "cu_new", {B + 1});
-  int64_t max_new = given(a[8]) ? integer(a[8], "max_new") : T;
-  Tensor mask, out, lse, ws;
-  int64_t words = 0;
-  if (given(a[6])) {
-    mask = tensor(a[6], "tree_mask");
-    dims_check(mask, 2, "tree_mask");
-    words = mask.size(1);
-    exact(mask, at::kInt, "tree_mask", {T, words});
-    // a mask's bits are as many as one request's tokens may be
-    if (!given(a[8])) max_new = std::min(T, 32 * words);
-    value_check(max_new <= 32 * words, "tree_mask has ", 32 * words, " bits a token; max_new = ",
-                max_new);
-  }
-  double scale = 1.0 / std::sqrt((double)D);
-  if (given(a[7])) {
-    scale = PyFloat_AsDouble(a[7]);
-    if (scale == -1.0 && PyErr_Occurred()) {
-      PyErr_Clear();
-      refuse(PyExc_TypeError, "scale must be a number, got ", Py_TYPE(a[7])->tp_name);
-    }
-  }
-  if (given(a[9])) out = exact(tensor(a[9], "out"), dtype, "out", {T, H, D});
-  if (given(a[10])) lse = exact(tensor(a[10], "lse"), at::kFloat, "lse", {T, H});
-  const int want_lse = PyObject_IsTrue(a[11]);
-  if (want_lse < 0) return nullptr;
-  const int64_t need =
-      (int64_t)library.tree_attention_workspace_bytes(B, max_new, H, cache.heads, D);
-  if (given(a[12])) ws = flat(tensor(a[12], "workspace"), at::kByte, "workspace", need);
+  const Cache cache = cache_of(kc, vc, q.scalar_type());
+  Attention t(a[0], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11], cache);
   OneGpu gpu;
-  gpu.add(q, "q");
-  gpu.add(kc, "k_cache");
-  gpu.add(vc, "v_cache");
-  gpu.add(table, "block_table");
-  gpu.add(ctx, "ctx_lens");
-  gpu.add(cu, "cu_new");
-  if (mask.defined()) gpu.add(mask, "tree_mask");
-  if (!out.defined()) out = make({T, H, D}, dtype, q);
-  gpu.add(out, "out");
-  if (!lse.defined() && want_lse) lse = make({T, H}, at::kFloat, q);
-  if (lse.defined()) gpu.add(lse, "lse");
-  if (!ws.defined()) ws = make({std::max<int64_t>(16, need)}, at::kByte, q);
-  gpu.add(ws, "workspace");
+  t.place(gpu, {{&kc, "k_cache"}, {&vc, "v_cache"}}, a[12],
+          (int64_t)library.tree_attention_workspace_bytes(t.B, t.max_new, t.H, cache.heads, t.D));
   Current current(gpu.index());
   const flexq_status status = library.tree_attention(
-      (const uint16_t*)data(q), type, q.stride(0), q.stride(1), (const uint16_t*)data(kc),
-      (const uint16_t*)data(vc), cache.pages, cache.page_size, (const int32_t*)data(table),
-      max_blocks, (const int32_t*)data(ctx), (const int32_t*)data(cu), B, T, max_new, H,
-      cache.heads, D, mask.defined() ? (const int32_t*)data(mask) : nullptr, words, (float)scale,
-      ws.mutable_data_ptr(), ws.numel(), (uint16_t*)out.mutable_data_ptr(),
-      lse.defined() ? (float*)lse.mutable_data_ptr() : nullptr, stream_of(gpu.index()));
+      (const uint16_t*)data(q), t.type, q.stride(0), q.stride(1), (const uint16_t*)data(kc),
+      (const uint16_t*)data(vc), cache.pages, cache.page_size, (const int32_t*)data(t.table),
+      t.max_blocks, (const int32_t*)data(t.ctx), (const int32_t*)data(t.cu), t.B, t.T, t.max_new,
+      t.H, cache.heads, t.D, t.mask_data(), t.words, (float)t.scale, t.ws.mutable_data_ptr(),
+      t.ws.numel(), (uint16_t*)t.out.mutable_data_ptr(), t.lse_data(), stream_of(gpu.index()));
   if (status != FLEXQ_SUCCESS) return raise_status(status, "flexq_tree_attention");
-  if (!lse.defined()) return THPVariable_Wrap(out);
+  return t.result();
+}
+
+// codes [pages][Hkv][page_size/16][16][D/8] and [..][2][D/2][2], scales [..][4][16]
+Cache kv4_cache_of(const Tensor& k, const Tensor& v, const Tensor& s) {
+  value_check(k.dim() == 5, "k_codes must be a 5-D tensor [pages][Hkv][page_size/16][16][D/8]");
+  const int64_t blocks = k.size(2), D = 8 * k.size(4);
+  const bool page = blocks == 1 || blocks == 2 || blocks == 4 || blocks == 8 || blocks == 16;
+  const bool width = D == 64 || D == 96 || D == 128 || D == 256;
+  value_check(page && width && k.size(3) == 16,
+              "k_codes must be [pages][Hkv][page_size/16][16][D/8] with page_size one of (16, 32, "
+              "64, 128, 256) and D one of (64, 96, 128, 256), got ",
+              shape_text(k.sizes()));
+  exact(k, at::kInt, "k_codes", k.sizes());
+  exact(v, at::kInt, "v_codes", {k.size(0), k.size(1), blocks, 2, D / 2, 2});
+  exact(s, at::kHalf, "scales", {k.size(0), k.size(1), blocks, 4, 16});
+  return {k.size(0), k.size(1), D, (int32_t)(16 * blocks)};
+}
+
+PyObject* kv4_cache_write(PyObject* const* a) {
+  const Tensor& k = tensor(a[0], "k");
+  const Tensor& v = tensor(a[1], "v");
+  const int32_t type = half_type(k, "k");
+  const at::ScalarType dtype = k.scalar_type();
+  rows(k, dtype, "k", 3);
+  const Tensor &kc = tensor(a[3], "k_codes"), &vc = tensor(a[4], "v_codes");
+  const Tensor& sc = tensor(a[5], "scales");
+  const Cache cache = kv4_cache_of(kc, vc, sc);
+  const int64_t T = k.size(0);
+  const int64_t shape[3] = {T, cache.heads, cache.width};
+  value_check(k.sizes() == at::IntArrayRef(shape), "k must have shape ", shape_text(shape),
+              ", got ", shape_text(k.sizes()));
+  rows(v, dtype, "v", 3);
+  value_check(v.sizes() == k.sizes(), "v must have shape ", shape_text(shape), ", got ",
+              shape_text(v.sizes()));
+  const Tensor& slots = exact(tensor(a[2], "slot_map"), at::kInt, "slot_map", {T});
+  OneGpu gpu;
+  gpu.add(k, "k");
+  gpu.add(v, "v");
+  gpu.add(slots, "slot_map");
+  gpu.add(kc, "k_codes");
+  gpu.add(vc, "v_codes");
+  gpu.add(sc, "scales");
+  Current current(gpu.index());
+  const flexq_status status = library.kv4_cache_write(
+      (const uint16_t*)data(k), k.stride(0), k.stride(1), (const uint16_t*)data(v), v.stride(0),
+      v.stride(1), type, (const int32_t*)data(slots), T, cache.heads, cache.width, cache.pages,
+      cache.page_size, (uint32_t*)kc.mutable_data_ptr(), (uint32_t*)vc.mutable_data_ptr(),
+      (uint16_t*)sc.mutable_data_ptr(), stream_of(gpu.index()));
+  if (status != FLEXQ_SUCCESS) return raise_status(status, "flexq_kv4_cache_write");
+  Py_RETURN_NONE;
+}
+
+PyObject* kv4_cache_read(PyObject* const* a) {
+  const Tensor &kc = tensor(a[1], "k_codes"), &vc = tensor(a[2], "v_codes");
+  const Tensor& sc = tensor(a[3], "scales");
+  const Cache cache = kv4_cache_of(kc, vc, sc);
+  const Tensor& slots = tensor(a[0], "slot_map");
+  dims_check(slots, 1, "slot_map");
+  exact(slots, at::kInt, "slot_map", slots.sizes());
+  const int64_t T = slots.size(0);
+  value_check(THPDtype_Check(a[4]), "dtype must be torch.float16 or torch.bfloat16");
+  const at::ScalarType dtype = reinterpret_cast<THPDtype*>(a[4])->scalar_type;
+  value_check(dtype == at::kHalf || dtype == at::kBFloat16,
+              "dtype must be torch.float16 or torch.bfloat16, got ", dtype_text(dtype));
+  const int64_t shape[3] = {T, cache.heads, cache.width};
+  OneGpu gpu;
+  Tensor k, v;
+  if (given(a[5])) k = exact(tensor(a[5], "k"), dtype, "k", shape);
+  if (given(a[6])) v = exact(tensor(a[6], "v"), dtype, "v", shape);
+  gpu.add(slots, "slot_map");
+  gpu.add(kc, "k_codes");
+  gpu.add(vc, "v_codes");
+  gpu.add(sc, "scales");
+  if (!k.defined()) k = make(shape, dtype, slots);
+  if (!v.defined()) v = make(shape, dtype, slots);
+  gpu.add(k, "k");
+  gpu.add(v, "v");
+  Current current(gpu.index());
+  const flexq_status status = library.kv4_cache_read(
+      (const uint32_t*)data(kc), (const uint32_t*)data(vc), (const uint16_t*)data(sc),
+      (const int32_t*)data(slots), T, cache.heads, cache.width, cache.pages, cache.page_size,
+      dtype == at::kHalf ? FLEXQ_FP16 : FLEXQ_BF16, (uint16_t*)k.mutable_data_ptr(),
+      (uint16_t*)v.mutable_data_ptr(), stream_of(gpu.index()));
+  if (status != FLEXQ_SUCCESS) return raise_status(status, "flexq_kv4_cache_read");
   PyObject* both = PyTuple_New(2);
   if (!both) return nullptr;
-  PyTuple_SET_ITEM(both, 0, THPVariable_Wrap(out));
-  PyTuple_SET_ITEM(both, 1, THPVariable_Wrap(lse));
+  PyTuple_SET_ITEM(both, 0, THPVariable_Wrap(k));
+  PyTuple_SET_ITEM(both, 1, THPVariable_Wrap(v));
   return both;
+}
+
+PyObject* kv4_attention(PyObject* const* a) {
+  const Tensor &kc = tensor(a[1], "k_codes"), &vc = tensor(a[2], "v_codes");
+  const Tensor& sc = tensor(a[3], "scales");
+  const Cache cache = kv4_cache_of(kc, vc, sc);
+  Attention t(a[0], a[4], a[5], a[6], a[7], a[8], a[9], a[12], a[13], a[14], cache);
+  // (none is 0 in C)
+  const int64_t window = given(a[10]) ? integer(a[10], "window") : 0;
+  value_check(!given(a[10]) || window > 0, "window = ", window, " must be positive, or None");
+  const int64_t sinks = integer(a[11], "sinks");
+  value_check(sinks >= 0, "sinks = ", sinks, " must not be negative");
+  OneGpu gpu;
+  t.place(gpu, {{&kc, "k_codes"}, {&vc, "v_codes"}, {&sc, "scales"}}, a[15],
+          (int64_t)library.kv4_attention_workspace_bytes(t.B, t.max_new, t.H, cache.heads, t.D));
+  Current current(gpu.index());
+  const flexq_status status = library.kv4_attention(
+      (const uint16_t*)data(t.q), t.type, t.q.stride(0), t.q.stride(1), (const uint32_t*)data(kc),
+      (const uint32_t*)data(vc), (const uint16_t*)data(sc), cache.pages, cache.page_size,
+      (const int32_t*)data(t.table), t.max_blocks, (const int32_t*)data(t.ctx),
+      (const int32_t*)data(t.cu), t.B, t.T, t.max_new, t.H, cache.heads, t.D, t.mask_data(),
+      t.words, window, sinks, (float)t.scale, t.ws.mutable_data_ptr(), t.ws.numel(),
+      (uint16_t*)t.out.mutable_data_ptr(), t.lse_data(), stream_of(gpu.index()));
+  if (status != FLEXQ_SUCCESS) return raise_status(status, "flexq_kv4_attention");
+  return t.result();
+}
+
+PyObject* lora_add(PyObject* const* p) {
+  const Tensor& x = tensor(p[0], "x");
+  const int32_t type = half_type(x, "x");
+  const at::ScalarType dtype = x.scalar_type();
+  rows(x, dtype, "x", 2);
+  const int64_t T = x.size(0), K = x.size(1);
+  const Tensor& y = rows(tensor(p[1], "y"), dtype, "y", 2);
+  value_check(y.size(0) == T, "y must have ", T, " rows, got shape ", shape_text(y.sizes()));
+  const int64_t N = y.size(1);
+  value_check(K > 0 && K % 128 == 0, "lora_add: K = ", K, " must be a positive multiple of 128");
+  value_check(N % 16 == 0, "N = ", N, " must be a multiple of 16");
+  const Tensor& adapters = exact(tensor(p[2], "adapters"), at::kInt, "adapters", {T});
+  const Tensor& a = tensor(p[3], "a");
+  dims_check(a, 3, "a");
+  const int64_t L = a.size(0), R = a.size(1);
+  value_check(R > 0 && R % 8 == 0 && R <= 256, "a has rank ", R,
+              ", which must be a multiple of 8 up to 256");
+  exact(a, dtype, "a", {L, R, K});
+  const Tensor& b = exact(tensor(p[4], "b"), dtype, "b", {L, N, R});
+  OneGpu gpu;
+  gpu.add(x, "x");
+  gpu.add(y, "y");
+  gpu.add(adapters, "adapters");
+  gpu.add(a, "a");
+  gpu.add(b, "b");
+  Tensor ranks, scales, out = y, ws;
+  if (given(p[5])) gpu.add(ranks = exact(tensor(p[5], "ranks"), at::kInt, "ranks", {L}), "ranks");
+  if (given(p[6]))
+    gpu.add(scales = exact(tensor(p[6], "scales"), at::kFloat, "scales", {L}), "scales");
+  if (given(p[7])) {
+    out = rows(tensor(p[7], "out"), dtype, "out", 2);
+    value_check(out.sizes() == y.sizes(), "out must have shape ", shape_text(y.sizes()), ", got ",
+                shape_text(out.sizes()));
+    gpu.add(out, "out");
+  }
+  const int64_t need = (int64_t)library.lora_add_workspace_bytes(T, N, K, R, L);
+  if (given(p[8]))
+    ws = flat(tensor(p[8], "workspace"), at::kByte, "workspace", need);
+  else if (need > 0)
+    ws = make({need}, at::kByte, x);
+  if (ws.defined()) gpu.add(ws, "workspace");
+  Current current(gpu.index());
+  const flexq_status status = library.lora_add(
+      (const uint16_t*)data(x), type, x.stride(0), (const uint16_t*)data(y), y.stride(0),
+      (const int32_t*)data(adapters), (const uint16_t*)data(a), (const uint16_t*)data(b),
+      ranks.defined() ? (const int32_t*)data(ranks) : nullptr,
+      scales.defined() ? (const float*)data(scales) : nullptr, T, N, K, R, L,
+      ws.defined() ? ws.mutable_data_ptr() : nullptr, ws.defined() ? ws.numel() : 0,
+      (uint16_t*)out.mutable_data_ptr(), out.stride(0), stream_of(gpu.index()));
+  if (status != FLEXQ_SUCCESS) return raise_status(status, "flexq_lora_add");
+  return THPVariable_Wrap(out);
 }
 
 template <class F>
@@ -406,6 +615,12 @@ PyObject* bind(PyObject* const* a) {
   take(library.kv_cache_write, a[3]);
   take(library.tree_attention, a[4]);
   take(library.tree_attention_workspace_bytes, a[5]);
+  take(library.kv4_cache_write, a[6]);
+  take(library.kv4_cache_read, a[7]);
+  take(library.kv4_attention, a[8]);
+  take(library.kv4_attention_workspace_bytes, a[9]);
+  take(library.lora_add, a[10]);
+  take(library.lora_add_workspace_bytes, a[11]);
   if (PyErr_Occurred()) return nullptr;
   Py_RETURN_NONE;
 }
@@ -434,8 +649,10 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {
-    method<bind, 6>("bind"), method<gemv_w4, 6>("gemv_w4"), method<block_tables, 10>("block_tables"),
+    method<bind, 12>("bind"), method<gemv_w4, 6>("gemv_w4"), method<block_tables, 10>("block_tables"),
     method<kv_cache_write, 5>("kv_cache_write"), method<tree_attention, 13>("tree_attention"),
+    method<kv4_cache_write, 6>("kv4_cache_write"), method<kv4_cache_read, 7>("kv4_cache_read"),
+    method<kv4_attention, 16>("kv4_attention"), method<lora_add, 9>("lora_add"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve", nullptr, -1, methods,

@@ -10,6 +10,9 @@ that run once a layer and step the checks are in ``_serve.so`` (csrc/serve_bindi
 * :func:`kv_cache`, :func:`kv_cache_write`  the paged cache and the writing of new tokens
 * :func:`tree_attention`   attention of drafted tokens (one token, a chain or a tree)
   over the paged cache
+* :func:`kv4_cache`, :func:`kv4_cache_write`, :func:`kv4_cache_read`, :func:`kv4_attention`
+  the same over a cache of 4-bit codes, with an optional sliding window
+* :func:`lora_add`         low-rank adapters of many requests, added to a layer's output
 """
 from __future__ import annotations
 
@@ -38,6 +41,17 @@ SIGNATURES = {
                                             _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _I64,
                                             _F, _P, _SZ, _P, _P, _P]),
     "flexq_tree_attention_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "flexq_kv4_cache_write": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I64, _I32, _P, _I64, _I64,
+                                             _I64, _I64, _I32, _P, _P, _P, _P]),
+    "flexq_kv4_cache_read": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32, _I32, _P,
+                                            _P, _P]),
+    "flexq_kv4_attention": (ctypes.c_int, [_P, _I32, _I64, _I64, _P, _P, _P, _I64, _I32, _P, _I64,
+                                           _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _I64,
+                                           _I64, _I64, _F, _P, _SZ, _P, _P, _P]),
+    "flexq_kv4_attention_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "flexq_lora_add": (ctypes.c_int, [_P, _I32, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _I64,
+                                      _I64, _I64, _I64, _P, _SZ, _P, _I64, _P]),
+    "flexq_lora_add_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
 }
 
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1}
@@ -72,7 +86,10 @@ def _native():
         module.bind(*(ctypes.cast(getattr(lib, f"flexq_{name}"), ctypes.c_void_p).value
                       for name in ("gemv_w4", "gemv_w4_workspace_bytes", "block_tables",
                                    "kv_cache_write", "tree_attention",
-                                   "tree_attention_workspace_bytes")))
+                                   "tree_attention_workspace_bytes", "kv4_cache_write",
+                                   "kv4_cache_read", "kv4_attention",
+                                   "kv4_attention_workspace_bytes", "lora_add",
+                                   "lora_add_workspace_bytes")))
         _calls = module
     return _calls
 
@@ -204,3 +221,71 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     return (_calls or _native()).tree_attention(q, k_cache, v_cache, block_table, ctx_lens,
                                                 cu_new, tree_mask, scale, max_new, out, lse,
                                                 return_lse, workspace)
+
+
+def kv4_cache(num_pages: int, Hkv: int, D: int, page_size: int, device="cuda"):
+    """An empty paged cache of 4-bit codes, for fp16 and bf16 models alike: (k_codes int32
+    [pages][Hkv][page_size/16][16][D/8], v_codes int32 [pages][Hkv][page_size/16][2][D/2][2],
+    scales fp16 [pages][Hkv][page_size/16][4][16])."""
+    if page_size not in PAGE_SIZES or D not in HEAD_WIDTHS:
+        raise ValueError(f"page_size must be one of {PAGE_SIZES} and D one of {HEAD_WIDTHS}")
+    lead = (num_pages, Hkv, page_size // 16)
+    return (torch.empty((*lead, 16, D // 8), dtype=torch.int32, device=device),
+            torch.empty((*lead, 2, D // 2, 2), dtype=torch.int32, device=device),
+            torch.empty((*lead, 4, 16), dtype=torch.float16, device=device))
+
+
+def kv4_cache_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
+                    k_codes: torch.Tensor, v_codes: torch.Tensor, scales: torch.Tensor):
+    """Keys and values k, v [T][Hkv][D] into the 4-bit cache at the slots slot_map int32[T]
+    (flexq_kv4_cache_write), each token and head with a scale and an offset of its own; negative
+    slots drop their token, and the others should differ.  k and v may be strided over tokens
+    and heads."""
+    (_calls or _native()).kv4_cache_write(k, v, slot_map, k_codes, v_codes, scales)
+
+
+def kv4_cache_read(slot_map: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor,
+                   scales: torch.Tensor, dtype=torch.float16, k: torch.Tensor | None = None,
+                   v: torch.Tensor | None = None):
+    """The cache's tokens at slot_map int32[T] as rows of `dtype` (flexq_kv4_cache_read): what
+    :func:`kv4_attention` sees of them.  Slots outside the cache read as 0.  Returns (k, v)
+    [T][Hkv][D]."""
+    return (_calls or _native()).kv4_cache_read(slot_map, k_codes, v_codes, scales, dtype, k, v)
+
+
+def kv4_attention_workspace_bytes(B: int, max_new: int, H: int, Hkv: int, D: int) -> int:
+    return int(_fq.lib().flexq_kv4_attention_workspace_bytes(B, max_new, H, Hkv, D))
+
+
+def kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor,
+                  scales: torch.Tensor, block_table: torch.Tensor, ctx_lens: torch.Tensor,
+                  cu_new: torch.Tensor, tree_mask: torch.Tensor | None = None,
+                  scale: float | None = None, max_new: int | None = None,
+                  window: int | None = None, sinks: int = 0, out: torch.Tensor | None = None,
+                  lse: torch.Tensor | None = None, return_lse: bool = False,
+                  workspace: torch.Tensor | None = None):
+    """:func:`tree_attention` over the 4-bit cache (flexq_kv4_attention), q fp16 or bf16.
+
+    With a window a token attends the last `window` positions, its own among them, and the
+    first `sinks` of its request; the keys between are not read.  In a tree the drafted
+    tokens that a token attends are the last of its window's positions, and are attended
+    whatever the window."""
+    return (_calls or _native()).kv4_attention(q, k_codes, v_codes, scales, block_table, ctx_lens,
+                                               cu_new, tree_mask, scale, max_new, window, sinks,
+                                               out, lse, return_lse, workspace)
+
+
+def lora_add_workspace_bytes(T: int, N: int, K: int, R: int, L: int) -> int:
+    return int(_fq.lib().flexq_lora_add_workspace_bytes(T, N, K, R, L))
+
+
+def lora_add(x: torch.Tensor, y: torch.Tensor, adapters: torch.Tensor, a: torch.Tensor,
+             b: torch.Tensor, ranks: torch.Tensor | None = None,
+             scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None):
+    """The requests' own low-rank adapters beside a layer they share (flexq_lora_add): token t
+    of x [T][K] with adapter i = adapters[t] (int32; none where that is outside [0, L)) adds
+    scales[i] * b[i] (a[i] x[t]) to y[t] [N], a [L][R][K] and b [L][N][R] of which the first
+    ranks[i] rows and columns count (all R where ranks is None).  x and y are fp16 or bf16 and may
+    be strided rows.  In place on y unless `out` is given; returns it."""
+    return (_calls or _native()).lora_add(x, y, adapters, a, b, ranks, scales, out, workspace)
