@@ -216,7 +216,8 @@ flexq_status flexq_kv4_cache_write(const uint16_t* k, int64_t k_stride_t, int64_
                                    void* stream);
 
 /* The tokens at slots slot_map[0 .. T) of the 4-bit cache as rows of dtype, b + s c rounded
-   once: what attention over the cache sees of them.  A slot outside the cache reads as 0.
+   once: what attention over the cache sees of them.  A slot outside the cache reads as 0.  (The
+   last code of a row that reaches fp16's largest value may stand for more, infinite in fp16.)
      k, v      [T][Hkv][D] of dtype, 16-byte aligned (output)
    T == 0 is a no-op.  Errors: INVALID_VALUE (null, negative size, dtype, overlap), UNSUPPORTED
    (D, page_size, sizes as flexq_kv_cache_write, alignment). */
@@ -234,8 +235,8 @@ flexq_status flexq_kv4_cache_read(const uint32_t* k_codes, const uint32_t* v_cod
    sinks   with a window, the first `sinks` tokens of the request stay visible; without one it
            plays no part.
    Keys that no token's window holds are not read.  Scores, statistics and sums are fp32; the
-   queries enter with 11 bits or more down to 2^-28 of a row's largest; probabilities times the
-   values' scales enter their product as two fp16 parts, within 2^-22 of themselves or 2^-35 of
+   queries enter whole down to 2^-24 of a row's largest, and below within 2^-34 of it; probabilities
+   times the values' scales enter their product as two fp16 parts, within 2^-22 of themselves or 2^-35 of
    the row's largest, whichever is more; out is rounded once.  What masked places, unused
    slots and pages hold does not matter.  A row that attends a NaN key or value is NaN.
    All else (arguments, masks, rows that attend nothing, rows past cu_new[B], workspace, limits,

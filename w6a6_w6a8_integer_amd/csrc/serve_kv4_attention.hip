@@ -8,7 +8,7 @@
 // so both products are MFMAs on c - 8, which fp16 holds exactly, whatever the tensors' type, and the
 // scales meet scores and probabilities.  (c - 8 rather than c: sums of codes of one sign would
 // err with their size, not their result's.)  The queries enter as fp16 after a row's power of
-// two: exact for bfloat16, and for fp16, but for what is below 2^-28 of the row's largest.
+// two, whole down to 2^-24 of the row's largest and below within 2^-34 of it.
 // w_j = p_j s_j enters as the sum of two fp16 parts, within 2^-22 of itself or 2^-35 of the row's
 // largest, whichever is more.
 //
@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kWaves = 4;
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 // A row's largest w is held as 2^(kTop - 1) to 2^(kTop + kLag): fp16 reaches no further up, and
 // down to 2^-24, so that small ones keep their bits.
@@ -48,6 +49,9 @@ struct Codes {
     return __builtin_bit_cast(uint32_t, v - f16x2{1152.0f16, 1152.0f16});
   }
 };
+
+// (by value: a bit cast of a vector's element takes the whole vector's first bits)
+__device__ __forceinline__ f16x2 pair_of(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
 
 __device__ __forceinline__ float half_at(const u32x4& v, int e) {
   return half_bits_to_float((uint16_t)(e & 1 ? v[e >> 1] >> 16 : v[e >> 1] & 0xFFFFu));
@@ -123,6 +127,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
   const uint32_t* vc = reinterpret_cast<const uint32_t*>(a.vc) + (p & 1) * D;
   const uint16_t* sc = a.scales + (p & 1) * 8;
   const int key_half = c >> 3, value_half = p >> 1;
+  float zero = 0.0f;  // the compiler's own zero would keep p s from being one instruction
+  asm("" : "+v"(zero));
 
   for (; b < a.B && before < share_end; ++b) {
     if ((uint32_t)(b - window.base) >= 64u) {
@@ -338,10 +344,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
         float top = raw[g][0];
 #pragma unroll
         for (int e = 1; e < 8; ++e) top = fmaxf(top, raw[g][e]);
-        f16x2 most = __builtin_bit_cast(f16x2, vs[g][0]);
+        // (scales are not negative: their bits are in their order)
+        u16x2 most = {0, 0};
 #pragma unroll
-        for (int i = 1; i < 4; ++i) most = __builtin_elementwise_max(most, __builtin_bit_cast(f16x2, vs[g][i]));
-        const float scale = fmaxf((float)most[0], (float)most[1]);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t two = vs[g][i];
+          most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, two));
+        }
+        const float scale = half_bits_to_float(most[0] > most[1] ? most[0] : most[1]);
         top = fmaf(top, by[g], (float)__builtin_amdgcn_frexp_expf(scale));
         if (__ballot(top > m[g] + kLag)) {  // rare after a request's first step
           top = row_max<16>(top);
@@ -358,17 +368,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
         const float ref = m[g] == -INFINITY ? 0.0f : kTop - m[g];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          float prob[2], step[2];
           f16x2 h, rest;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float prob = __builtin_amdgcn_exp2f(fmaf(raw[g][2 * i + j], by[g], ref));
-            const float step = half_at(vs[g], 2 * i + j);
-            l[g] += prob;
-            B[g] = fmaf(prob, fmaf(step, 8.0f, half_at(vb[g], 2 * i + j)), B[g]);
-            h[j] = (_Float16)(prob * step);
-            rest[j] = (_Float16)fmaf(prob, step, -(float)h[j]);
+            prob[j] = __builtin_amdgcn_exp2f(fmaf(raw[g][2 * i + j], by[g], ref));
+            step[j] = half_at(vs[g], 2 * i + j);
+            l[g] += prob[j];
+            B[g] = fmaf(prob[j], fmaf(step[j], 8.0f, half_at(vb[g], 2 * i + j)), B[g]);
+            h[j] = (_Float16)fmaf(prob[j], step[j], zero);
           }
-          hi[g][i] = __builtin_bit_cast(uint32_t, h);
+          uint32_t bits = __builtin_bit_cast(uint32_t, h);
+          asm("" : "+v"(bits));  // the very bits that the product takes are what is left out of the rest
+          hi[g][i] = bits;
+          h = pair_of(bits);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) rest[j] = (_Float16)fmaf(prob[j], step[j], -(float)h[j]);
           lo[g][i] = __builtin_bit_cast(uint32_t, rest);
         }
       }
