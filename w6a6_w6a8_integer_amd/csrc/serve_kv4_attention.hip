@@ -16,8 +16,8 @@
 // (1024 + c, or 1024 + 16 c of the next four bits), and one addition of a pair takes the rest
 // off, leaving c - 8 or 16 (c - 8).  The factor 16 goes into the queries or out of the sums.
 //
-// A wave takes 32-key steps straight from memory into registers, the next step's loads on
-// their way while one is worked on, and needs no barrier until a request's end.  Rows are
+// A wave stages its own 32-key steps in LDS straight from memory, S - 1 of them on their way while one
+// is worked on, and needs no barrier until a request's end.  Rows are
 // columns of the MFMAs (16 a group), so a lane owns one row's statistics, and the keys are
 // dealt to the score tiles' rows so that a lane's scores are those that its fragment of P takes:
 // row r of score tile t holds key 8 (r / 4) + 4 t + r % 4, lane l keys 8 (l / 16) .. + 7.  Waves
@@ -29,6 +29,7 @@ namespace flexq {
 namespace {
 
 constexpr int kWaves = 4;
+typedef __attribute__((address_space(1))) const void* global_ptr_t;
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
@@ -36,49 +37,46 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 // down to 2^-24, so that small ones keep their bits.
 constexpr float kTop = 11.0f, kLag = 4.0f;
 
-// Eight codes of a dword, four instructions and a shift each for c - 8 (even pairs: low four
-// bits of the bytes) and 16 (c - 8).
-struct Codes {
-  uint32_t base = 0x64006400u;
-  __device__ __forceinline__ uint32_t low(uint32_t w) const {
-    const f16x2 v = __builtin_bit_cast(f16x2, (w & 0x000F000Fu) | base);
-    return __builtin_bit_cast(uint32_t, v - f16x2{1032.0f16, 1032.0f16});
-  }
-  __device__ __forceinline__ uint32_t high(uint32_t w) const {
-    const f16x2 v = __builtin_bit_cast(f16x2, (w & 0x00F000F0u) | base);
-    return __builtin_bit_cast(uint32_t, v - f16x2{1152.0f16, 1152.0f16});
-  }
-};
+// Workgroups a compute unit holds.
+constexpr int units_per_cu(int64_t D, int groups) { return groups == 1 && D <= 128 ? 3 : 2; }
 
 // (by value: a bit cast of a vector's element takes the whole vector's first bits)
 __device__ __forceinline__ f16x2 pair_of(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
+
+// Eight codes of a dword, four pairs: c - 8 from the low four bits of its bytes, 16 (c - 8) from the
+// high ones.  The constants sit in registers: as literals they would take an and and an or.
+struct Codes {
+  uint32_t base = 0x64006400u, low_bits = 0x000F000Fu, high_bits = 0x00F000F0u;
+  __device__ __forceinline__ Codes() {
+    asm("" : "+v"(base));
+    asm("" : "+s"(low_bits));
+    asm("" : "+s"(high_bits));
+  }
+  __device__ __forceinline__ uint32_t low(uint32_t w) const {
+    return __builtin_bit_cast(uint32_t, pair_of((w & low_bits) | base) - f16x2{1032.0f16, 1032.0f16});
+  }
+  __device__ __forceinline__ uint32_t high(uint32_t w) const {
+    return __builtin_bit_cast(uint32_t, pair_of((w & high_bits) | base) - f16x2{1152.0f16, 1152.0f16});
+  }
+};
 
 __device__ __forceinline__ float half_at(const u32x4& v, int e) {
   return half_bits_to_float((uint16_t)(e & 1 ? v[e >> 1] >> 16 : v[e >> 1] & 0xFFFFu));
 }
 
-// What a lane holds of a 32-key step: key dwords of tile t (consecutive eights of its quarter of D),
-// value dwords (pairs of d, four keys each), scales and offsets of its eight keys.
+// A 32-key step as a wave stages it in LDS: the codes of the keys' two 16-token blocks, of the
+// values', and both blocks' scales, in 16-byte pieces as they lie in memory, but for the key rows of
+// 64 and 128 bytes, whose pieces change places by their row so that the eight rows that
+// eight lanes read at once meet different banks.
 template <int DT>
-struct Step {
-  uint32_t k[2][DT];
-  uint32_t v[2 * DT];
-  u32x4 ks, kb, vs, vb;
-  int index;      // of the step in the request
-  uint32_t hole;  // bit h: no page behind keys 16 h ..
-};
-
-template <int N>
-__device__ __forceinline__ void load_dwords(uint32_t (&to)[N], int at, const uint32_t* from, int n) {
-  if (n == 4) {
-    const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) to[at + i] = v[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < n; ++i) to[at + i] = from[i];
+struct Stage {
+  static constexpr int D = 32 * DT;
+  static constexpr int kBytes = 32 * D + 256;
+  static constexpr int kLoads = DT + 1;  // that a wave issues for a step
+  static __device__ __forceinline__ int swizzle(int row) {
+    return DT == 4 ? (row >> 1 & 1) | (row >> 3 & 1) << 1 : DT == 8 ? (row & 3) | (row >> 3 & 1) << 2 : 0;
   }
-}
+};
 
 }  // namespace
 
@@ -92,8 +90,8 @@ __device__ __forceinline__ int window_gap(const Kv4AttentionArgs& a, const Reque
 
 // One workgroup = one share of the cache, key head and block of rows: KW of its waves take the steps in
 // turn, 4 / KW the rows, RG groups of 16 each.
-template <int DT, int RG>
-__global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4AttentionArgs a,
+template <int DT, int RG, int S>
+__global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_attention_kernel(const Kv4AttentionArgs a,
                                                                       int shares, int row_blocks,
                                                                       int key_waves) {
   constexpr int D = 32 * DT;
@@ -121,12 +119,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
   const Parts parts = parts_of(a, shares, a.max_new * group);
   const int per_page = 1 << (a.page_shift - 4);  // 16-token blocks of a page
 
-  // a lane's places in a block of 2 D dwords of codes and 64 scales
-  const uint32_t* kc = reinterpret_cast<const uint32_t*>(a.kc) +
-                       (8 * (c >> 2 & 1) + (c & 3)) * (D / 8) + p * DT;
-  const uint32_t* vc = reinterpret_cast<const uint32_t*>(a.vc) + (p & 1) * D;
-  const uint16_t* sc = a.scales + (p & 1) * 8;
-  const int key_half = c >> 3, value_half = p >> 1;
+  // This wave's stages, and the lane's places in one: its first key's quarter row (the other
+  // key's is four rows on), its eight keys' value pairs, their scales.
+  using Staged = Stage<DT>;
+  char* const ring = lds + wave * (S * Staged::kBytes);
+  const int key_row = 8 * (c >> 2 & 1) + (c & 3);
+  const int key_at = (c >> 3) * 8 * D + key_row * (D / 2);
+  const int value_at = 16 * D + (p >> 1) * 8 * D + (p & 1) * 4 * D;
+  const int scale_at = 32 * D + (p >> 1) * 128 + (p & 1) * 16;
+  const Codes codes;
   float zero = 0.0f;  // the compiler's own zero would keep p s from being one instruction
   asm("" : "+v"(zero));
 
@@ -167,6 +168,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
     int tok[RG];
     bool in[RG];
     float Q[RG], by[RG];       // sum of the fp16 queries; from raw scores to exponents of 2
+    u32x4 loaded[RG][DT];
     uint32_t q[RG][DT][4];
     int since[RG];             // first key of the row's window
 #pragma unroll
@@ -176,14 +178,81 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
       const int64_t at = (int64_t)cu + tok[g];
       in[g] = row < rows && at >= 0 && at < a.T;
       const uint16_t* from = a.q + at * a.q_st + (int64_t)(hk * group + row % group) * a.q_sh + p * 8 * DT;
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+        loaded[g][i] = in[g] ? *reinterpret_cast<const u32x4*>(from + 8 * i) : u32x4{};
+    }
+
+    const scalar_ptr_t table = (scalar_ptr_t)(a.table + (int64_t)b * a.max_blocks);
+    auto page_of = [&](int step, int half) {
+      const int pos = step * 32 + half * 16;
+      return pos < len ? table[pos >> a.page_shift] : -1;
+    };
+    auto block_of = [&](int page, int step, int half) {
+      if ((unsigned)page >= (unsigned)a.num_pages) return -1;
+      return (page * a.Hkv + hk) * per_page + ((step * 2 + half) & (per_page - 1));
+    };
+    auto next = [&](int v) { return following(v + key_waves); };
+    const int first = following(begin + key_wave);
+    const bool works = row0 < rows && first < end;
+    int ahead = min(first, end - 1);  // the next step to be staged, and its pages
+    int page0 = page_of(actual(ahead), 0), page1 = page_of(actual(ahead), 1);
+    uint32_t holes = 0;  // bit 2 slot + h: no page behind the staged step's keys 16 h ..
+    // Stages the step `ahead`, and fetches the pages of the one after it.
+    auto stage = [&](int slot) {
+      const int step = actual(ahead);
+      const int b0 = block_of(page0, step, 0), b1 = block_of(page1, step, 1);
+      holes = (holes & ~(3u << 2 * slot)) | ((b0 < 0 ? 1u : 0u) | (b1 < 0 ? 2u : 0u)) << 2 * slot;
+      const int64_t at0 = (int64_t)max(b0, 0) * (8 * D), at1 = (int64_t)max(b1, 0) * (8 * D);
+      const char* keys = reinterpret_cast<const char*>(a.kc);
+      const char* values = reinterpret_cast<const char*>(a.vc);
+      char* const to = ring + slot * Staged::kBytes;
+#pragma unroll
+      for (int u = 0; u < DT; ++u) {
+        const char* from;
+        if constexpr (DT % 4 == 0) {  // whole kilobytes of one block
+          constexpr int kEach = DT / 4;
+          const int part = u % kEach, i = 64 * part + lane;
+          const int row = i / (DT / 4 * 4), piece = i % (DT / 4 * 4) ^ Staged::swizzle(row);
+          from = u < DT / 2 ? keys + (u / kEach ? at1 : at0) + (row * (DT / 4 * 4) + piece) * 16
+                            : values + (u / kEach % 2 ? at1 : at0) + i * 16;
+        } else {
+          const int i = 64 * u + lane, j = i % D;
+          from = (i < D ? keys : values) + (j < D / 2 ? at0 : at1) + j % (D / 2) * 16;
+        }
+        __builtin_amdgcn_global_load_lds((global_ptr_t)from, (lds_ptr_t)(to + u * 1024), 16, 0,
+                                         kNonTemporal);
+      }
+      const char* from = reinterpret_cast<const char*>(a.scales) +
+                         (int64_t)max(lane < 32 ? b0 : b1, 0) * 128 + (lane & 31) * 4;
+      __builtin_amdgcn_global_load_lds((global_ptr_t)from, (lds_ptr_t)(to + 32 * D), 4, 0,
+                                       kNonTemporal);
+      const int after = next(ahead);
+      ahead = after;
+      const int then = actual(min(after, end - 1));
+      page0 = page_of(then, 0);
+      page1 = page_of(then, 1);
+    };
+    // S - 1 steps, the last again where there are fewer: with a fixed number of loads behind it the
+    // wait for q leaves them in flight.
+    if (works)
+#pragma unroll
+      for (int i = 0; i < S - 1; ++i) {
+        const int v = ahead;
+        stage(i);
+        if (ahead >= end && i < S - 2) ahead = v;
+      }
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
       float x[DT][8];
       float most = 0.0f;
 #pragma unroll
       for (int i = 0; i < DT; ++i) {
-        const u32x4 v = in[g] ? *reinterpret_cast<const u32x4*>(from + 8 * i) : u32x4{};
+        asm volatile("" : "+v"(loaded[g][i]));  // (not before the first steps are on their way)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const uint16_t bits = (uint16_t)(e & 1 ? v[e >> 1] >> 16 : v[e >> 1] & 0xFFFFu);
+          const uint32_t two = loaded[g][i][e >> 1];
+          const uint16_t bits = (uint16_t)(e & 1 ? two >> 16 : two & 0xFFFFu);
           x[i][e] = a.bf16 ? Bfloat::value(bits) : Half::value(bits);
           most = fmaxf(most, fabsf(x[i][e]));
         }
@@ -216,7 +285,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
         if (a.mask) {
           drafted = 0;
           if (in[g]) {
-            const int32_t* words = a.mask + at * a.mask_words;
+            const int32_t* words = a.mask + ((int64_t)cu + tok[g]) * a.mask_words;
             for (int w = 0; w < a.mask_words && 32 * w < n_new; ++w) {
               const int bits = n_new - 32 * w;
               drafted += __builtin_popcount((uint32_t)words[w] & (bits >= 32 ? ~0u : (1u << bits) - 1u));
@@ -226,55 +295,32 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
         since[g] = ctx + drafted - a.window;
       }
     }
-    const bool idle = row0 >= rows;
-
-    const scalar_ptr_t table = (scalar_ptr_t)(a.table + (int64_t)b * a.max_blocks);
-    auto page_of = [&](int step, int half) {
-      const int pos = step * 32 + half * 16;
-      return pos < len ? table[pos >> a.page_shift] : -1;
-    };
-    auto block_of = [&](int page, int step, int half) {
-      if ((unsigned)page >= (unsigned)a.num_pages) return -1;
-      return (page * a.Hkv + hk) * per_page + ((step * 2 + half) & (per_page - 1));
-    };
-    const int first = following(begin + key_wave);
-    auto next = [&](int v) { return following(v + key_waves); };
-    int page0 = page_of(actual(min(first, end - 1)), 0), page1 = page_of(actual(min(first, end - 1)), 1);
-    // Loads step v, whose pages are known, and fetches the pages of the one after it.
-    auto load = [&](Step<DT>& s, int v) {
-      s.index = actual(v);
-      const int b0 = block_of(page0, s.index, 0), b1 = block_of(page1, s.index, 1);
-      s.hole = (b0 < 0 ? 1u : 0u) | (b1 < 0 ? 2u : 0u);
-      const int64_t kb = max(key_half ? b1 : b0, 0), vb = max(value_half ? b1 : b0, 0);
-      const uint32_t* k = kc + kb * (2 * D);
-      const uint32_t* vv = vc + vb * (2 * D);
-      const uint16_t* sv = sc + vb * 64;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < DT; i += 4)
-          load_dwords(s.k[t], i, k + 4 * t * (D / 8) + i, DT - i < 4 ? DT - i : 4);
-#pragma unroll
-      for (int u = 0; u < 2 * DT; u += 4) {
-        const int n = 2 * DT - u < 4 ? 2 * DT - u : 4;
-        load_dwords(s.v, u, vv + 16 * u + n * c, n);
-      }
-      s.ks = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(sv));
-      s.kb = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(sv + 16));
-      s.vs = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(sv + 32));
-      s.vb = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(sv + 48));
-      const int after = actual(min(next(v), end - 1));
-      page0 = page_of(after, 0);
-      page1 = page_of(after, 1);
-    };
-
     f32x4 o[RG][kTiles] = {};
     float m[RG], l[RG], B[RG];  // reference, sum of p, sum of p (b + 8 s)
 #pragma unroll
     for (int g = 0; g < RG; ++g) m[g] = -INFINITY, l[g] = B[g] = 0.0f;
 
-    auto work = [&](Step<DT>& s) __attribute__((always_inline)) {
-      const Codes codes;
+    auto work = [&](int slot, int index) __attribute__((always_inline)) {
+      const char* const from = ring + slot * Staged::kBytes;
+      auto scales_at = [&](int which) {
+        return *reinterpret_cast<const u32x4*>(from + scale_at + 32 * which);
+      };
+      uint32_t kd[2][DT];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const char* row = from + key_at + t * (2 * D);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+          if constexpr (DT % 4 == 0) {
+            const int piece = (p * (DT / 4) + i / 4) ^ Staged::swizzle(key_row);
+            const u32x4 v = *reinterpret_cast<const u32x4*>(row + piece * 16);
+            kd[t][i] = v[i & 3];
+          } else {
+            kd[t][i] = reinterpret_cast<const uint32_t*>(row)[p * DT + i];
+          }
+        }
+      }
+      const u32x4 ks = scales_at(0), kb = scales_at(1);
       f32x4 x[RG][2];
 #pragma unroll
       for (int g = 0; g < RG; ++g)
@@ -284,7 +330,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
       for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const uint32_t w = s.k[t][i], w8 = w >> 8;
+          const uint32_t w = kd[t][i], w8 = w >> 8;
           const u32x4 f = {codes.low(w), codes.high(w), codes.low(w8), codes.high(w8)};
 #pragma unroll
           for (int g = 0; g < RG; ++g)
@@ -294,18 +340,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
       float raw[RG][8];
 #pragma unroll
       for (int g = 0; g < RG; ++g) {
-        vs[g] = s.vs;
-        vb[g] = s.vb;
+        vs[g] = scales_at(2);
+        vb[g] = scales_at(3);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          raw[g][e] = fmaf(half_at(s.ks, e), x[g][e >> 2][e & 3], half_at(s.kb, e) * Q[g]);
+          raw[g][e] = fmaf(half_at(ks, e), x[g][e >> 2][e & 3], half_at(kb, e) * Q[g]);
       }
       // Keys that are no context (drafted, or none at all), on no page, or before some row's
       // window: the wave masks.
-      const int pos = s.index * 32;
-      if (s.hole != 0 || pos + 32 > ctx || (a.window > 0 && pos < ctx + n_new - a.window)) {
+      const int pos = index * 32;
+      const uint32_t hole = holes >> 2 * slot & 3u;
+      if (hole != 0 || pos + 32 > ctx || (a.window > 0 && pos < ctx + n_new - a.window)) {
         const int pos0 = pos + 8 * p;
-        const uint32_t there = (s.hole >> value_half) & 1u ? 0u : low_bits(len - pos0);
+        const uint32_t there = (hole >> (p >> 1)) & 1u ? 0u : low_bits(len - pos0);
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
           const uint32_t inside = a.window > 0 ? low_bits(a.sinks - pos0) | ~low_bits(since[g] - pos0) : ~0u;
@@ -388,9 +435,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
         }
       }
       // tile 4 u + j of O (2 u + j of the last two where D = 96) is d = 64 u + 4 row + j
+      uint32_t vd[2 * DT];
+#pragma unroll
+      for (int u = 0; u < 2 * DT; ++u) {
+        const int n = 2 * DT - u / 4 * 4 < 4 ? 2 : 4;
+        vd[u] = reinterpret_cast<const uint32_t*>(from + value_at + u / 4 * 256)[n * c + (u & 3)];
+      }
 #pragma unroll
       for (int i = 0; i < DT; ++i) {
-        const uint32_t w0 = s.v[2 * i], w1 = s.v[2 * i + 1], w0s = w0 >> 8, w1s = w1 >> 8;
+        const uint32_t w0 = vd[2 * i], w1 = vd[2 * i + 1], w0s = w0 >> 8, w1s = w1 >> 8;
         const u32x4 even = {codes.low(w0), codes.low(w0s), codes.low(w1), codes.low(w1s)};
         const u32x4 odd = {codes.high(w0), codes.high(w0s), codes.high(w1), codes.high(w1s)};
 #pragma unroll
@@ -403,19 +456,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
       }
     };
 
-    if (!idle && first < end) {
-      Step<DT> one, two;
-      int v = first;
-      load(one, v);
-      for (;;) {
-        v = next(v);
-        load(two, min(v, end - 1));
-        work(one);
-        if (v >= end) break;
-        v = next(v);
-        load(one, min(v, end - 1));
-        work(two);
-        if (v >= end) break;
+    if (works) {
+      int slot = 0;
+      for (int v = first; v < end; v = next(v)) {
+        const int free = slot == 0 ? S - 1 : slot - 1;  // (worked on the time before)
+        if (ahead < end) {
+          stage(free);
+          wait_vm<(S - 1) * Staged::kLoads>();
+        } else {
+          wait_vm<0>();
+        }
+        asm volatile("" ::: "memory");
+        work(slot, actual(v));
+        slot = slot == S - 1 ? 0 : slot + 1;
       }
     }
 
@@ -471,7 +524,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
     // the waves that shared the steps: each adds up some of the quads
     f32x4* sums = reinterpret_cast<f32x4*>(lds) + wave * (RG * kTiles * 64) + lane;
     float2* stats = reinterpret_cast<float2*>(lds + kWaves * RG * kTiles * 1024);
-    lds_barrier();  // those of the request before have been read
+    lds_barrier();  // every wave's stages have been read
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
       if (p == 0) stats[(wave * RG + g) * 16 + c] = {m[g], total[g]};
@@ -501,6 +554,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_attention_kernel(const Kv4
         put(g, j, v, top, sum);
       }
     }
+    lds_barrier();  // the sums have been read, and steps may be staged where they were
   }
 }
 
@@ -519,7 +573,7 @@ Layout layout_of(int64_t max_new, int64_t H, int64_t Hkv, int64_t D) {
   p.key_waves = waves == 1 ? 4 : waves == 2 ? 2 : 1;
   const int64_t block_rows = kWaves / p.key_waves * 16 * p.groups;
   p.row_blocks = (int)((rows + block_rows - 1) / block_rows);
-  const int64_t target = 2 * device_cu_count();
+  const int64_t target = units_per_cu(D, p.groups) * device_cu_count();
   p.shares = (int)std::max<int64_t>(1, target / (Hkv * p.row_blocks));
   return p;
 }
@@ -535,12 +589,15 @@ hipError_t launch_rows(const Kv4AttentionArgs& a, hipStream_t stream) {
       p.shares, std::max<int64_t>(1, a.B * (a.kHead + room) / a.kMinShare));
   const int64_t units = (int64_t)p.shares * a.Hkv;
   const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.row_blocks));
-  auto* kernel = kv4_attention_kernel<DT, 1>;
+  constexpr int S1 = DT <= 4 ? 3 : 2;
+  int S = S1;
+  auto* kernel = kv4_attention_kernel<DT, 1, S1>;
   if constexpr (DT <= 4) {
-    if (p.groups == 2) kernel = kv4_attention_kernel<DT, 2>;
+    if (p.groups == 2) kernel = kv4_attention_kernel<DT, 2, 4>, S = 4;
   }
-  const size_t lds =
+  const size_t sums =
       p.key_waves == 1 ? 0 : (size_t)kWaves * p.groups * (2 * DT * 1024 + 16 * sizeof(float2));
+  const size_t lds = std::max(sums, (size_t)kWaves * S * Stage<DT>::kBytes);
   const hipError_t e = launch_kernel_lds(kernel, grid, dim3(64 * kWaves), lds, stream, a, p.shares,
                                          p.row_blocks, p.key_waves);
   if (e != hipSuccess || p.shares == 1) return e;
