@@ -429,13 +429,12 @@ flexq_status flexq_kv4_attention(const uint16_t* q, int32_t dtype, int64_t q_str
       mask_words, scale, workspace, workspace_bytes, flexq::kv4_attention_workspace_bytes, out, lse,
       a, nothing));
   if (nothing) return FLEXQ_SUCCESS;
-  a.bf16 = dtype == FLEXQ_BF16;
   a.scales = scales;
   // a request has at most 2^24 positions: more is no window, or sinks throughout
   constexpr int64_t kAll = 1LL << 26;
   a.window = window >= kAll ? 0 : (int32_t)window;
   a.sinks = (int32_t)std::min(sinks, kAll);
-  return launched(flexq::launch_kv4_attention(a, (hipStream_t)stream));
+  return launched(flexq::launch_kv4_attention(a, dtype == FLEXQ_BF16, (hipStream_t)stream));
 }
 
 size_t flexq_lora_add_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {

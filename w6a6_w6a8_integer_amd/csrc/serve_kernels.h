@@ -62,14 +62,13 @@ hipError_t launch_tree_attention(const AttentionArgs& a, bool bf16, hipStream_t 
 struct Kv4AttentionArgs : AttentionArgs {
   static constexpr uint32_t kHead = 5, kMinShare = 8;
   static constexpr bool kWindowed = true;
-  bool bf16;
   const uint16_t* scales;
   int32_t window, sinks;
 };
 
 size_t kv4_attention_workspace_bytes(int64_t B, int64_t max_new, int64_t H, int64_t Hkv,
                                      int64_t D);
-hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t stream);
+hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, bool bf16, hipStream_t stream);
 
 hipError_t launch_kv4_cache_write(const uint16_t* k, int64_t k_st, int64_t k_sh,
                                   const uint16_t* v, int64_t v_st, int64_t v_sh, bool bf16,

@@ -22,6 +22,8 @@
 // dealt to the score tiles' rows so that a lane's scores are those that its fragment of P takes:
 // row r of score tile t holds key 8 (r / 4) + 4 t + r % 4, lane l keys 8 (l / 16) .. + 7.  Waves
 // that the rows leave over take the steps in turn and add up in LDS.
+#include <type_traits>
+
 #include "serve_plan.h"
 
 namespace flexq {
@@ -43,25 +45,62 @@ constexpr int units_per_cu(int64_t D, int groups) { return groups == 1 && D <= 1
 // (by value: a bit cast of a vector's element takes the whole vector's first bits)
 __device__ __forceinline__ f16x2 pair_of(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
 
-// Eight codes of a dword, four pairs: c - 8 from the low four bits of its bytes, 16 (c - 8) from the
-// high ones.  The constants sit in registers: as literals they would take an and and an or.
+// Eight codes of a dword as four pairs of halves.  The constants sit in registers: as literals they
+// would take an and and an or.
 struct Codes {
-  uint32_t base = 0x64006400u, low_bits = 0x000F000Fu, high_bits = 0x00F000F0u;
+  uint32_t base64 = 0x54005400u, base1024 = 0x64006400u;
+  uint32_t low_bits = 0x000F000Fu, high_bits = 0x00F000F0u;
   __device__ __forceinline__ Codes() {
-    asm("" : "+v"(base));
+    asm("" : "+v"(base64));
+    asm("" : "+v"(base1024));
     asm("" : "+s"(low_bits));
     asm("" : "+s"(high_bits));
   }
+  // 64 + c, pairs in the order of a key's dword: the bits below 64's exponent are the halves' bits
+  // 4 to 7, so three shifts and four and-ors
+  __device__ __forceinline__ u32x4 key(uint32_t w) const {
+    return u32x4{(w << 4 & high_bits) | base64, (w & high_bits) | base64,
+                 (w >> 4 & high_bits) | base64, (w >> 8 & high_bits) | base64};
+  }
+  // c - 8 from the low four bits of the bytes, 16 (c - 8) from the high ones: (1024 + c) - 1032 and
+  // (1024 + 16 c) - 1152
   __device__ __forceinline__ uint32_t low(uint32_t w) const {
-    return __builtin_bit_cast(uint32_t, pair_of((w & low_bits) | base) - f16x2{1032.0f16, 1032.0f16});
+    return __builtin_bit_cast(uint32_t,
+                              pair_of((w & low_bits) | base1024) - f16x2{1032.0f16, 1032.0f16});
   }
   __device__ __forceinline__ uint32_t high(uint32_t w) const {
-    return __builtin_bit_cast(uint32_t, pair_of((w & high_bits) | base) - f16x2{1152.0f16, 1152.0f16});
+    return __builtin_bit_cast(uint32_t,
+                              pair_of((w & high_bits) | base1024) - f16x2{1152.0f16, 1152.0f16});
   }
 };
 
-__device__ __forceinline__ float half_at(const u32x4& v, int e) {
+// The 16 lanes of a group of rows hold 16 / FOLD rows FOLD times over, each 1 / FOLD of the row's keys.
+// Maximum and sum over the lanes that hold a row:
+template <int FOLD>
+__device__ __forceinline__ float fold_max(float x) {
+  if constexpr (FOLD >= 2) x = fmaxf(x, __shfl_xor(x, 8));
+  if constexpr (FOLD >= 4) x = fmaxf(x, __shfl_xor(x, 4));
+  return row_max<16>(x);
+}
+template <int FOLD>
+__device__ __forceinline__ float fold_sum(float x) {
+  if constexpr (FOLD >= 2) x += __shfl_xor(x, 8);
+  if constexpr (FOLD >= 4) x += __shfl_xor(x, 4);
+  return row_sum<16>(x);
+}
+// the value of the lane N places on, round the 16 of a DPP row
+template <int N>
+__device__ __forceinline__ uint32_t from_lane(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + 16 - N, 0xF, 0xF, false);
+}
+
+__device__ __forceinline__ float half_at(const uint32_t* v, int e) {
   return half_bits_to_float((uint16_t)(e & 1 ? v[e >> 1] >> 16 : v[e >> 1] & 0xFFFFu));
+}
+
+__device__ __forceinline__ u32x4 all_halves(float f) {
+  const uint32_t h = Half::bits(f) * 0x10001u;
+  return u32x4{h, h, h, h};
 }
 
 // A 32-key step as a wave stages it in LDS: the codes of the keys' two 16-token blocks, of the
@@ -78,6 +117,62 @@ struct Stage {
   }
 };
 
+// A lane's queries (consecutive eights of its quarter of D) as fp16 times the power of 2 that takes the
+// row's largest to 2^14 .. 2^15 (for fp16 2^30 at most), a negative scale in their sign, a zero one
+// in the queries themselves.  Returns what takes raw scores to exponents of 2.
+template <class E, int DT>
+__device__ __forceinline__ float scaled_queries(u32x4 (&q)[DT], float scale) {
+  u16x2 most = {0, 0};
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t two = q[i][e] & 0x7FFF7FFFu;
+      most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, two));
+    }
+  int up = 15 - __builtin_amdgcn_frexp_expf(row_max<16>(E::value(most[0] > most[1] ? most[0] : most[1])));
+  const float sign = scale == 0.0f ? 0.0f : scale < 0.0f ? -1.0f : 1.0f;
+  if constexpr (std::is_same_v<E, Half>) {
+    up = min(up, 30);
+    const _Float16 f0 = (_Float16)(__builtin_amdgcn_ldexpf(sign, min(up, 15)));
+    const _Float16 f1 = (_Float16)(__builtin_amdgcn_ldexpf(1.0f, max(up - 15, 0)));
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t two = q[i][e];
+        q[i][e] = __builtin_bit_cast(uint32_t, pair_of(two) * f16x2{f0, f0} * f16x2{f1, f1});
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t two = q[i][e];
+        const float v0 = __builtin_amdgcn_ldexpf(E::value((uint16_t)(two & 0xFFFFu)) * sign, up);
+        const float v1 = __builtin_amdgcn_ldexpf(E::value((uint16_t)(two >> 16)) * sign, up);
+        q[i][e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(v0, v1));
+      }
+  }
+  return __builtin_amdgcn_ldexpf(scale != 0.0f ? fabsf(scale) * kLog2e : 1.0f, -up);
+}
+
+// The pairs of the lanes that hold a row's other keys, behind the lane's own.  (Only the first 16 / FOLD
+// lanes of 16 get them in order; the others' columns are nobody's rows.)
+template <int FOLD>
+__device__ __forceinline__ void gather(u32x4& v) {
+  if constexpr (FOLD == 2) {
+    const uint32_t v0 = v[0], v1 = v[1];
+    v[2] = from_lane<8>(v0);
+    v[3] = from_lane<8>(v1);
+  } else {
+    const uint32_t v0 = v[0];
+    v[1] = from_lane<4>(v0);
+    v[2] = from_lane<8>(v0);
+    v[3] = from_lane<12>(v0);
+  }
+}
+
 }  // namespace
 
 // 32-key steps between the first tokens and the earliest key that any row's window holds.
@@ -90,11 +185,14 @@ __device__ __forceinline__ int window_gap(const Kv4AttentionArgs& a, const Reque
 
 // One workgroup = one share of the cache, key head and block of rows: KW of its waves take the steps in
 // turn, 4 / KW the rows, RG groups of 16 each.
-template <int DT, int RG, int S>
-__global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_attention_kernel(const Kv4AttentionArgs a,
-                                                                      int shares, int row_blocks,
-                                                                      int key_waves) {
+template <class E, int DT, int RG, int FOLD, int S>
+__global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_attention_kernel(
+    const Kv4AttentionArgs a, int shares, int row_blocks, int key_waves) {
+  static_assert(FOLD == 1 || RG == 1, "few rows are one group");
   constexpr int D = 32 * DT;
+  constexpr int kRows = 16 / FOLD;  // of a group
+  constexpr int kKeys = 8 / FOLD;   // whose scores a lane holds
+  constexpr bool kTwoParts = std::is_same_v<E, Half>;
   constexpr int kTiles = 2 * DT;  // of O, and quads of consecutive d that a lane ends up with
   extern __shared__ __attribute__((aligned(1024))) char lds[];
 
@@ -126,7 +224,14 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
   const int key_row = 8 * (c >> 2 & 1) + (c & 3);
   const int key_at = (c >> 3) * 8 * D + key_row * (D / 2);
   const int value_at = 16 * D + (p >> 1) * 8 * D + (p & 1) * 4 * D;
-  const int scale_at = 32 * D + (p >> 1) * 128 + (p & 1) * 16;
+  const int part = c / kRows * kKeys;  // the first of the lane's keys among those eight
+  const int scale_at = 32 * D + (p >> 1) * 128 + (p & 1) * 16 + 2 * part;
+  uint32_t key_from[DT < 4 ? 1 : DT / 4];  // the piece of a block's keys that the lane fetches
+#pragma unroll
+  for (int u = 0; u < DT / 4; ++u) {
+    const int i = 64 * u + lane, row = i / DT;
+    key_from[u] = (row * DT + (i % DT ^ Staged::swizzle(row))) * 16;
+  }
   const Codes codes;
   float zero = 0.0f;  // the compiler's own zero would keep p s from being one instruction
   asm("" : "+v"(zero));
@@ -168,19 +273,19 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
     int tok[RG];
     bool in[RG];
     float Q[RG], by[RG];       // sum of the fp16 queries; from raw scores to exponents of 2
-    u32x4 loaded[RG][DT];
-    uint32_t q[RG][DT][4];
+    f32x4 minus64[RG];         // - 64 Q
+    u32x4 q[RG][DT];
     int since[RG];             // first key of the row's window
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
-      const int row = row0 + 16 * g + c;
+      const int row = row0 + 16 * g + c % kRows;
       tok[g] = row / group;
       const int64_t at = (int64_t)cu + tok[g];
       in[g] = row < rows && at >= 0 && at < a.T;
       const uint16_t* from = a.q + at * a.q_st + (int64_t)(hk * group + row % group) * a.q_sh + p * 8 * DT;
 #pragma unroll
       for (int i = 0; i < DT; ++i)
-        loaded[g][i] = in[g] ? *reinterpret_cast<const u32x4*>(from + 8 * i) : u32x4{};
+        q[g][i] = in[g] ? *reinterpret_cast<const u32x4*>(from + 8 * i) : u32x4{};
     }
 
     const scalar_ptr_t table = (scalar_ptr_t)(a.table + (int64_t)b * a.max_blocks);
@@ -212,10 +317,8 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
         const char* from;
         if constexpr (DT % 4 == 0) {  // whole kilobytes of one block
           constexpr int kEach = DT / 4;
-          const int part = u % kEach, i = 64 * part + lane;
-          const int row = i / (DT / 4 * 4), piece = i % (DT / 4 * 4) ^ Staged::swizzle(row);
-          from = u < DT / 2 ? keys + (u / kEach ? at1 : at0) + (row * (DT / 4 * 4) + piece) * 16
-                            : values + (u / kEach % 2 ? at1 : at0) + i * 16;
+          from = (u < DT / 2 ? keys : values) + (u / kEach % 2 ? at1 : at0) +
+                 (u < DT / 2 ? key_from[u % kEach] : lane * 16u + u % kEach * 1024u);
         } else {
           const int i = 64 * u + lane, j = i % D;
           from = (i < D ? keys : values) + (j < D / 2 ? at0 : at1) + j % (D / 2) * 16;
@@ -244,41 +347,16 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
       }
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
-      float x[DT][8];
-      float most = 0.0f;
-#pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        asm volatile("" : "+v"(loaded[g][i]));  // (not before the first steps are on their way)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t two = loaded[g][i][e >> 1];
-          const uint16_t bits = (uint16_t)(e & 1 ? two >> 16 : two & 0xFFFFu);
-          x[i][e] = a.bf16 ? Bfloat::value(bits) : Half::value(bits);
-          most = fmaxf(most, fabsf(x[i][e]));
-        }
-      }
-      // A row's largest query becomes 2^14 to 2^15; a negative scale goes into the sign, a zero
-      // one into the queries.
-      most = row_max<16>(most);
-      const int up = 15 - __builtin_amdgcn_frexp_expf(most);
-      Q[g] = 0.0f;
 #pragma unroll
       for (int i = 0; i < DT; ++i)
+        asm volatile("" : "+v"(q[g][i]));  // (not before the first steps are on their way)
+      by[g] = scaled_queries<E, DT>(q[g], a.scale);
+      // the sums that take the codes' 64 off, by the MFMAs that will add it
+      minus64[g] = f32x4{};
+      const u32x4 m64 = all_halves(-64.0f);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          float y[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            y[j] = __builtin_amdgcn_ldexpf(x[i][e + j], up);
-            y[j] = a.scale == 0.0f ? 0.0f : a.scale < 0.0f ? -y[j] : y[j];
-            const float h = (float)(_Float16)y[j];
-            Q[g] += h;
-            y[j] = e & 2 ? h * 0.0625f : h;  // (codes there come as 16 (c - 8))
-          }
-          q[g][i][e >> 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(y[0], y[1]));
-        }
-      Q[g] = row_sum<16>(Q[g]);
-      by[g] = __builtin_amdgcn_ldexpf(a.scale != 0.0f ? fabsf(a.scale) * kLog2e : 1.0f, -up);
+      for (int i = 0; i < DT; ++i) minus64[g] = Half::mfma(m64, q[g][i], minus64[g]);
+      Q[g] = minus64[g][0] * -0.015625f;
       since[g] = -(1 << 30);
       if (a.window > 0) {
         int drafted = tok[g] + 1;
@@ -296,14 +374,18 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
       }
     }
     f32x4 o[RG][kTiles] = {};
-    float m[RG], l[RG], B[RG];  // reference, sum of p, sum of p (b + 8 s)
+    f32x4 W[RG] = {};           // sum of w, of all keys in every lane of a column
+    float m[RG], l[RG], B[RG];  // reference, and the lane's share of the sums of p and p b
+    const u32x4 ones = all_halves(1.0f);
 #pragma unroll
     for (int g = 0; g < RG; ++g) m[g] = -INFINITY, l[g] = B[g] = 0.0f;
 
     auto work = [&](int slot, int index) __attribute__((always_inline)) {
       const char* const from = ring + slot * Staged::kBytes;
-      auto scales_at = [&](int which) {
-        return *reinterpret_cast<const u32x4*>(from + scale_at + 32 * which);
+      auto scales_at = [&](int which, uint32_t* to) {
+        const uint32_t* at = reinterpret_cast<const uint32_t*>(from + scale_at + 32 * which);
+#pragma unroll
+        for (int i = 0; i < kKeys / 2; ++i) to[i] = at[i];
       };
       uint32_t kd[2][DT];
 #pragma unroll
@@ -320,31 +402,34 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
           }
         }
       }
-      const u32x4 ks = scales_at(0), kb = scales_at(1);
+      uint32_t ks[kKeys / 2], kb[kKeys / 2], vs[RG][kKeys / 2], vb[RG][kKeys / 2];
+      scales_at(0, ks);
+      scales_at(1, kb);
       f32x4 x[RG][2];
-#pragma unroll
-      for (int g = 0; g < RG; ++g)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) x[g][t] = f32x4{8 * Q[g], 8 * Q[g], 8 * Q[g], 8 * Q[g]};
 #pragma unroll
       for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const uint32_t w = kd[t][i], w8 = w >> 8;
-          const u32x4 f = {codes.low(w), codes.high(w), codes.low(w8), codes.high(w8)};
+          const u32x4 f = codes.key(kd[t][i]);
 #pragma unroll
-          for (int g = 0; g < RG; ++g)
-            x[g][t] = Half::mfma(f, u32x4{q[g][i][0], q[g][i][1], q[g][i][2], q[g][i][3]}, x[g][t]);
+          for (int g = 0; g < RG; ++g) x[g][t] = Half::mfma(f, q[g][i], i == 0 ? minus64[g] : x[g][t]);
         }
-      u32x4 vs[RG], vb[RG];  // of what the row attends
-      float raw[RG][8];
+      float raw[RG][kKeys];
 #pragma unroll
       for (int g = 0; g < RG; ++g) {
-        vs[g] = scales_at(2);
-        vb[g] = scales_at(3);
+        scales_at(2, vs[g]);  // (of what the row attends)
+        scales_at(3, vb[g]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          raw[g][e] = fmaf(half_at(ks, e), x[g][e >> 2][e & 3], half_at(kb, e) * Q[g]);
+        for (int e = 0; e < kKeys; ++e) {
+          float qc;
+          if constexpr (FOLD == 1)
+            qc = x[g][e >> 2][e & 3];
+          else if constexpr (FOLD == 2)
+            qc = c >= 8 ? x[g][1][e] : x[g][0][e];
+          else
+            qc = c >= 8 ? (c & 4 ? x[g][1][2 + e] : x[g][1][e]) : (c & 4 ? x[g][0][2 + e] : x[g][0][e]);
+          raw[g][e] = fmaf(half_at(ks, e), qc, half_at(kb, e) * Q[g]);
+        }
       }
       // Keys that are no context (drafted, or none at all), on no page, or before some row's
       // window: the wave masks.
@@ -370,12 +455,12 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
           } else {  // a chain: the tokens up to the row's own, in the window
             seen = low_bits(ctx + tok[g] + 1 - pos0) & inside;
           }
-          seen &= there;
+          seen = (seen & there) >> part;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
+          for (int e = 0; e < kKeys; ++e)
             if (!((seen >> e) & 1u)) raw[g][e] = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // (what masked places hold does not matter, NaN included)
+          for (int i = 0; i < kKeys / 2; ++i) {  // (what masked places hold does not matter, NaN included)
             const uint32_t keep = (seen >> (2 * i) & 1u) * 0xFFFFu | (seen >> (2 * i + 1) & 1u) * 0xFFFF0000u;
             vs[g][i] &= keep;
             vb[g][i] &= keep;
@@ -390,23 +475,23 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
       for (int g = 0; g < RG; ++g) {
         float top = raw[g][0];
 #pragma unroll
-        for (int e = 1; e < 8; ++e) top = fmaxf(top, raw[g][e]);
+        for (int e = 1; e < kKeys; ++e) top = fmaxf(top, raw[g][e]);
         // (scales are not negative: their bits are in their order)
         u16x2 most = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t two = vs[g][i];
-          most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, two));
-        }
+        for (int i = 0; i < kKeys / 2; ++i)
+          most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, vs[g][i]));
         const float scale = half_bits_to_float(most[0] > most[1] ? most[0] : most[1]);
         top = fmaf(top, by[g], (float)__builtin_amdgcn_frexp_expf(scale));
         if (__ballot(top > m[g] + kLag)) {  // rare after a request's first step
-          top = row_max<16>(top);
+          top = fold_max<FOLD>(top);
           top = fmaxf(m[g], ceilf(top));
           const float down = m[g] - (top == -INFINITY ? 0.0f : top);
           m[g] = top;
           l[g] = scaled(l[g], down);
           B[g] = scaled(B[g], down);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) W[g][i] = scaled(W[g][i], down);
 #pragma unroll
           for (int t = 0; t < kTiles; ++t)
 #pragma unroll
@@ -414,7 +499,7 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
         }
         const float ref = m[g] == -INFINITY ? 0.0f : kTop - m[g];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kKeys / 2; ++i) {
           float prob[2], step[2];
           f16x2 h, rest;
 #pragma unroll
@@ -422,19 +507,24 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
             prob[j] = __builtin_amdgcn_exp2f(fmaf(raw[g][2 * i + j], by[g], ref));
             step[j] = half_at(vs[g], 2 * i + j);
             l[g] += prob[j];
-            B[g] = fmaf(prob[j], fmaf(step[j], 8.0f, half_at(vb[g], 2 * i + j)), B[g]);
+            B[g] = fmaf(prob[j], half_at(vb[g], 2 * i + j), B[g]);
             h[j] = (_Float16)fmaf(prob[j], step[j], zero);
           }
           uint32_t bits = __builtin_bit_cast(uint32_t, h);
           asm("" : "+v"(bits));  // the very bits that the product takes are what is left out of the rest
           hi[g][i] = bits;
-          h = pair_of(bits);
+          if constexpr (kTwoParts) {
+            h = pair_of(bits);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) rest[j] = (_Float16)fmaf(prob[j], step[j], -(float)h[j]);
-          lo[g][i] = __builtin_bit_cast(uint32_t, rest);
+            for (int j = 0; j < 2; ++j) rest[j] = (_Float16)fmaf(prob[j], step[j], -(float)h[j]);
+            lo[g][i] = __builtin_bit_cast(uint32_t, rest);
+          }
         }
+        if constexpr (FOLD > 1) gather<FOLD>(hi[g]);
+        if constexpr (FOLD > 1 && kTwoParts) gather<FOLD>(lo[g]);
+        W[g] = Half::mfma(ones, hi[g], W[g]);
+        if constexpr (kTwoParts) W[g] = Half::mfma(ones, lo[g], W[g]);
       }
-      // tile 4 u + j of O (2 u + j of the last two where D = 96) is d = 64 u + 4 row + j
       uint32_t vd[2 * DT];
 #pragma unroll
       for (int u = 0; u < 2 * DT; ++u) {
@@ -450,8 +540,10 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
         for (int g = 0; g < RG; ++g) {
           o[g][2 * i] = Half::mfma(even, hi[g], o[g][2 * i]);
           o[g][2 * i + 1] = Half::mfma(odd, hi[g], o[g][2 * i + 1]);
-          o[g][2 * i] = Half::mfma(even, lo[g], o[g][2 * i]);
-          o[g][2 * i + 1] = Half::mfma(odd, lo[g], o[g][2 * i + 1]);
+          if constexpr (kTwoParts) {
+            o[g][2 * i] = Half::mfma(even, lo[g], o[g][2 * i]);
+            o[g][2 * i + 1] = Half::mfma(odd, lo[g], o[g][2 * i + 1]);
+          }
         }
       }
     };
@@ -477,8 +569,8 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
     float total[RG];
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
-      total[g] = row_sum<16>(l[g]);
-      const float offset = row_sum<16>(B[g]);
+      total[g] = fold_sum<FOLD>(l[g]);
+      const float offset = fmaf(W[g][0], 8.0f, fold_sum<FOLD>(B[g]));
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
@@ -496,7 +588,7 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
     };
     auto put = [&](int g, int j, f32x4 v, float ref, float sum) {
       const int row = row0 + 16 * g + c;
-      if (row >= rows) return;
+      if (row >= rows || c >= kRows) return;
       const int d4 = d4_of(j);
       const float top = ref == -INFINITY ? ref : ref - kTop;
       if (s0 != s1) {
@@ -508,10 +600,7 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
         const int64_t t = (int64_t)cu + tok[g];
         const int h = hk * group + row % group;
         const float zero = top == -INFINITY ? 0.0f : top;
-        if (a.bf16)
-          write_row<Bfloat>(a, t, h, d4, v, zero, sum);
-        else
-          write_row<Half>(a, t, h, d4, v, zero, sum);
+        write_row<E>(a, t, h, d4, v, zero, sum);
       }
     };
     if (key_waves == 1) {
@@ -560,15 +649,17 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
 
 namespace {
 
-// How a call is laid out: groups of 16 rows a wave, waves along the keys, row blocks, shares
+// How a call is laid out: groups of 16 rows a wave, times over that fewer rows fill one, waves along
+// the keys, row blocks, shares
 struct Layout {
-  int groups, key_waves, row_blocks, shares;
+  int groups, fold, key_waves, row_blocks, shares;
 };
 
 Layout layout_of(int64_t max_new, int64_t H, int64_t Hkv, int64_t D) {
   Layout p;
   const int64_t rows = max_new * (H / Hkv);
   p.groups = rows <= 16 || D > 128 ? 1 : 2;
+  p.fold = rows <= 4 ? 4 : rows <= 8 ? 2 : 1;
   const int64_t waves = (rows + 16 * p.groups - 1) / (16 * p.groups);  // that hold rows
   p.key_waves = waves == 1 ? 4 : waves == 2 ? 2 : 1;
   const int64_t block_rows = kWaves / p.key_waves * 16 * p.groups;
@@ -578,7 +669,7 @@ Layout layout_of(int64_t max_new, int64_t H, int64_t Hkv, int64_t D) {
   return p;
 }
 
-template <int DT>
+template <class E, int DT>
 hipError_t launch_rows(const Kv4AttentionArgs& a, hipStream_t stream) {
   Layout p = layout_of(a.max_new, a.H, a.Hkv, a.D);
   // no more shares than the tables' room can fill (short contexts: one, and no join)
@@ -589,20 +680,32 @@ hipError_t launch_rows(const Kv4AttentionArgs& a, hipStream_t stream) {
       p.shares, std::max<int64_t>(1, a.B * (a.kHead + room) / a.kMinShare));
   const int64_t units = (int64_t)p.shares * a.Hkv;
   const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.row_blocks));
-  constexpr int S1 = DT <= 4 ? 3 : 2;
-  int S = S1;
-  auto* kernel = kv4_attention_kernel<DT, 1, S1>;
+  // stages: what a workgroup's share of a compute unit's LDS holds
+  constexpr int S = DT <= 4 ? 3 : 2, S2 = 4;
+  auto* kernel = p.fold == 4   ? kv4_attention_kernel<E, DT, 1, 4, S>
+                 : p.fold == 2 ? kv4_attention_kernel<E, DT, 1, 2, S>
+                               : kv4_attention_kernel<E, DT, 1, 1, S>;
   if constexpr (DT <= 4) {
-    if (p.groups == 2) kernel = kv4_attention_kernel<DT, 2, 4>, S = 4;
+    if (p.groups == 2) kernel = kv4_attention_kernel<E, DT, 2, 1, S2>;
   }
   const size_t sums =
       p.key_waves == 1 ? 0 : (size_t)kWaves * p.groups * (2 * DT * 1024 + 16 * sizeof(float2));
-  const size_t lds = std::max(sums, (size_t)kWaves * S * Stage<DT>::kBytes);
+  const size_t lds =
+      std::max(sums, (size_t)kWaves * (p.groups == 2 ? S2 : S) * Stage<DT>::kBytes);
   const hipError_t e = launch_kernel_lds(kernel, grid, dim3(64 * kWaves), lds, stream, a, p.shares,
                                          p.row_blocks, p.key_waves);
   if (e != hipSuccess || p.shares == 1) return e;
-  return a.bf16 ? launch_join<Kv4AttentionArgs, Bfloat, DT>(a, p.shares, stream)
-                : launch_join<Kv4AttentionArgs, Half, DT>(a, p.shares, stream);
+  return launch_join<Kv4AttentionArgs, E, DT>(a, p.shares, stream);
+}
+
+template <class E>
+hipError_t launch_width(const Kv4AttentionArgs& a, hipStream_t stream) {
+  switch (a.D) {
+    case 64: return launch_rows<E, 2>(a, stream);
+    case 96: return launch_rows<E, 3>(a, stream);
+    case 128: return launch_rows<E, 4>(a, stream);
+    default: return launch_rows<E, 8>(a, stream);
+  }
 }
 
 }  // namespace
@@ -612,13 +715,8 @@ size_t kv4_attention_workspace_bytes(int64_t B, int64_t max_new, int64_t H, int6
   return parts_bytes(B, max_new, H, D, layout_of(max_new, H, Hkv, D).shares);
 }
 
-hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t stream) {
-  switch (a.D) {
-    case 64: return launch_rows<2>(a, stream);
-    case 96: return launch_rows<3>(a, stream);
-    case 128: return launch_rows<4>(a, stream);
-    default: return launch_rows<8>(a, stream);
-  }
+hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, bool bf16, hipStream_t stream) {
+  return bf16 ? launch_width<Bfloat>(a, stream) : launch_width<Half>(a, stream);
 }
 
 }  // namespace flexq
