@@ -430,6 +430,8 @@ flexq_status flexq_kv4_attention(const uint16_t* q, int32_t dtype, int64_t q_str
       a, nothing));
   if (nothing) return FLEXQ_SUCCESS;
   a.scales = scales;
+  a.group = (uint32_t)(H / Hkv);
+  a.group_inverse = a.group > 1 ? (uint32_t)((1ull << 32) / a.group) : 0xFFFFFFFFu;
   // a request has at most 2^24 positions: more is no window, or sinks throughout
   constexpr int64_t kAll = 1LL << 26;
   a.window = window >= kAll ? 0 : (int32_t)window;

@@ -62,6 +62,7 @@ hipError_t launch_tree_attention(const AttentionArgs& a, bool bf16, hipStream_t 
 struct Kv4AttentionArgs : AttentionArgs {
   static constexpr uint32_t kHead = 5, kMinShare = 8;
   static constexpr bool kWindowed = true;
+  uint32_t group, group_inverse;  // H / Hkv, floor(2^32 / group) (less one for a group of one)
   const uint16_t* scales;
   int32_t window, sinks;
 };

@@ -74,26 +74,30 @@ struct Codes {
   }
 };
 
-// The 16 lanes of a group of rows hold 16 / FOLD rows FOLD times over, each 1 / FOLD of the row's keys.
-// Maximum and sum over the lanes that hold a row:
-template <int FOLD>
-__device__ __forceinline__ float fold_max(float x) {
-  if constexpr (FOLD >= 2) x = fmaxf(x, __shfl_xor(x, 8));
-  if constexpr (FOLD >= 4) x = fmaxf(x, __shfl_xor(x, 4));
-  return row_max<16>(x);
-}
-template <int FOLD>
-__device__ __forceinline__ float fold_sum(float x) {
-  if constexpr (FOLD >= 2) x += __shfl_xor(x, 8);
-  if constexpr (FOLD >= 4) x += __shfl_xor(x, 4);
-  return row_sum<16>(x);
-}
 // the value of the lane N places on, round the 16 of a DPP row
 template <int N>
 __device__ __forceinline__ uint32_t from_lane(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + 16 - N, 0xF, 0xF, false);
 }
+template <int N>
+__device__ __forceinline__ float from_lane(float v) {
+  return __builtin_bit_cast(float, from_lane<N>(__builtin_bit_cast(uint32_t, v)));
+}
 
+// The 16 lanes of a group of rows hold 16 / FOLD rows FOLD times over, each 1 / FOLD of the row's keys.
+// Maximum and sum over the lanes that hold a row:
+template <int FOLD>
+__device__ __forceinline__ float fold_max(float x) {
+  if constexpr (FOLD >= 2) x = fmaxf(x, from_lane<8>(x));
+  if constexpr (FOLD >= 4) x = fmaxf(x, from_lane<4>(x));
+  return row_max<16>(x);
+}
+template <int FOLD>
+__device__ __forceinline__ float fold_sum(float x) {
+  if constexpr (FOLD >= 2) x += from_lane<8>(x);
+  if constexpr (FOLD >= 4) x += from_lane<4>(x);
+  return row_sum<16>(x);
+}
 __device__ __forceinline__ float half_at(const uint32_t* v, int e) {
   return half_bits_to_float((uint16_t)(e & 1 ? v[e >> 1] >> 16 : v[e >> 1] & 0xFFFFu));
 }
@@ -199,22 +203,31 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, p = lane >> 4;
-  const int key_wave = wave & (key_waves - 1), row_wave = wave / key_waves;
-  const int block_rows = kWaves / key_waves * (16 * RG);
+  const int key_wave = wave & (key_waves - 1), row_wave = wave >> __builtin_ctz(key_waves);
+  const int block_rows = (kWaves >> __builtin_ctz(key_waves)) * (16 * RG);
   // Workgroups 8 apart share an XCD: the row blocks that read the same keys do.
-  const int id = blockIdx.x;
-  const int unit = id / (8 * row_blocks) * 8 + id % 8;
-  const int hk = unit % a.Hkv;
-  const uint32_t share = unit / a.Hkv;
-  const int block_row0 = id / 8 % row_blocks * block_rows;
+  int hk = blockIdx.x, block_row0 = 0;
+  uint32_t share = blockIdx.y;
+  if (row_blocks > 1) {
+    const int id = blockIdx.x;
+    const int unit = id / (8 * row_blocks) * 8 + id % 8;
+    hk = unit % a.Hkv;
+    share = unit / a.Hkv;
+    block_row0 = id / 8 % row_blocks * block_rows;
+  }
   int b;
   uint32_t before;
   Window window;
   const Plan plan = make_plan(a, shares, share, b, before, window);
   if (b >= a.B) return;
   const uint32_t share_begin = plan.start(share), share_end = plan.start(share + 1);
-  const int group = a.H / a.Hkv;
+  const int group = a.group;
   const Parts parts = parts_of(a, shares, a.max_new * group);
+  // row / group
+  auto token_of = [&](int row) {
+    const int t = __umulhi(row, a.group_inverse);
+    return t + (row - t * group >= group ? 1 : 0);
+  };
   const int per_page = 1 << (a.page_shift - 4);  // 16-token blocks of a page
 
   // This wave's stages, and the lane's places in one: its first key's quarter row (the other
@@ -251,9 +264,11 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
     int end = min(steps, (int)(share_end - first_step));
     before += weight;
     if (end <= begin) continue;
-    const uint32_t s0 = plan.share_of(first_step), s1 = plan.share_of(first_step + steps - 1);
-    if (threadIdx.x == 0 && hk == 0 && block_row0 == 0 && share == s0)
-      parts.plan[b] = {(int)s0, (int)s1};
+    // whether the request begins in this share, and whether all of it is there
+    const bool begins = first_step >= share_begin;
+    const bool whole = begins && first_step + steps <= share_end;
+    if (threadIdx.x == 0 && hk == 0 && block_row0 == 0 && begins)
+      parts.plan[b] = {(int)share, whole ? (int)share : (int)plan.share_of(first_step + steps - 1)};
     const int rows = n_new * group;
     if (block_row0 >= rows) continue;
     // Steps count without the gap: step v is the request's step v, or v + gap behind the sinks.
@@ -261,9 +276,9 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
     int gap = r.gap, skip = 0;  // of this row block: what its own window passes over besides
     if (!a.mask) {  // a chain: nothing past the last row's token, or before the first's window
       const int last = min(block_row0 + block_rows, rows) - 1;
-      const int to = (ctx + last / group + 32) >> 5;
+      const int to = (ctx + token_of(last) + 32) >> 5;
       end = min(end, to <= sink_steps ? to : max(sink_steps, to - gap));
-      if (gap > 0) skip = max(0, ((ctx + block_row0 / group + 1 - a.window) >> 5) - gap - sink_steps);
+      if (gap > 0) skip = max(0, ((ctx + token_of(block_row0) + 1 - a.window) >> 5) - gap - sink_steps);
     }
     auto actual = [&](int v) { return v < sink_steps ? v : v + gap; };
     auto following = [&](int v) { return v >= sink_steps && v < sink_steps + skip ? sink_steps + skip : v; };
@@ -279,10 +294,10 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
       const int row = row0 + 16 * g + c % kRows;
-      tok[g] = row / group;
+      tok[g] = token_of(row);
       const int64_t at = (int64_t)cu + tok[g];
       in[g] = row < rows && at >= 0 && at < a.T;
-      const uint16_t* from = a.q + at * a.q_st + (int64_t)(hk * group + row % group) * a.q_sh + p * 8 * DT;
+      const uint16_t* from = a.q + at * a.q_st + (int64_t)(hk * group + row - tok[g] * group) * a.q_sh + p * 8 * DT;
 #pragma unroll
       for (int i = 0; i < DT; ++i)
         q[g][i] = in[g] ? *reinterpret_cast<const u32x4*>(from + 8 * i) : u32x4{};
@@ -591,14 +606,14 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
       if (row >= rows || c >= kRows) return;
       const int d4 = d4_of(j);
       const float top = ref == -INFINITY ? ref : ref - kTop;
-      if (s0 != s1) {
-        const int64_t place = 2 * (int64_t)share + (share == s0 ? 1 : 0);
+      if (!whole) {
+        const int64_t place = 2 * (int64_t)share + (begins ? 1 : 0);
         const int64_t at = (place * a.Hkv + hk) * (a.max_new * group) + row;
         parts.out[at * (D / 4) + d4] = v;
         if (d4 == 0) parts.stat[at] = {top, sum};
       } else if (in[g]) {
         const int64_t t = (int64_t)cu + tok[g];
-        const int h = hk * group + row % group;
+        const int h = hk * group + row - tok[g] * group;
         const float zero = top == -INFINITY ? 0.0f : top;
         write_row<E>(a, t, h, d4, v, zero, sum);
       }
@@ -679,7 +694,8 @@ hipError_t launch_rows(const Kv4AttentionArgs& a, hipStream_t stream) {
   p.shares = (int)std::min<int64_t>(
       p.shares, std::max<int64_t>(1, a.B * (a.kHead + room) / a.kMinShare));
   const int64_t units = (int64_t)p.shares * a.Hkv;
-  const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.row_blocks));
+  const dim3 grid = p.row_blocks == 1 ? dim3((unsigned)a.Hkv, (unsigned)p.shares)
+                                      : dim3((unsigned)((units + 7) / 8 * 8 * p.row_blocks));
   // stages: what a workgroup's share of a compute unit's LDS holds
   constexpr int S = DT <= 4 ? 3 : 2, S2 = 4;
   auto* kernel = p.fold == 4   ? kv4_attention_kernel<E, DT, 1, 4, S>

@@ -34,8 +34,16 @@ __device__ __forceinline__ float row_max(float x) {
 }
 template <int RW>
 __device__ __forceinline__ float row_sum(float x) {
-  if constexpr (RW == 16) x += __shfl_xor(x, 16);
-  return x + __shfl_xor(x, 32);
+  if constexpr (RW == 16) {
+    const uint32_t v = __builtin_bit_cast(uint32_t, x);
+    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+    const uint32_t b0 = b[0], b1 = b[1];
+    x = __builtin_bit_cast(float, b0) + __builtin_bit_cast(float, b1);
+  }
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(u, u, false, false));
+  const uint32_t a0 = a[0], a1 = a[1];
+  return __builtin_bit_cast(float, a0) + __builtin_bit_cast(float, a1);
 }
 
 // the low n bits, n clamped to 0 .. 8
@@ -85,12 +93,18 @@ __device__ __forceinline__ Request load_request(const A& a, int b) {
   return b < a.B ? make_request(a, a.cu[b], a.cu[b + 1], a.ctx[b]) : Request{};
 }
 
-__device__ __forceinline__ uint32_t inclusive_sum(uint32_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const uint32_t u = __shfl_up(v, o);
-    if (lane >= o) v += u;
-  }
+// Sums over the lanes up to each, by DPP moves (a move through LDS takes ten times as long): within rows
+// of 16, then a row's last lane into the next row, and the first half's into the second.
+__device__ __forceinline__ uint32_t inclusive_sum(uint32_t v) {
+#define FLEXQ_SCAN_STEP(ctrl, rows) \
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xF, false)
+  FLEXQ_SCAN_STEP(0x111, 0xF);  // row_shr:1, 2, 4, 8
+  FLEXQ_SCAN_STEP(0x112, 0xF);
+  FLEXQ_SCAN_STEP(0x114, 0xF);
+  FLEXQ_SCAN_STEP(0x118, 0xF);
+  FLEXQ_SCAN_STEP(0x142, 0xA);  // row_bcast:15 into rows 1 and 3
+  FLEXQ_SCAN_STEP(0x143, 0xC);  // row_bcast:31 into rows 2 and 3
+#undef FLEXQ_SCAN_STEP
   return v;
 }
 
@@ -126,7 +140,7 @@ __device__ __forceinline__ Plan make_plan(const A& a, uint32_t shares, uint32_t 
   if (lane * per < a.B) sum = window.mine.template weight<A>();
 #pragma unroll 4
   for (int j = 1; j < per; ++j) sum += load_request(a, lane * per + j).template weight<A>();
-  const uint32_t inc = inclusive_sum(sum, lane);
+  const uint32_t inc = inclusive_sum(sum);
   const uint32_t total = __builtin_amdgcn_readlane(inc, 63);
   Plan plan;
   plan.shares = min(shares, max(1u, total / A::kMinShare));
@@ -143,7 +157,7 @@ __device__ __forceinline__ Plan make_plan(const A& a, uint32_t shares, uint32_t 
     window.base = b;
     window.mine = load_request(a, b + lane);
     const uint32_t w = lane < per ? window.mine.template weight<A>() : 0;
-    const uint32_t in = inclusive_sum(w, lane);
+    const uint32_t in = inclusive_sum(w);
     const int k = __builtin_ctzll(__ballot(before + in > x));
     before += __builtin_amdgcn_readlane(in - w, k);
     b += k;
