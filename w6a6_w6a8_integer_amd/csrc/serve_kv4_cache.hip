@@ -10,68 +10,115 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Threads that share a head row of D elements, eight each (16 with four that have none for
-// D = 96), all in one wave.
+// Threads that share a head row of D elements: two words of eight elements each, word `lane` and word
+// `lane + kLanes` (of 96-wide rows the last four have one).
 template <int D>
-constexpr int kLanes = D == 96 ? 16 : D / 8;
+constexpr int kLanes = D == 64 ? 4 : D == 256 ? 16 : 8;
 
-// extremes over N neighbouring lanes
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("v_min3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
+}
+// smallest and largest over N neighbouring lanes: swap pairs, pairs of pairs, mirror 8, mirror 16
 template <int N>
-__device__ __forceinline__ float lanes_min(float x) {
-#pragma unroll
-  for (int o = 1; o < N; o *= 2) x = fminf(x, __shfl_xor(x, o));
-  return x;
-}
-template <int N>
-__device__ __forceinline__ float lanes_max(float x) {
-#pragma unroll
-  for (int o = 1; o < N; o *= 2) x = fmaxf(x, __shfl_xor(x, o));
-  return x;
+__device__ __forceinline__ void extremes(float& low, float& high) {
+  low = fminf(low, moved<0xB1>(low)), high = fmaxf(high, moved<0xB1>(high));
+  low = fminf(low, moved<0x4E>(low)), high = fmaxf(high, moved<0x4E>(high));
+  if constexpr (N >= 8) low = fminf(low, moved<0x141>(low)), high = fmaxf(high, moved<0x141>(high));
+  if constexpr (N >= 16) low = fminf(low, moved<0x140>(low)), high = fmaxf(high, moved<0x140>(high));
 }
 
-// rint((x - b) / s) clamped to 0 .. 15, s > 0, r = 1 / s.  The quotient is first taken as
-// q = (x - b) r, within 2^-18 of the correctly rounded one where that is below 32 (beyond, both
-// clamp); only where q is that near to a rounding boundary (told with room, 2^-15) is the
-// quotient itself formed.
-__device__ __forceinline__ uint32_t code_of(float x, float b, float s, float r) {
-  const float d = x - b, q = d * r;
-  float k = rintf(q);
-  if (fabsf(fabsf(q - k) - 0.5f) < 0x1p-15f) k = rintf(d / s);
-  return (uint32_t)fminf(fmaxf(k, 0.0f), 15.0f);
+// x / 15 correctly rounded (the quotient by the rounded reciprocal, and its remainder added).
+__device__ __forceinline__ float by_15(float x) {
+  const float r = 1.0f / 15.0f, q = x * r;
+  return fmaf(fmaf(-15.0f, q, x), r, q);
 }
 
-// A lane's eight elements of a row that N lanes share, as codes (element e at bits 4 e); s and b
+// A lane's two words of a row that N lanes share, as codes (element e of a word at bits 4 e); s and b
 // receive the row's scale and offset as fp16.  A row that fp16 scales cannot hold (a NaN in it, or
-// s or b not finite) gets NaN for both.  Every lane of the row takes part; `some`: it has
-// elements.
+// s or b not finite) gets NaN for both.  `some`: the second word is there.
+//
+// rint((x - b) / s): the quotient is first taken as q = (x - b) r with r = 1 / s to within a step, so
+// q is within 2^-17 of the correctly rounded quotient where that is below 32 (beyond, both clamp).
+// Where some q is that near to a rounding boundary (told with room, 2^-15: one wave in thirty)
+// the quotients themselves are formed.  Adding 1.5 2^23 rounds q to a whole number in its low bits.
 template <class E, int N>
-__device__ __forceinline__ uint32_t quantize_row(const u32x4 v, bool some, uint16_t& s, uint16_t& b) {
-  float x[8];
-  float low = INFINITY, high = -INFINITY, nan = 0.0f;
+__device__ __forceinline__ u32x2 quantize_row(const u32x4 (&v)[2], bool some, uint16_t& s, uint16_t& b) {
+  float x[2][8];
+  float low, high, finite = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = E::value((uint16_t)(e & 1 ? v[e >> 1] >> 16 : v[e >> 1] & 0xFFFFu));
-    if (some) {
-      low = fminf(low, x[e]);
-      high = fmaxf(high, x[e]);
-      nan = x[e] != x[e] ? 1.0f : nan;
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const uint32_t two = v[w][e >> 1];
+      x[w][e] = E::value((uint16_t)(two & 0xFFFFu));
+      x[w][e + 1] = E::value((uint16_t)(two >> 16));
+    }
+  low = high = x[0][0];
+  finite = x[0][0] * 0.0f;
+#pragma unroll
+  for (int e = 1; e < 8; ++e) finite = fmaf(x[0][e], 0.0f, finite);
+#pragma unroll
+  for (int e = 1; e < 7; e += 2) {
+    low = min3(low, x[0][e], x[0][e + 1]);
+    high = max3(high, x[0][e], x[0][e + 1]);
+  }
+  low = fminf(low, x[0][7]), high = fmaxf(high, x[0][7]);
+  if (some) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) finite = fmaf(x[1][e], 0.0f, finite);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      low = min3(low, x[1][e], x[1][e + 1]);
+      high = max3(high, x[1][e], x[1][e + 1]);
     }
   }
-  low = lanes_min<N>(low);
-  high = lanes_max<N>(high);
-  nan = lanes_max<N>(nan);
+  if (finite != 0.0f) high = INFINITY;  // (NaN: an infinity or a NaN was there)
+  extremes<N>(low, high);
   b = Half::bits(low);
-  s = Half::bits((high - low) / 15.0f);
-  if (nan != 0.0f || (b & 0x7C00u) == 0x7C00u || (s & 0x7C00u) == 0x7C00u) {
-    b = s = 0x7E00u;
-    return 0;
-  }
+  s = Half::bits(by_15(high - low));
+  if ((b & 0x7C00u) == 0x7C00u || (s & 0x7C00u) == 0x7C00u) b = s = 0x7E00u;
   const float sf = Half::value(s), bf = Half::value(b);
-  if (sf == 0.0f) return 0;
-  const float r = 1.0f / sf;
-  uint32_t codes = 0;
+  if (!(sf > 0.0f)) return u32x2{0, 0};
+  const float r = __builtin_amdgcn_rcpf(sf);
+  constexpr float kRound = 12582912.0f;
+  constexpr uint32_t kRounds = 0x4B400000u * 0x111u;  // its bits, eight times over (mod 2^32 three)
+  u32x2 codes;
+  float near = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) codes |= code_of(x[e], bf, sf, r) << (4 * e);
+  for (int w = 0; w < 2; ++w) {
+    uint32_t sum = 0;
+#pragma unroll
+    for (int e = 7; e >= 0; --e) {
+      const float q = __builtin_amdgcn_fmed3f((x[w][e] - bf) * r, 0.0f, 15.0f), m = q + kRound;
+      near = fmaxf(near, fabsf(q - (m - kRound)));
+      sum = (sum << 4) + __float_as_uint(m);
+    }
+    codes[w] = sum - kRounds;
+  }
+  if (near > 0.5f - 0x1p-15f) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t sum = 0;
+#pragma unroll
+      for (int e = 7; e >= 0; --e) {
+        const float q = __builtin_amdgcn_fmed3f((x[w][e] - bf) / sf, 0.0f, 15.0f);
+        sum = (sum << 4) + __float_as_uint(q + kRound);
+      }
+      codes[w] = sum - kRounds;
+    }
+  }
   return codes;
 }
 
@@ -99,10 +146,23 @@ __device__ __forceinline__ int byte_of(int r) { return (r >> 1 & 1) | (r & 1) <<
 
 }  // namespace
 
+// Four dwords' bytes as four dwords of one byte of each, in the order 0, 2, 1, 3 of the tokens.
+__device__ __forceinline__ void turn(const uint32_t (&c)[4], uint32_t (&o)[4]) {
+  const uint32_t low02 = __builtin_amdgcn_perm(c[2], c[0], 0x05010400u);
+  const uint32_t high02 = __builtin_amdgcn_perm(c[2], c[0], 0x07030602u);
+  const uint32_t low13 = __builtin_amdgcn_perm(c[3], c[1], 0x05010400u);
+  const uint32_t high13 = __builtin_amdgcn_perm(c[3], c[1], 0x07030602u);
+  o[0] = __builtin_amdgcn_perm(low13, low02, 0x05040100u);
+  o[1] = __builtin_amdgcn_perm(low13, low02, 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(high13, high02, 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(high13, high02, 0x07060302u);
+}
+
 // One workgroup = TOKENS tokens of one head.  kLanes lanes a row find its extremes and form its codes;
-// the keys' go to the cache at once, the values' through LDS, where eight tokens of consecutive
-// slots from a multiple of eight become whole 32-byte pieces of four pairs of d.  Other
-// tokens are written byte by byte, so that no token's codes are read to write another's.
+// the keys' go to the cache at once, the values' and the scales through LDS, where eight
+// tokens of consecutive slots from a multiple of eight become whole 32-byte pieces of four pairs
+// of d and 16-byte pieces of scales.  Other tokens are written byte by byte (scales half by half),
+// so that no token's codes are read to write another's.
 template <class E, int D, int TOKENS>
 __global__ __launch_bounds__(kThreads) void kv4_cache_write_kernel(
     const uint16_t* __restrict__ k, int64_t k_st, int64_t k_sh, const uint16_t* __restrict__ v,
@@ -110,105 +170,114 @@ __global__ __launch_bounds__(kThreads) void kv4_cache_write_kernel(
     int shift, uint32_t* __restrict__ kc, uint32_t* __restrict__ vc, uint16_t* __restrict__ sc) {
   constexpr int N = kLanes<D>, kWords = D / 8;
   __shared__ uint32_t tile[TOKENS * kWords];  // value codes, element e at bits 4 e
+  __shared__ __attribute__((aligned(16))) uint16_t scales[4][TOKENS];
   __shared__ int slot_of[TOKENS + 8];         // -1 where a token is dropped
-  __shared__ uint64_t led;                    // tokens that begin eight consecutive slots
-  static_assert(TOKENS <= 64, "one bit a token");
+  __shared__ int eights[TOKENS / 8 + 1], singles[TOKENS];  // tokens that begin eight slots; alone
+  __shared__ int num_eights, num_singles;
+  static_assert(TOKENS <= 64, "one lane a token");
   const int h = blockIdx.y, t0 = blockIdx.x * TOKENS, tid = threadIdx.x;
   if (tid < TOKENS + 8) {
     const int64_t slot = tid < TOKENS && t0 + tid < T ? slots[t0 + tid] : -1;
     slot_of[tid] = slot >= 0 && slot < num_slots ? (int)slot : -1;
   }
   __syncthreads();
-  if (tid < 64) {
-    bool leads = tid < TOKENS && slot_of[tid] >= 0 && (slot_of[tid] & 7) == 0;
-    for (int i = 1; leads && i < 8; ++i) leads = slot_of[tid + i] == slot_of[tid] + i;
+  // rows of this thread's turns: the keys, then the values
+  const int lane = tid % N;
+  const bool some = lane + N < kWords;
+  constexpr int kTurns = 2 * TOKENS * N / kThreads > 0 ? 2 * TOKENS * N / kThreads : 1;
+  u32x4 x[kTurns][2];
+#pragma unroll
+  for (int u = 0; u < kTurns; ++u) {
+    const int row = tid / N + u * (kThreads / N), i = row % TOKENS;
+    const bool value = row >= TOKENS;
+    x[u][0] = x[u][1] = u32x4{};
+    if (row < 2 * TOKENS && slot_of[i] >= 0) {
+      const uint16_t* from = value ? v + (int64_t)(t0 + i) * v_st + h * v_sh
+                                   : k + (int64_t)(t0 + i) * k_st + h * k_sh;
+      x[u][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + 8 * lane));
+      if (some) x[u][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + 8 * (lane + N)));
+    }
+  }
+  if (tid < 64) {  // (while the rows are on their way)
+    const int slot = tid < TOKENS ? slot_of[tid] : -1;
+    bool leads = slot >= 0 && (slot & 7) == 0;
+    for (int i = 1; leads && i < 8; ++i) leads = slot_of[tid + i] == slot + i;
     const uint64_t all = __ballot(leads);
-    if (tid == 0) led = all;
+    // alone: kept, and no token up to seven before begins eight that hold this one
+    const bool alone = slot >= 0 && (all & (tid >= 7 ? 0xFFull << (tid - 7) : 0xFFull >> (7 - tid))) == 0;
+    const uint64_t some_alone = __ballot(alone);
+    const uint64_t below = (1ull << tid) - 1;
+    if (leads) eights[__builtin_popcountll(all & below)] = tid;
+    if (alone) singles[__builtin_popcountll(some_alone & below)] = tid;
+    if (tid == 0) {
+      num_eights = __builtin_popcountll(all);
+      num_singles = __builtin_popcountll(some_alone);
+    }
   }
   auto block_of = [&](int slot) {
     const int r = slot & ((1 << shift) - 1);
     return ((int64_t)(slot >> shift) * Hkv + h) * (1 << (shift - 4)) + (r >> 4);
   };
-  // rows of this turn's lanes: the keys, then the values
-  const int lane = tid % N;
-  const bool some = lane < kWords;
-  constexpr int kTurns = (2 * TOKENS * N + kThreads - 1) / kThreads;
-  u32x4 x[kTurns];
-#pragma unroll
-  for (int u = 0; u < kTurns; ++u) {
-    const int row = tid / N + u * (kThreads / N), i = row % TOKENS;
-    const bool value = row >= TOKENS;
-    x[u] = u32x4{};
-    if (row < 2 * TOKENS && some && slot_of[i] >= 0) {
-      const uint16_t* from = value ? v + (int64_t)(t0 + i) * v_st + h * v_sh
-                                   : k + (int64_t)(t0 + i) * k_st + h * k_sh;
-      x[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + 8 * lane));
-    }
-  }
 #pragma unroll
   for (int u = 0; u < kTurns; ++u) {
     const int row = tid / N + u * (kThreads / N), i = row % TOKENS;
     const bool value = row >= TOKENS;
     uint16_t s, b;
-    const uint32_t codes = quantize_row<E, N>(x[u], some, s, b);
+    const u32x2 codes = quantize_row<E, N>(x[u], some, s, b);
     const int slot = row < 2 * TOKENS ? slot_of[i] : -1;
     if (slot < 0) continue;
-    const int64_t block = block_of(slot);
-    const int r = slot & 15;
     if (lane == 0) {
-      uint16_t* to = sc + block * 64 + (value ? 32 : 0) + r;
-      to[0] = s;
-      to[16] = b;
+      scales[value ? 2 : 0][i] = s;
+      scales[value ? 3 : 1][i] = b;
     }
-    if (!some) continue;
-    if (value)
-      tile[i * kWords + lane] = codes;
-    else
-      kc[block * (2 * D) + r * kWords + lane] = key_order(codes);
+    if (value) {
+      tile[i * kWords + lane] = codes[0];
+      if (some) tile[i * kWords + lane + N] = codes[1];
+    } else {
+      uint32_t* to = kc + block_of(slot) * (2 * D) + (slot & 15) * kWords + lane;
+      to[0] = key_order(codes[0]);
+      if (some) to[N] = key_order(codes[1]);
+    }
   }
   __syncthreads();
-  const uint64_t leads = led;
-  for (int i = tid; i < TOKENS * kWords; i += kThreads) {
-    const int t = i / kWords, w = i % kWords;
-    const int slot = slot_of[t];
-    if (slot < 0) continue;
-    // whether a token up to seven before leads eight that hold this one
-    if ((leads >> t & 1) != 0) {
-      uint32_t c[8];
+  for (int i = tid; i < num_eights * kWords; i += kThreads) {
+    const int t = eights[i / kWords], w = i % kWords, slot = slot_of[t];
+    uint32_t* const to = vc + block_of(slot) * (2 * D) + (slot >> 3 & 1) * D + 8 * w;
+    uint32_t c[2][4], o[2][4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) c[j] = tile[(t + j) * kWords + w];
-      u32x4 out[2];
+    for (int q = 0; q < 2; ++q) {
 #pragma unroll
-      for (int pair = 0; pair < 4; ++pair)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t o = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o |= (c[4 * q + j] >> (8 * pair) & 0xFFu) << (8 * (j >> 1 | (j & 1) << 1));
-          out[pair >> 1][2 * (pair & 1) + q] = o;
-        }
-      u32x4* to = reinterpret_cast<u32x4*>(vc + block_of(slot) * (2 * D) + (slot >> 3 & 1) * D + 8 * w);
-      to[0] = out[0];
-      to[1] = out[1];
-    } else if ((leads & (t >= 7 ? 0x7Full << (t - 7) : 0x7Full >> (7 - t))) == 0) {
-      uint8_t* to = reinterpret_cast<uint8_t*>(vc + block_of(slot) * (2 * D) + (slot >> 3 & 1) * D +
-                                               8 * w + (slot >> 2 & 1)) +
-                    byte_of(slot);
-      const uint32_t c = tile[t * kWords + w];
-#pragma unroll
-      for (int pair = 0; pair < 4; ++pair) to[8 * pair] = (uint8_t)(c >> (8 * pair));
+      for (int j = 0; j < 4; ++j) c[q][j] = tile[(t + 4 * q + j) * kWords + w];
+      turn(c[q], o[q]);
     }
+    reinterpret_cast<u32x4*>(to)[0] = u32x4{o[0][0], o[1][0], o[0][1], o[1][1]};
+    reinterpret_cast<u32x4*>(to)[1] = u32x4{o[0][2], o[1][2], o[0][3], o[1][3]};
+    if (w < 4) {
+      u32x4 eight;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        eight[j] = scales[w][t + 2 * j] | (uint32_t)scales[w][t + 2 * j + 1] << 16;
+      *reinterpret_cast<u32x4*>(sc + block_of(slot) * 64 + 16 * w + (slot & 8)) = eight;
+    }
+  }
+  for (int i = tid; i < num_singles * kWords; i += kThreads) {
+    const int t = singles[i / kWords], w = i % kWords, slot = slot_of[t];
+    uint8_t* to = reinterpret_cast<uint8_t*>(vc + block_of(slot) * (2 * D) + (slot >> 3 & 1) * D + 8 * w +
+                                             (slot >> 2 & 1)) + byte_of(slot);
+    const uint32_t c = tile[t * kWords + w];
+#pragma unroll
+    for (int pair = 0; pair < 4; ++pair) to[8 * pair] = (uint8_t)(c >> (8 * pair));
+    if (w < 4) sc[block_of(slot) * 64 + 16 * w + (slot & 15)] = scales[w][t];
   }
 }
 
-// kLanes lanes a token and head: x = b + s c, rounded once.  A token outside the cache reads as 0.
+// A lane a word of eight elements of a token and head: x = b + s c, rounded once.  A token outside the cache reads as 0.
 template <class E, int D>
 __global__ __launch_bounds__(kThreads) void kv4_cache_read_kernel(
     const uint32_t* __restrict__ kc, const uint32_t* __restrict__ vc,
     const uint16_t* __restrict__ sc, const int* __restrict__ slots, int64_t rows, int Hkv,
     int64_t num_slots, int shift, uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
-  constexpr int N = kLanes<D>, kWords = D / 8;
+  constexpr int N = D == 96 ? 16 : D / 8, kWords = D / 8;
   const int lane = threadIdx.x % N;
   const int64_t row = (int64_t)blockIdx.x * (kThreads / N) + threadIdx.x / N;  // (token, head)
   if (row >= rows || lane >= kWords) return;
