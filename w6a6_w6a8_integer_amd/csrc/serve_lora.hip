@@ -35,29 +35,35 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& a, int64_t t0, int lan
   return id >= 0 && id < a.L ? id : -1;
 }
 
-// The tokens of one adapter in the tile, as this wave sees them: its 16 columns, if it has any, and
-// which part of the other axis it takes.
+// The tokens of one adapter in the tile, as this wave sees them: its CT times 16 columns, if it has any,
+// and which part of the other axis it takes.
+template <int CT>
 struct Columns {
-  int token;        // of the lane's column in the tile; where there is none, the first
-  bool in;          // the column exists
+  int token[CT];    // of the lane's columns in the tile; where there is none, the first
+  bool in[CT];      // the column exists
   int parts, part;  // waves that share the columns, and which of them this is
   bool idle;
 };
 
-__device__ __forceinline__ Columns columns_of(uint64_t members, int lane, int wave) {
+template <int CT>
+__device__ __forceinline__ Columns<CT> columns_of(uint64_t members, int lane, int wave) {
   const int n = __builtin_popcountll(members);
   const bool mine = members >> lane & 1;
   // lane i receives the i-th member (behind them the other tokens follow: every lane has a place)
   const int rank = __builtin_popcountll(members & ((1ull << lane) - 1));
   const int list = __builtin_amdgcn_ds_permute((mine ? rank : n + lane - rank) << 2, lane);
-  Columns c;
-  c.parts = n <= 16 ? 4 : n <= 32 ? 2 : 1;
+  Columns<CT> c;
+  const int shift = n <= 16 * CT ? 2 : n <= 32 * CT ? 1 : 0;
+  c.parts = 1 << shift;
   c.part = wave & (c.parts - 1);
-  const int first = wave / c.parts * 16;
-  const int column = first + (lane & 15);
-  c.in = column < n;
+  const int first = (wave >> shift) * (16 * CT);
+#pragma unroll
+  for (int i = 0; i < CT; ++i) {
+    const int column = first + 16 * i + (lane & 15);
+    c.in[i] = column < n;
+    c.token[i] = __builtin_amdgcn_ds_bpermute((c.in[i] ? column : 0) << 2, list);
+  }
   c.idle = first >= n;
-  c.token = __builtin_amdgcn_ds_bpermute((c.in ? column : 0) << 2, list);
   return c;
 }
 
@@ -80,10 +86,10 @@ __device__ __forceinline__ void each_adapter(int id, int turn, int turns, F&& f)
 
 // h: one workgroup = a tile's adapters (those of its turn) and a slice of K.  Waves that the columns
 // leave over share the slice and add up in LDS.  RT: 16-row tiles of an adapter at most.
-template <class E, int RT>
+template <class E, int RT, int CT>
 __global__ __launch_bounds__(64 * kWaves) void lora_shrink_kernel(const LoraArgs a, int turns,
                                                                  int slices) {
-  __shared__ __attribute__((aligned(16))) f32x4 sums[(kWaves - 1) * RT * 64];
+  __shared__ __attribute__((aligned(16))) f32x4 sums[(kWaves - 1) * RT * CT * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, p = lane >> 4;
@@ -97,65 +103,96 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_kernel(const LoraArgs
   each_adapter(id, turn, turns, [&](int cur, uint64_t members) {
     const int rank = a.ranks ? min(max(0, a.ranks[cur]), a.R) : a.R;
     const int tiles = (rank + 15) / 16;
-    const Columns col = columns_of(members, lane, wave);
-    f32x4 h[RT] = {};
+    const Columns<CT> col = columns_of<CT>(members, lane, wave);
+    f32x4 h[CT][RT] = {};
     if (!col.idle) {
       const int n = (k1 - k0) / col.parts, at = k0 + n * col.part + 8 * p;
-      const uint16_t* x = a.x + (t0 + col.token) * a.x_st + at;
-      const uint16_t* w = a.a + ((int64_t)cur * a.R) * a.K + at;
-      int64_t row[RT];  // (rows past the adapter's last are read again, and not used)
+      const uint16_t* x[CT];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) row[i] = (int64_t)min(16 * i + c, a.R - 1) * a.K;
-      constexpr int kUnroll = RT <= 2 ? 8 : RT == 4 ? 4 : 2;
+      for (int j = 0; j < CT; ++j) x[j] = a.x + (t0 + col.token[j]) * a.x_st + at;
+      const uint16_t* w[RT];  // (rows past the adapter's last are read again, and not used)
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        w[i] = a.a + ((int64_t)cur * a.R + min(16 * i + c, a.R - 1)) * a.K + at;
+      constexpr int kUnroll = RT * CT <= 2 ? 8 : RT * CT <= 8 ? 4 : 2;
       int k = 0;
       for (; k + 32 * kUnroll <= n; k += 32 * kUnroll) {
-        u32x4 xf[kUnroll], wf[kUnroll][RT];
+        u32x4 xf[kUnroll][CT], wf[kUnroll][RT];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          xf[u] = *reinterpret_cast<const u32x4*>(x + k + 32 * u);
+#pragma unroll
+          for (int j = 0; j < CT; ++j) xf[u][j] = *reinterpret_cast<const u32x4*>(x[j] + k + 32 * u);
 #pragma unroll
           for (int i = 0; i < RT; ++i)
-            if (i < tiles) wf[u][i] = *reinterpret_cast<const u32x4*>(w + row[i] + k + 32 * u);
+            if (i < tiles) wf[u][i] = *reinterpret_cast<const u32x4*>(w[i] + k + 32 * u);
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
           for (int i = 0; i < RT; ++i)
-            if (i < tiles) h[i] = E::mfma(wf[u][i], xf[u], h[i]);
+#pragma unroll
+            for (int j = 0; j < CT; ++j)
+              if (i < tiles) h[j][i] = E::mfma(wf[u][i], xf[u][j], h[j][i]);
       }
       for (; k < n; k += 32) {
-        const u32x4 xf = *reinterpret_cast<const u32x4*>(x + k);
+        u32x4 xf[CT];
+#pragma unroll
+        for (int j = 0; j < CT; ++j) xf[j] = *reinterpret_cast<const u32x4*>(x[j] + k);
 #pragma unroll
         for (int i = 0; i < RT; ++i)
-          if (i < tiles) h[i] = E::mfma(*reinterpret_cast<const u32x4*>(w + row[i] + k), xf, h[i]);
+          if (i < tiles) {
+            const u32x4 wf = *reinterpret_cast<const u32x4*>(w[i] + k);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) h[j][i] = E::mfma(wf, xf[j], h[j][i]);
+          }
       }
     }
     if (col.parts > 1) {
+      auto place = [&](int of, int j, int i) {
+        return (((of - of / col.parts - 1) * CT + j) * RT + i) * 64 + lane;
+      };
       __syncthreads();  // the sums of the adapter before have been read
       if (col.part > 0)
 #pragma unroll
-        for (int i = 0; i < RT; ++i) sums[((wave - wave / col.parts - 1) * RT + i) * 64 + lane] = h[i];
+        for (int j = 0; j < CT; ++j)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) sums[place(wave, j, i)] = h[j][i];
       __syncthreads();
       if (col.part > 0) return;
       for (int q = 1; q < col.parts; ++q)
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const int from = wave + q;
-          h[i] += sums[((from - from / col.parts - 1) * RT + i) * 64 + lane];
-        }
-    }
-    if (!col.in) return;
-    float* to = a.h + ((int64_t)slice * a.T + t0 + col.token) * (16 * RT) + 4 * p;
+        for (int j = 0; j < CT; ++j)
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-      if (i < tiles) *reinterpret_cast<f32x4*>(to + 16 * i) = h[i];
+          for (int i = 0; i < RT; ++i) h[j][i] += sums[place(wave + q, j, i)];
+    }
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+      if (!col.in[j]) continue;
+      float* to = a.h + ((int64_t)slice * a.T + t0 + col.token[j]) * (16 * RT) + 4 * p;
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        if (i < tiles) *reinterpret_cast<f32x4*>(to + 16 * i) = h[j][i];
+    }
   });
 }
 
-// out: one workgroup = a tile's adapters (those of its turn) and `units` times 64 columns of out for each
-// wave that shares a token's.  Row r of the MFMA's 16-row tile i is n = 16 (r / 4) + 4 i + r % 4
-// of 64, so that a lane ends up with 16 consecutive n of its token.
-template <class E, int RT>
+// The slices' sums, into the first slice's place.  (What lies past a token's rank is summed as it is, and
+// not used.)
+__global__ __launch_bounds__(256) void lora_join_kernel(float* h, int64_t quads, int slices) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= quads) return;
+  f32x4* at = reinterpret_cast<f32x4*>(h) + i;
+  f32x4 sum = at[0];
+#pragma unroll 4
+  for (int q = 1; q < slices; ++q) sum += at[q * quads];
+  at[0] = sum;
+}
+
+// out: one workgroup = a tile's adapters (those of its turn) and a block of out's columns, in units of 64
+// that the waves which share a token's take in turn, the next one's loads on their way while
+// one is worked on.  Row r of the MFMA's 16-row tile i is n = 16 (r / 4) + 4 i + r % 4 of the
+// unit, so that a lane ends up with 16 consecutive n of its tokens.
+template <class E, int RT, int CT>
 __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs a, int turns,
                                                                  int blocks, int slices) {
   constexpr int KS = (RT + 1) / 2;  // 32-deep steps over the rank
@@ -180,93 +217,136 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
   each_adapter(id, turn, turns, [&](int cur, uint64_t members) {
     const int rank = a.ranks ? min(max(0, a.ranks[cur]), a.R) : a.R;
     const float by = a.scales ? a.scales[cur] : 1.0f;
-    const Columns col = columns_of(members, lane, wave);
+    const Columns<CT> col = columns_of<CT>(members, lane, wave);
     if (col.idle) return;
-    const int64_t t = t0 + col.token;
-    // this lane's eight of each 32 of h, scaled, their largest, and their two parts
-    float h[KS][8];
-    float most = 0.0f;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      f32x4 part[2] = {};
-      const int r = 32 * s + 8 * p;
-      if (r < rank) {
-        const float* from = a.h + t * (16 * RT) + r;
-        for (int q = 0; q < slices; ++q)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            part[j] += *reinterpret_cast<const f32x4*>(from + (int64_t)q * a.T * (16 * RT) + 4 * j);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[s][e] = r + e < rank ? part[e >> 2][e & 3] * by : 0.0f;
-        most = fmaxf(most, fabsf(h[s][e]));
-      }
-    }
-    most = column_max(most);
-    const int up = 15 - __builtin_amdgcn_frexp_expf(most);
-    u32x4 hi[KS], lo[KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v0 = __builtin_amdgcn_ldexpf(h[s][2 * i], up);
-        const float v1 = __builtin_amdgcn_ldexpf(h[s][2 * i + 1], up);
-        const uint32_t b0 = E::bits(v0), b1 = E::bits(v1);
-        // (an infinite or NaN h is its first part alone)
-        const float r0 = v0 - E::value((uint16_t)b0), r1 = v1 - E::value((uint16_t)b1);
-        hi[s][i] = b0 | b1 << 16;
-        lo[s][i] = E::bits(fabsf(r0) < INFINITY ? r0 : 0.0f) |
-                   (uint32_t)E::bits(fabsf(r1) < INFINITY ? r1 : 0.0f) << 16;
-      }
     const uint16_t* w = a.b + (int64_t)cur * a.N * a.R;
     const int n_of = 16 * (c >> 2) + (c & 3);
-    for (int unit = unit0 + col.part; unit < unit1; unit += col.parts) {
-      const int n0 = 64 * unit;
-      const int mine = n0 + 16 * p;  // the lane's 16 of out
-      u32x4 y[2] = {};
-      if (col.in && mine < a.N)
+    struct Unit {
+      u32x4 y[CT][2], f[KS][4];
+    };
+    auto load = [&](Unit& u, int unit) {
+      const int n0 = 64 * unit, mine = min(n0 + 16 * p, a.N - 16);  // the lane's 16 of out
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          y[j] = *reinterpret_cast<const u32x4*>(a.y + t * a.y_st + mine + 8 * j);
-      f32x4 o[4] = {};
+      for (int j = 0; j < CT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          u.y[j][i] = *reinterpret_cast<const u32x4*>(a.y + (t0 + col.token[j]) * a.y_st + mine + 8 * i);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const int r = 32 * s + 8 * p;
         if (32 * s >= rank) break;
-        u32x4 f[4];
+        const int r = 32 * s + 8 * p;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int64_t n = min(n0 + n_of + 4 * i, a.N - 1);
-          f[i] = r < rank ? *reinterpret_cast<const u32x4*>(w + n * a.R + r) : u32x4{};
+          u.f[s][i] = r < rank ? *reinterpret_cast<const u32x4*>(w + n * a.R + r) : u32x4{};
         }
+      }
+    };
+    int unit = unit0 + col.part;
+    if (unit >= unit1) return;
+    Unit now;
+    load(now, unit);
+
+    // the lane's eight of each 32 of h, scaled, and, after the power of 2 that takes the token's largest
+    // to 2^14 .. 2^15, their two parts
+    u32x4 hi[CT][KS], lo[CT][KS];
+    int up[CT];
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+      float h[KS][8];
+      float most = 0.0f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        f32x4 sum[2] = {};
+        const int r = 32 * s + 8 * p;
+        if (r < rank) {
+          const float* from = a.h + (t0 + col.token[j]) * (16 * RT) + r;
+          const int64_t apart = a.T * (16 * RT);
+          int q = 0;
+          for (; q + 4 <= slices; q += 4) {
+            f32x4 four[4][2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                four[k][i] = *reinterpret_cast<const f32x4*>(from + (q + k) * apart + 4 * i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) sum[i] += four[k][i];
+          }
+          for (; q < slices; ++q)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sum[i] += *reinterpret_cast<const f32x4*>(from + q * apart + 4 * i);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[s][e] = r + e < rank ? sum[e >> 2][e & 3] * by : 0.0f;
+          most = fmaxf(most, fabsf(h[s][e]));
+        }
+      }
+      most = column_max(most);
+      up[j] = 15 - __builtin_amdgcn_frexp_expf(most);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v0 = __builtin_amdgcn_ldexpf(h[s][2 * i], up[j]);
+          const float v1 = __builtin_amdgcn_ldexpf(h[s][2 * i + 1], up[j]);
+          const uint32_t b0 = E::bits(v0), b1 = E::bits(v1);
+          // (an infinite or NaN h is its first part alone)
+          const float r0 = v0 - E::value((uint16_t)b0), r1 = v1 - E::value((uint16_t)b1);
+          hi[j][s][i] = b0 | b1 << 16;
+          lo[j][s][i] = E::bits(fabsf(r0) < INFINITY ? r0 : 0.0f) |
+                        (uint32_t)E::bits(fabsf(r1) < INFINITY ? r1 : 0.0f) << 16;
+        }
+    }
+
+    for (;;) {
+      const int after = unit + col.parts;
+      Unit then;
+      if (after < unit1) load(then, after);
+      const int mine = 64 * unit + 16 * p;
+      f32x4 o[CT][4] = {};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        if (32 * s >= rank) break;
         if (32 * s + 32 > rank)  // what an adapter's rows hold past its rank does not matter
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t keep = (r + 2 * e < rank ? 0xFFFFu : 0u) | (r + 2 * e + 1 < rank ? 0xFFFF0000u : 0u);
+            const int r = 32 * s + 8 * p + 2 * e;
+            const uint32_t keep = (r < rank ? 0xFFFFu : 0u) | (r + 1 < rank ? 0xFFFF0000u : 0u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i][e] &= keep;
+            for (int i = 0; i < 4; ++i) now.f[s][i][e] &= keep;
           }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o[i] = E::mfma(f[i], hi[s], o[i]);
-          o[i] = E::mfma(f[i], lo[s], o[i]);
-        }
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < CT; ++j) {
+            o[j][i] = E::mfma(now.f[s][i], hi[j][s], o[j][i]);
+            o[j][i] = E::mfma(now.f[s][i], lo[j][s], o[j][i]);
+          }
       }
-      if (!col.in || mine >= a.N) continue;
-      u32x4 out[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < CT; ++j) {
+        if (!col.in[j] || mine >= a.N) continue;
+        u32x4 out[2];
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          const uint32_t was = y[i >> 1][2 * (i & 1) + k / 2];
-          const float v0 = E::value((uint16_t)(was & 0xFFFFu)) + __builtin_amdgcn_ldexpf(o[i][k], -up);
-          const float v1 = E::value((uint16_t)(was >> 16)) + __builtin_amdgcn_ldexpf(o[i][k + 1], -up);
-          out[i >> 1][2 * (i & 1) + k / 2] = E::bits(v0) | (uint32_t)E::bits(v1) << 16;
-        }
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<u32x4*>(a.out + t * a.out_st + mine + 8 * j) = out[j];
+          for (int k = 0; k < 4; k += 2) {
+            const uint32_t was = now.y[j][i >> 1][2 * (i & 1) + k / 2];
+            const float v0 = E::value((uint16_t)(was & 0xFFFFu)) + __builtin_amdgcn_ldexpf(o[j][i][k], -up[j]);
+            const float v1 = E::value((uint16_t)(was >> 16)) + __builtin_amdgcn_ldexpf(o[j][i][k + 1], -up[j]);
+            out[i >> 1][2 * (i & 1) + k / 2] = E::bits(v0) | (uint32_t)E::bits(v1) << 16;
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<u32x4*>(a.out + (t0 + col.token[j]) * a.out_st + mine + 8 * i) = out[i];
+      }
+      if (after >= unit1) break;
+      now = then;
+      unit = after;
     }
   });
 }
@@ -274,35 +354,51 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
 namespace {
 
 struct Layout {
-  int row_tiles, tiles, turns, slices, blocks;
+  int row_tiles, column_tiles, tiles, turns, slices, blocks;
+  bool join;
 };
 
 Layout layout_of(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   Layout p;
   const int64_t need = (R + 15) / 16;
   p.row_tiles = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : 16;
+  p.column_tiles = T > kTile && p.row_tiles <= 4 ? 2 : 1;
   p.tiles = (int)((T + kTile - 1) / kTile);
-  const int64_t target = 2 * device_cu_count();
-  // a workgroup an adapter in one tile of a decoding step, where many may occur
-  p.turns = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(T, kTile),
-                                                        8 * target / 16 / p.tiles));
-  const int64_t adapters = std::max<int64_t>(1, std::min<int64_t>(L, p.turns));
-  p.slices = (int)std::max<int64_t>(
-      1, std::min<int64_t>(std::min<int64_t>(K / 128, 16), target / (p.tiles * adapters)));
-  p.blocks = (int)std::max<int64_t>(
-      1, std::min<int64_t>((N + 255) / 256, 2 * target / (p.tiles * adapters)));
+  const int64_t cu = device_cu_count();
+  auto within = [](int64_t v, int64_t low, int64_t high) { return (int)std::max(low, std::min(v, high)); };
+  // Workgroups for each adapter of a decoding step's tile, where many may occur; prompts' tiles hold
+  // few, which one workgroup takes after the other.
+  p.turns = within(cu / p.tiles, 1, std::min<int64_t>(T, kTile));
+  const int64_t adapters = p.tiles == 1 ? within(L, 1, p.turns) : 1;  // at once
+  p.slices = within((p.tiles == 1 ? 1 : 2) * cu / (p.tiles * adapters), 1, std::min<int64_t>(K / 128, 16));
+  p.blocks = within(4 * cu / (p.tiles == 1 ? 1 : p.tiles), 1, (N + 255) / 256);
+  p.join = p.slices > 1 && p.tiles >= 8;
   return p;
+}
+
+template <class E, int RT, int CT>
+hipError_t launch(const LoraArgs& a, const Layout& p, hipStream_t stream) {
+  hipError_t e = launch_kernel(lora_shrink_kernel<E, RT, CT>,
+                               dim3((unsigned)(p.turns * p.slices), (unsigned)p.tiles),
+                               dim3(64 * kWaves), stream, a, p.turns, p.slices);
+  if (e != hipSuccess) return e;
+  if (p.join) {
+    const int64_t quads = a.T * (4 * RT);
+    e = launch_kernel(lora_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), stream, a.h,
+                      quads, p.slices);
+    if (e != hipSuccess) return e;
+  }
+  return launch_kernel(lora_expand_kernel<E, RT, CT>,
+                       dim3((unsigned)(p.turns * p.blocks), (unsigned)p.tiles), dim3(64 * kWaves),
+                       stream, a, p.turns, p.blocks, p.join ? 1 : p.slices);
 }
 
 template <class E, int RT>
 hipError_t launch(const LoraArgs& a, const Layout& p, hipStream_t stream) {
-  const hipError_t e =
-      launch_kernel(lora_shrink_kernel<E, RT>, dim3((unsigned)(p.turns * p.slices), (unsigned)p.tiles),
-                    dim3(64 * kWaves), stream, a, p.turns, p.slices);
-  if (e != hipSuccess) return e;
-  return launch_kernel(lora_expand_kernel<E, RT>,
-                       dim3((unsigned)(p.turns * p.blocks), (unsigned)p.tiles), dim3(64 * kWaves),
-                       stream, a, p.turns, p.blocks, p.slices);
+  if constexpr (RT <= 4) {
+    if (p.column_tiles == 2) return launch<E, RT, 2>(a, p, stream);
+  }
+  return launch<E, RT, 1>(a, p, stream);
 }
 
 template <class E>
