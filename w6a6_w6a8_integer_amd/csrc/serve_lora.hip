@@ -114,38 +114,66 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_kernel(const LoraArgs
 #pragma unroll
       for (int i = 0; i < RT; ++i)
         w[i] = a.a + ((int64_t)cur * a.R + min(16 * i + c, a.R - 1)) * a.K + at;
-      constexpr int kUnroll = RT * CT <= 2 ? 8 : RT * CT <= 8 ? 4 : 2;
-      int k = 0;
-      for (; k + 32 * kUnroll <= n; k += 32 * kUnroll) {
-        u32x4 xf[kUnroll][CT], wf[kUnroll][RT];
+      // The adapter's tiles, rounded up to a quarter of the most, as a constant: loads without branches
+      // between them can stay on their way while the chunk before is worked on.
+      auto run = [&](auto number) __attribute__((always_inline)) {
+        constexpr int NT = decltype(number)::value;
+        constexpr int U = CT + NT <= 3 ? 8 : CT == 1 && NT <= 4 ? 4 : NT <= 4 ? 2 : 1;  // steps of a chunk
+        struct Chunk {
+          u32x4 x[U][CT], w[U][NT];
+        };
+        auto load = [&](Chunk& f, int k) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-#pragma unroll
-          for (int j = 0; j < CT; ++j) xf[u][j] = *reinterpret_cast<const u32x4*>(x[j] + k + 32 * u);
-#pragma unroll
-          for (int i = 0; i < RT; ++i)
-            if (i < tiles) wf[u][i] = *reinterpret_cast<const u32x4*>(w[i] + k + 32 * u);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-          for (int i = 0; i < RT; ++i)
+          for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int j = 0; j < CT; ++j)
-              if (i < tiles) h[j][i] = E::mfma(wf[u][i], xf[u][j], h[j][i]);
-      }
-      for (; k < n; k += 32) {
-        u32x4 xf[CT];
+              f.x[u][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x[j] + k + 32 * u));
 #pragma unroll
-        for (int j = 0; j < CT; ++j) xf[j] = *reinterpret_cast<const u32x4*>(x[j] + k);
+            for (int i = 0; i < NT; ++i) f.w[u][i] = *reinterpret_cast<const u32x4*>(w[i] + k + 32 * u);
+          }
+        };
+        auto add = [&](const Chunk& f) {
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-          if (i < tiles) {
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int j = 0; j < CT; ++j) h[j][i] = E::mfma(f.w[u][i], f.x[u][j], h[j][i]);
+        };
+        int k = 0;
+        if (n >= 32 * U) {
+          Chunk now;
+          load(now, 0);
+          for (; k + 64 * U <= n; k += 32 * U) {
+            Chunk then;
+            load(then, k + 32 * U);
+            add(now);
+            now = then;
+          }
+          add(now);
+          k += 32 * U;
+        }
+        for (; k < n; k += 32) {
+          u32x4 xf[CT];
+#pragma unroll
+          for (int j = 0; j < CT; ++j) xf[j] = *reinterpret_cast<const u32x4*>(x[j] + k);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
             const u32x4 wf = *reinterpret_cast<const u32x4*>(w[i] + k);
 #pragma unroll
             for (int j = 0; j < CT; ++j) h[j][i] = E::mfma(wf, xf[j], h[j][i]);
           }
-      }
+        }
+      };
+      constexpr int Q = RT < 4 ? 1 : RT / 4;
+      if (tiles > 3 * Q && RT >= 4)
+        run(std::integral_constant<int, RT < 4 ? 1 : RT>{});
+      else if (tiles > 2 * Q && RT >= 4)
+        run(std::integral_constant<int, RT < 4 ? 1 : 3 * Q>{});
+      else if (tiles > Q && RT >= 2)
+        run(std::integral_constant<int, RT < 2 ? 1 : 2 * Q>{});
+      else if (tiles > 0)
+        run(std::integral_constant<int, Q>{});
     }
     if (col.parts > 1) {
       auto place = [&](int of, int j, int i) {
@@ -230,15 +258,15 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
       for (int j = 0; j < CT; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          u.y[j][i] = *reinterpret_cast<const u32x4*>(a.y + (t0 + col.token[j]) * a.y_st + mine + 8 * i);
+          u.y[j][i] = __builtin_nontemporal_load(
+              reinterpret_cast<const u32x4*>(a.y + (t0 + col.token[j]) * a.y_st + mine + 8 * i));
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        if (32 * s >= rank) break;
-        const int r = 32 * s + 8 * p;
+        const int r = 32 * s + 8 * p < rank ? 32 * s + 8 * p : 0;  // (past the rank: masked below)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int64_t n = min(n0 + n_of + 4 * i, a.N - 1);
-          u.f[s][i] = r < rank ? *reinterpret_cast<const u32x4*>(w + n * a.R + r) : u32x4{};
+          u.f[s][i] = *reinterpret_cast<const u32x4*>(w + n * a.R + r);
         }
       }
     };
@@ -302,10 +330,7 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
         }
     }
 
-    for (;;) {
-      const int after = unit + col.parts;
-      Unit then;
-      if (after < unit1) load(then, after);
+    auto finish = [&](Unit& now, int unit) __attribute__((always_inline)) {
       const int mine = 64 * unit + 16 * p;
       f32x4 o[CT][4] = {};
 #pragma unroll
@@ -342,12 +367,19 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
           }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<u32x4*>(a.out + (t0 + col.token[j]) * a.out_st + mine + 8 * i) = out[i];
+          __builtin_nontemporal_store(
+              out[i], reinterpret_cast<u32x4*>(a.out + (t0 + col.token[j]) * a.out_st + mine + 8 * i));
       }
-      if (after >= unit1) break;
+    };
+    // (no branch between a unit's loads and the next one's, so that the wait for the first leaves the
+    // second on their way)
+    for (; unit + col.parts < unit1; unit += col.parts) {
+      Unit then;
+      load(then, unit + col.parts);
+      finish(now, unit);
       now = then;
-      unit = after;
     }
+    finish(now, unit);
   });
 }
 
@@ -368,10 +400,10 @@ Layout layout_of(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   auto within = [](int64_t v, int64_t low, int64_t high) { return (int)std::max(low, std::min(v, high)); };
   // Workgroups for each adapter of a decoding step's tile, where many may occur; prompts' tiles hold
   // few, which one workgroup takes after the other.
-  p.turns = within(cu / p.tiles, 1, std::min<int64_t>(T, kTile));
+  p.turns = within(p.tiles == 1 ? T : cu / (4 * p.tiles), 1, std::min<int64_t>(T, kTile));
   const int64_t adapters = p.tiles == 1 ? within(L, 1, p.turns) : 1;  // at once
   p.slices = within((p.tiles == 1 ? 1 : 2) * cu / (p.tiles * adapters), 1, std::min<int64_t>(K / 128, 16));
-  p.blocks = within(4 * cu / (p.tiles == 1 ? 1 : p.tiles), 1, (N + 255) / 256);
+  p.blocks = within((p.tiles == 1 ? 4 : 2) * cu / p.tiles, 1, (N + 255) / 256);
   p.join = p.slices > 1 && p.tiles >= 8;
   return p;
 }
