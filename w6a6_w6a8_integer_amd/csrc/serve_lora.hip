@@ -67,6 +67,20 @@ __device__ __forceinline__ Columns<CT> columns_of(uint64_t members, int lane, in
   return c;
 }
 
+// Eight of h times 2^up as two parts each (an infinite or NaN one is its first part alone).
+template <class E>
+__device__ __forceinline__ void two_parts(const float (&h)[8], int up, u32x4& hi, u32x4& lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float v0 = __builtin_amdgcn_ldexpf(h[2 * i], up), v1 = __builtin_amdgcn_ldexpf(h[2 * i + 1], up);
+    const uint32_t b0 = E::bits(v0), b1 = E::bits(v1);
+    const float r0 = v0 - E::value((uint16_t)b0), r1 = v1 - E::value((uint16_t)b1);
+    hi[i] = b0 | b1 << 16;
+    lo[i] = E::bits(fabsf(r0) < INFINITY ? r0 : 0.0f) |
+            (uint32_t)E::bits(fabsf(r1) < INFINITY ? r1 : 0.0f) << 16;
+  }
+}
+
 // f(adapter, tokens that have it) for the adapters of the tile whose first token is turn modulo
 // turns.
 template <class F>
@@ -316,18 +330,7 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
       most = column_max(most);
       up[j] = 15 - __builtin_amdgcn_frexp_expf(most);
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v0 = __builtin_amdgcn_ldexpf(h[s][2 * i], up[j]);
-          const float v1 = __builtin_amdgcn_ldexpf(h[s][2 * i + 1], up[j]);
-          const uint32_t b0 = E::bits(v0), b1 = E::bits(v1);
-          // (an infinite or NaN h is its first part alone)
-          const float r0 = v0 - E::value((uint16_t)b0), r1 = v1 - E::value((uint16_t)b1);
-          hi[j][s][i] = b0 | b1 << 16;
-          lo[j][s][i] = E::bits(fabsf(r0) < INFINITY ? r0 : 0.0f) |
-                        (uint32_t)E::bits(fabsf(r1) < INFINITY ? r1 : 0.0f) << 16;
-        }
+      for (int s = 0; s < KS; ++s) two_parts<E>(h[s], up[j], hi[j][s], lo[j][s]);
     }
 
     auto finish = [&](Unit& now, int unit) __attribute__((always_inline)) {
@@ -383,11 +386,264 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
   });
 }
 
+// Prompts.  The kernels above take fragments straight from memory: 16 rows, a piece of 16 bytes of each in
+// neighbouring lanes, which the address units take one by one (64 cycles a load, the bound with 64
+// tokens of one adapter: 62 us of 95).  Here tiles of rows come into LDS in whole lines, four waves'
+// worth at once, and fragments from there; pieces change places by their row so that eight lanes'
+// reads meet different banks.
+
+// Sixteen-byte piece `piece` of row `row` in a tile whose rows are PR pieces: its place in the row.
+template <int PR>
+__device__ __forceinline__ int placed(int row, int piece) {
+  return piece ^ (PR >= 16 ? row & 15 : PR == 8 ? row & 7 : row >> 1 & 3);
+}
+
+// The tile's members of one adapter in order: member i's token (of the tile) in lane i.
+__device__ __forceinline__ int members_list(uint64_t members, int lane) {
+  const int n = __builtin_popcountll(members);
+  const bool mine = members >> lane & 1;
+  const int rank = __builtin_popcountll(members & ((1ull << lane) - 1));
+  return __builtin_amdgcn_ds_permute((mine ? rank : n + lane - rank) << 2, lane);
+}
+
+typedef __attribute__((address_space(1))) const void* global_ptr_t;
+
+// h of a tile and a slice of K, 128 deep stages of it in LDS, two of them.  A wave takes 32 tokens and half
+// of a stage's depth.
+template <class E, int RT>
+__global__ __launch_bounds__(64 * kWaves, 2) void lora_shrink_tiles_kernel(const LoraArgs a, int turns,
+                                                                           int slices) {
+  constexpr int kRows = kTile + 16 * RT, kStage = kRows * 256;  // x's rows, then the adapter's
+  constexpr int kLoads = kRows / 4 / kWaves;                    // four rows each
+  static_assert(kRows % (4 * kWaves) == 0, "whole loads");
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, p = lane >> 4;
+  const int slice = blockIdx.x % slices, turn = blockIdx.x / slices;
+  const int64_t t0 = (int64_t)blockIdx.y * kTile;
+  const int groups = a.K / 128;
+  const int g0 = (int)((int64_t)groups * slice / slices), g1 = (int)((int64_t)groups * (slice + 1) / slices);
+  const int id = adapter_of(a, t0, lane);
+  each_adapter(id, turn, turns, [&](int cur, uint64_t members) {
+    const int rank = a.ranks ? min(max(0, a.ranks[cur]), a.R) : a.R;
+    const int tiles = (rank + 15) / 16, n = __builtin_popcountll(members);
+    const int list = members_list(members, lane);
+    // the rows that this wave stages, four at a time: lane / 16 of them, piece lane % 16
+    const uint16_t* from[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = (wave * kLoads + i) * 4 + p, piece = placed<16>(row, c);
+      const int token = __builtin_amdgcn_ds_bpermute((row < n ? row : 0) << 2, list);
+      from[i] = (row < kTile ? a.x + (t0 + token) * a.x_st
+                             : a.a + ((int64_t)cur * a.R + min(row - kTile, a.R - 1)) * a.K) +
+                piece * 8;
+    }
+    auto stage = [&](int g) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        __builtin_amdgcn_global_load_lds(
+            (global_ptr_t)(from[i] + g * 128),
+            (lds_ptr_t)(lds + (g & 1) * kStage + (wave * kLoads + i) * 1024), 16, 0, 0);
+    };
+    f32x4 h[2][RT] = {};
+    const int first = wave >> 1 << 5, half = wave & 1;  // the wave's tokens, its half of a stage
+    stage(g0);
+    for (int g = g0; g < g1; ++g) {
+      wait_vm<0>();
+      lds_barrier();  // the stage has come, and the one before has been read
+      if (g + 1 < g1) stage(g + 1);
+      if (first >= n) continue;
+      const char* at = lds + (g & 1) * kStage;
+      auto fragment = [&](int row, int step) {
+        return *reinterpret_cast<const u32x4*>(at + row * 256 + placed<16>(row, half * 8 + step * 4 + p) * 16);
+      };
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        const u32x4 x0 = fragment(first + c, step), x1 = fragment(first + 16 + c, step);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const u32x4 w = fragment(kTile + 16 * i + c, step);
+          h[0][i] = E::mfma(w, x0, h[0][i]);
+          h[1][i] = E::mfma(w, x1, h[1][i]);
+        }
+      }
+    }
+    // the two halves of the depth
+    f32x4* sums = reinterpret_cast<f32x4*>(lds) + (wave >> 1) * (2 * RT * 64) + lane;
+    lds_barrier();
+    if (half == 1)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) sums[(j * RT + i) * 64] = h[j][i];
+    lds_barrier();
+    if (half == 0)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int column = first + 16 * j + c;
+        const int token = __builtin_amdgcn_ds_bpermute((column < n ? column : 0) << 2, list);
+        if (column >= n) continue;
+        float* to = a.h + ((int64_t)slice * a.T + t0 + token) * (16 * RT) + 4 * p;
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          if (i < tiles) *reinterpret_cast<f32x4*>(to + 16 * i) = h[j][i] + sums[(j * RT + i) * 64];
+      }
+    lds_barrier();  // the sums have been read
+  });
+}
+
+// out of a tile and a block of its columns, 128 at a time: B's rows in LDS, two such units of them.  A wave
+// takes 16 tokens, as the MFMAs' rows; column c of tile i is n = 8 c + i, so that a lane has eight
+// consecutive n of four tokens, and 16 lanes 256 bytes of each.  h's slices have been joined.
+template <class E, int RT>
+__global__ __launch_bounds__(64 * kWaves, 3) void lora_expand_tiles_kernel(const LoraArgs a, int turns,
+                                                                           int blocks) {
+  constexpr int KS = (RT + 1) / 2, PR = 4 * KS, kStage = 128 * PR * 16;
+  constexpr int kLoads = kStage / 1024 / kWaves;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, p = lane >> 4;
+  const int block = blockIdx.x % blocks, turn = blockIdx.x / blocks;
+  const int64_t t0 = (int64_t)blockIdx.y * kTile;
+  const int units = (a.N + 127) / 128;
+  const int unit0 = (int)((int64_t)units * block / blocks);
+  const int unit1 = (int)((int64_t)units * (block + 1) / blocks);
+  const int id = adapter_of(a, t0, lane);
+  if (turn == 0 && a.out != a.y) {  // tokens without an adapter
+    const int n0 = 128 * unit0, n1 = min(128 * unit1, a.N);
+    for (uint64_t left = __ballot(id < 0 && t0 + lane < a.T); left != 0; left &= left - 1) {
+      const int64_t t = t0 + __builtin_ctzll(left);
+      for (int n = n0 + 8 * (int)threadIdx.x; n < n1; n += 8 * 64 * kWaves)
+        *reinterpret_cast<u32x4*>(a.out + t * a.out_st + n) =
+            *reinterpret_cast<const u32x4*>(a.y + t * a.y_st + n);
+    }
+  }
+  if (unit0 >= unit1) return;
+  each_adapter(id, turn, turns, [&](int cur, uint64_t members) {
+    const int rank = a.ranks ? min(max(0, a.ranks[cur]), a.R) : a.R;
+    const float by = a.scales ? a.scales[cur] : 1.0f;
+    const int n_members = __builtin_popcountll(members);
+    const int list = members_list(members, lane);
+    const bool works = 16 * wave < n_members;
+    int token[4];  // of the lane's four rows; where there is none, the first
+    bool in[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = 16 * wave + 4 * p + k;
+      in[k] = row < n_members;
+      token[k] = __builtin_amdgcn_ds_bpermute((in[k] ? row : 0) << 2, list);
+    }
+    const uint16_t* w = a.b + (int64_t)cur * a.N * a.R;
+    auto stage = [&](int unit) {  // row 16 i + c of the stage is n = 8 c + i
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = (wave * kLoads + i) * 64 + lane, row = at / PR, piece = placed<PR>(row, at % PR);
+        const int64_t n = min(128 * unit + 8 * (row & 15) + (row >> 4), a.N - 1);
+        __builtin_amdgcn_global_load_lds((global_ptr_t)(w + n * a.R + (8 * piece < rank ? 8 * piece : 0)),
+                                         (lds_ptr_t)(lds + (unit & 1) * kStage + (wave * kLoads + i) * 1024),
+                                         16, 0, 0);
+      }
+    };
+    u32x4 y[4], then[4];
+    auto load = [&](u32x4 (&to)[4], int unit) {
+      const int n = min(128 * unit + 8 * c, a.N - 8);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        to[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.y + (t0 + token[k]) * a.y_st + n));
+    };
+    stage(unit0);
+    load(y, unit0);
+
+    // h of the lane's token c as the first factor: two parts each of its eight of every 32, and the power
+    // of 2 that is taken off again, of the tokens that the lane ends up with
+    u32x4 hi[KS], lo[KS];
+    int down[4];
+    {
+      const int column = 16 * wave + c;
+      const int mine = __builtin_amdgcn_ds_bpermute((column < n_members ? column : 0) << 2, list);
+      const float* from = a.h + (t0 + mine) * (16 * RT);
+      float h[KS][8];
+      float most = 0.0f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int r = 32 * s + 8 * p;
+        f32x4 part[2] = {};
+        if (r < rank) {
+          part[0] = *reinterpret_cast<const f32x4*>(from + r);
+          part[1] = *reinterpret_cast<const f32x4*>(from + r + 4);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[s][e] = r + e < rank ? part[e >> 2][e & 3] * by : 0.0f;
+          most = fmaxf(most, fabsf(h[s][e]));
+        }
+      }
+      const int up = 15 - __builtin_amdgcn_frexp_expf(column_max(most));
+#pragma unroll
+      for (int s = 0; s < KS; ++s) two_parts<E>(h[s], up, hi[s], lo[s]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) down[k] = -__builtin_amdgcn_ds_bpermute((4 * p + k) << 2, up);
+    }
+    wait_vm<0>();
+    lds_barrier();
+    for (int unit = unit0; unit < unit1; ++unit) {
+      const bool more = unit + 1 < unit1;
+      if (more) stage(unit + 1);
+      load(then, more ? unit + 1 : unit);
+      u32x4 out[4];
+      if (works) {
+        const char* at = lds + (unit & 1) * kStage;
+        f32x4 o[8] = {};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          if (32 * s >= rank) break;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 16 * i + c;
+            u32x4 f = *reinterpret_cast<const u32x4*>(at + (row * PR + placed<PR>(row, 4 * s + p)) * 16);
+            if (32 * s + 32 > rank)  // what an adapter's rows hold past its rank does not matter
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int r = 32 * s + 8 * p + 2 * e;
+                f[e] &= (r < rank ? 0xFFFFu : 0u) | (r + 1 < rank ? 0xFFFF0000u : 0u);
+              }
+            o[i] = E::mfma(hi[s], f, o[i]);
+            o[i] = E::mfma(lo[s], f, o[i]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const uint32_t was = y[k][i >> 1];
+            const float v0 = E::value((uint16_t)(was & 0xFFFFu)) + __builtin_amdgcn_ldexpf(o[i][k], down[k]);
+            const float v1 = E::value((uint16_t)(was >> 16)) + __builtin_amdgcn_ldexpf(o[i + 1][k], down[k]);
+            out[k][i >> 1] = E::bits(v0) | (uint32_t)E::bits(v1) << 16;
+          }
+      }
+      // (the next unit has come; the stores behind are waited for a unit later)
+      wait_vm<0>();
+      if (works) {
+        const int n = 128 * unit + 8 * c;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (in[k] && n < a.N)
+            __builtin_nontemporal_store(out[k], reinterpret_cast<u32x4*>(a.out + (t0 + token[k]) * a.out_st + n));
+      }
+      lds_barrier();  // this unit has been read, by every wave, and the next one is there
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = then[k];
+    }
+  });
+}
+
 namespace {
 
 struct Layout {
   int row_tiles, column_tiles, tiles, turns, slices, blocks;
-  bool join;
+  bool join, staged;
 };
 
 Layout layout_of(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
@@ -405,7 +661,28 @@ Layout layout_of(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   p.slices = within((p.tiles == 1 ? 1 : 2) * cu / (p.tiles * adapters), 1, std::min<int64_t>(K / 128, 16));
   p.blocks = within((p.tiles == 1 ? 4 : 2) * cu / p.tiles, 1, (N + 255) / 256);
   p.join = p.slices > 1 && p.tiles >= 8;
+  p.staged = p.tiles >= 8 && p.row_tiles <= 4;
+  if (p.staged) p.blocks = within(4 * cu / p.tiles, 1, (N + 127) / 128);
   return p;
+}
+
+hipError_t launch_slices_join(const LoraArgs& a, const Layout& p, hipStream_t stream) {
+  const int64_t quads = a.T * (4 * p.row_tiles);
+  return launch_kernel(lora_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), stream, a.h,
+                       quads, p.slices);
+}
+
+template <class E, int RT>
+hipError_t launch_tiles(const LoraArgs& a, const Layout& p, hipStream_t stream) {
+  hipError_t e = launch_kernel_lds(lora_shrink_tiles_kernel<E, RT>,
+                                   dim3((unsigned)(p.turns * p.slices), (unsigned)p.tiles),
+                                   dim3(64 * kWaves), 2 * (kTile + 16 * RT) * 256, stream, a, p.turns,
+                                   p.slices);
+  if (e == hipSuccess && p.join) e = launch_slices_join(a, p, stream);
+  if (e != hipSuccess) return e;
+  return launch_kernel_lds(lora_expand_tiles_kernel<E, RT>,
+                           dim3((unsigned)(p.turns * p.blocks), (unsigned)p.tiles), dim3(64 * kWaves),
+                           2 * 128 * 64 * ((RT + 1) / 2), stream, a, p.turns, p.blocks);
 }
 
 template <class E, int RT, int CT>
@@ -414,12 +691,8 @@ hipError_t launch(const LoraArgs& a, const Layout& p, hipStream_t stream) {
                                dim3((unsigned)(p.turns * p.slices), (unsigned)p.tiles),
                                dim3(64 * kWaves), stream, a, p.turns, p.slices);
   if (e != hipSuccess) return e;
-  if (p.join) {
-    const int64_t quads = a.T * (4 * RT);
-    e = launch_kernel(lora_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), stream, a.h,
-                      quads, p.slices);
-    if (e != hipSuccess) return e;
-  }
+  if (p.join) e = launch_slices_join(a, p, stream);
+  if (e != hipSuccess) return e;
   return launch_kernel(lora_expand_kernel<E, RT, CT>,
                        dim3((unsigned)(p.turns * p.blocks), (unsigned)p.tiles), dim3(64 * kWaves),
                        stream, a, p.turns, p.blocks, p.join ? 1 : p.slices);
@@ -428,6 +701,7 @@ hipError_t launch(const LoraArgs& a, const Layout& p, hipStream_t stream) {
 template <class E, int RT>
 hipError_t launch(const LoraArgs& a, const Layout& p, hipStream_t stream) {
   if constexpr (RT <= 4) {
+    if (p.staged) return launch_tiles<E, RT>(a, p, stream);
     if (p.column_tiles == 2) return launch<E, RT, 2>(a, p, stream);
   }
   return launch<E, RT, 1>(a, p, stream);
