@@ -100,6 +100,38 @@ def test_lora_add(fq, T, N, K, R, L, dtype):
     assert torch.equal(out, y)
 
 
+# several tiles of 64 tokens, whose rows come through LDS up to rank 64: blocks of 128 outputs that
+# end inside one, slices of K summed by the second product and (from eight tiles on) before it
+TILES = [(66, 128, 128, 8, 1), (100, 144, 384, 64, 3), (129, 272, 2176, 24, 6), (190, 1040, 512, 48, 2),
+         (321, 400, 640, 40, 70), (513, 16, 1152, 64, 5), (700, 272, 384, 32, 9), (1025, 528, 256, 16, 2)]
+
+
+@pytest.mark.parametrize("T,N,K,R,L", TILES)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_several_tiles(fq, T, N, K, R, L, dtype):
+    """Adapters mixed in every tile, then in runs; out apart, and in place the same."""
+    say("lora_add", T, N, K, R, L, dtype)
+    r = rng(48, T, N, K, R)
+    for ids in (r.integers(-1, L, T), np.sort(r.integers(-1, L, T))):
+        p = problem(r, T, N, K, R, L, dtype, ids)
+        y = p["y"].to(DEV)
+        out = call(fq, p, out=torch.full_like(y, NAN))
+        check(p, out)
+        p2 = {**p, "y": y}
+        assert call(fq, p2).data_ptr() == y.data_ptr() and torch.equal(out, y)
+
+
+@pytest.mark.parametrize("n", [1, 16, 17, 31, 32, 33, 48, 49, 63, 64])
+def test_tokens_of_one_adapter_in_several_tiles(fq, n):
+    """Every number of tokens that an adapter can have in a tile, others around them."""
+    r = rng(49, n)
+    ids = r.integers(1, 6, 200)
+    for t0 in (0, 64, 128):
+        ids[t0 + r.permutation(64)[:n]] = 0
+    p = problem(r, 200, 144, 512, 40, 6, BF16, ids)
+    check(p, call(fq, p))
+
+
 @pytest.mark.parametrize("n", [1, 15, 16, 17, 31, 32, 33, 48, 49, 64, 100])
 def test_tokens_of_one_adapter(fq, n):
     """Every number of columns that a tile can have, others between them."""

@@ -35,36 +35,55 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& a, int64_t t0, int lan
   return id >= 0 && id < a.L ? id : -1;
 }
 
-// The tokens of one adapter in the tile, as this wave sees them: its CT times 16 columns, if it has any,
-// and which part of the other axis it takes.
-template <int CT>
+// The tile's members of one adapter in order: member i's token (of the tile) in lane i.
+__device__ __forceinline__ int members_list(uint64_t members, int lane) {
+  const int n = __builtin_popcountll(members);
+  const bool mine = members >> lane & 1;
+  // (behind the members the other tokens follow: every lane has a place)
+  const int rank = __builtin_popcountll(members & ((1ull << lane) - 1));
+  return __builtin_amdgcn_ds_permute((mine ? rank : n + lane - rank) << 2, lane);
+}
+
+// The tokens of one adapter in the tile, as this wave sees them: its 16 columns, if it has any, and which
+// part of the other axis it takes.
 struct Columns {
-  int token[CT];    // of the lane's columns in the tile; where there is none, the first
-  bool in[CT];      // the column exists
+  int token;        // of the lane's column in the tile; where there is none, the first
+  bool in;          // the column exists
   int parts, part;  // waves that share the columns, and which of them this is
   bool idle;
 };
 
-template <int CT>
-__device__ __forceinline__ Columns<CT> columns_of(uint64_t members, int lane, int wave) {
+__device__ __forceinline__ Columns columns_of(uint64_t members, int lane, int wave) {
   const int n = __builtin_popcountll(members);
-  const bool mine = members >> lane & 1;
-  // lane i receives the i-th member (behind them the other tokens follow: every lane has a place)
-  const int rank = __builtin_popcountll(members & ((1ull << lane) - 1));
-  const int list = __builtin_amdgcn_ds_permute((mine ? rank : n + lane - rank) << 2, lane);
-  Columns<CT> c;
-  const int shift = n <= 16 * CT ? 2 : n <= 32 * CT ? 1 : 0;
+  const int list = members_list(members, lane);
+  Columns c;
+  const int shift = n <= 16 ? 2 : n <= 32 ? 1 : 0;
   c.parts = 1 << shift;
   c.part = wave & (c.parts - 1);
-  const int first = (wave >> shift) * (16 * CT);
-#pragma unroll
-  for (int i = 0; i < CT; ++i) {
-    const int column = first + 16 * i + (lane & 15);
-    c.in[i] = column < n;
-    c.token[i] = __builtin_amdgcn_ds_bpermute((c.in[i] ? column : 0) << 2, list);
-  }
+  const int first = (wave >> shift) * 16, column = first + (lane & 15);
+  c.in = column < n;
+  c.token = __builtin_amdgcn_ds_bpermute((c.in ? column : 0) << 2, list);
   c.idle = first >= n;
   return c;
+}
+
+// Eight consecutive fp32 of each of `slices` planes `apart` from one another, added in order.
+__device__ __forceinline__ void sum_slices(const float* from, int64_t apart, int slices, f32x4 (&sum)[2]) {
+  int q = 0;
+  for (; q + 4 <= slices; q += 4) {
+    f32x4 four[4][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) four[k][i] = *reinterpret_cast<const f32x4*>(from + (q + k) * apart + 4 * i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) sum[i] += four[k][i];
+  }
+  for (; q < slices; ++q)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sum[i] += *reinterpret_cast<const f32x4*>(from + q * apart + 4 * i);
 }
 
 // Eight of h times 2^up as two parts each (an infinite or NaN one is its first part alone).
@@ -81,17 +100,18 @@ __device__ __forceinline__ void two_parts(const float (&h)[8], int up, u32x4& hi
   }
 }
 
-// f(adapter, tokens that have it) for the adapters of the tile whose first token is turn modulo
-// turns.
+// f(adapter, tokens that have it) for the adapters of the tile, in the order of their first tokens, from
+// the turn-th on every turns-th.
 template <class F>
 __device__ __forceinline__ void each_adapter(int id, int turn, int turns, F&& f) {
-  const int lane = threadIdx.x & 63;
-  uint64_t left = __ballot(id >= 0 && lane % turns == turn);
-  while (left != 0) {
-    const int first = __builtin_ctzll(left);
-    const int cur = __builtin_amdgcn_readlane(id, first);
+  uint64_t left = __ballot(id >= 0);
+  for (int i = 0; left != 0; ++i) {
+    const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
     const uint64_t members = __ballot(id == cur);
-    if (__builtin_ctzll(members) == first) f(cur, members);
+    if (i == turn) {
+      f(cur, members);
+      turn += turns;
+    }
     left &= ~members;
   }
 }
@@ -100,10 +120,10 @@ __device__ __forceinline__ void each_adapter(int id, int turn, int turns, F&& f)
 
 // h: one workgroup = a tile's adapters (those of its turn) and a slice of K.  Waves that the columns
 // leave over share the slice and add up in LDS.  RT: 16-row tiles of an adapter at most.
-template <class E, int RT, int CT>
+template <class E, int RT>
 __global__ __launch_bounds__(64 * kWaves) void lora_shrink_kernel(const LoraArgs a, int turns,
                                                                  int slices) {
-  __shared__ __attribute__((aligned(16))) f32x4 sums[(kWaves - 1) * RT * CT * 64];
+  __shared__ __attribute__((aligned(16))) f32x4 sums[(kWaves - 1) * RT * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, p = lane >> 4;
@@ -117,13 +137,11 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_kernel(const LoraArgs
   each_adapter(id, turn, turns, [&](int cur, uint64_t members) {
     const int rank = a.ranks ? min(max(0, a.ranks[cur]), a.R) : a.R;
     const int tiles = (rank + 15) / 16;
-    const Columns<CT> col = columns_of<CT>(members, lane, wave);
-    f32x4 h[CT][RT] = {};
+    const Columns col = columns_of(members, lane, wave);
+    f32x4 h[RT] = {};
     if (!col.idle) {
       const int n = (k1 - k0) / col.parts, at = k0 + n * col.part + 8 * p;
-      const uint16_t* x[CT];
-#pragma unroll
-      for (int j = 0; j < CT; ++j) x[j] = a.x + (t0 + col.token[j]) * a.x_st + at;
+      const uint16_t* x = a.x + (t0 + col.token) * a.x_st + at;
       const uint16_t* w[RT];  // (rows past the adapter's last are read again, and not used)
 #pragma unroll
       for (int i = 0; i < RT; ++i)
@@ -132,16 +150,14 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_kernel(const LoraArgs
       // between them can stay on their way while the chunk before is worked on.
       auto run = [&](auto number) __attribute__((always_inline)) {
         constexpr int NT = decltype(number)::value;
-        constexpr int U = CT + NT <= 3 ? 8 : CT == 1 && NT <= 4 ? 4 : NT <= 4 ? 2 : 1;  // steps of a chunk
+        constexpr int U = NT <= 2 ? 8 : NT <= 4 ? 4 : 1;  // steps of a chunk
         struct Chunk {
-          u32x4 x[U][CT], w[U][NT];
+          u32x4 x[U], w[U][NT];
         };
         auto load = [&](Chunk& f, int k) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int j = 0; j < CT; ++j)
-              f.x[u][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x[j] + k + 32 * u));
+            f.x[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + k + 32 * u));
 #pragma unroll
             for (int i = 0; i < NT; ++i) f.w[u][i] = *reinterpret_cast<const u32x4*>(w[i] + k + 32 * u);
           }
@@ -150,9 +166,7 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_kernel(const LoraArgs
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-              for (int j = 0; j < CT; ++j) h[j][i] = E::mfma(f.w[u][i], f.x[u][j], h[j][i]);
+            for (int i = 0; i < NT; ++i) h[i] = E::mfma(f.w[u][i], f.x[u], h[i]);
         };
         int k = 0;
         if (n >= 32 * U) {
@@ -168,15 +182,10 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_kernel(const LoraArgs
           k += 32 * U;
         }
         for (; k < n; k += 32) {
-          u32x4 xf[CT];
+          const u32x4 xf = *reinterpret_cast<const u32x4*>(x + k);
 #pragma unroll
-          for (int j = 0; j < CT; ++j) xf[j] = *reinterpret_cast<const u32x4*>(x[j] + k);
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const u32x4 wf = *reinterpret_cast<const u32x4*>(w[i] + k);
-#pragma unroll
-            for (int j = 0; j < CT; ++j) h[j][i] = E::mfma(wf, xf[j], h[j][i]);
-          }
+          for (int i = 0; i < NT; ++i)
+            h[i] = E::mfma(*reinterpret_cast<const u32x4*>(w[i] + k), xf, h[i]);
         }
       };
       constexpr int Q = RT < 4 ? 1 : RT / 4;
@@ -190,31 +199,22 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_kernel(const LoraArgs
         run(std::integral_constant<int, Q>{});
     }
     if (col.parts > 1) {
-      auto place = [&](int of, int j, int i) {
-        return (((of - of / col.parts - 1) * CT + j) * RT + i) * 64 + lane;
-      };
+      auto place = [&](int of, int i) { return ((of - of / col.parts - 1) * RT + i) * 64 + lane; };
       __syncthreads();  // the sums of the adapter before have been read
       if (col.part > 0)
 #pragma unroll
-        for (int j = 0; j < CT; ++j)
-#pragma unroll
-          for (int i = 0; i < RT; ++i) sums[place(wave, j, i)] = h[j][i];
+        for (int i = 0; i < RT; ++i) sums[place(wave, i)] = h[i];
       __syncthreads();
       if (col.part > 0) return;
       for (int q = 1; q < col.parts; ++q)
 #pragma unroll
-        for (int j = 0; j < CT; ++j)
-#pragma unroll
-          for (int i = 0; i < RT; ++i) h[j][i] += sums[place(wave + q, j, i)];
+        for (int i = 0; i < RT; ++i) h[i] += sums[place(wave + q, i)];
     }
+    if (!col.in) return;
+    float* to = a.h + ((int64_t)slice * a.T + t0 + col.token) * (16 * RT) + 4 * p;
 #pragma unroll
-    for (int j = 0; j < CT; ++j) {
-      if (!col.in[j]) continue;
-      float* to = a.h + ((int64_t)slice * a.T + t0 + col.token[j]) * (16 * RT) + 4 * p;
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-        if (i < tiles) *reinterpret_cast<f32x4*>(to + 16 * i) = h[j][i];
-    }
+    for (int i = 0; i < RT; ++i)
+      if (i < tiles) *reinterpret_cast<f32x4*>(to + 16 * i) = h[i];
   });
 }
 
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(float* h, int64_t quads,
 // that the waves which share a token's take in turn, the next one's loads on their way while
 // one is worked on.  Row r of the MFMA's 16-row tile i is n = 16 (r / 4) + 4 i + r % 4 of the
 // unit, so that a lane ends up with 16 consecutive n of its tokens.
-template <class E, int RT, int CT>
+template <class E, int RT>
 __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs a, int turns,
                                                                  int blocks, int slices) {
   constexpr int KS = (RT + 1) / 2;  // 32-deep steps over the rank
@@ -259,21 +259,19 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
   each_adapter(id, turn, turns, [&](int cur, uint64_t members) {
     const int rank = a.ranks ? min(max(0, a.ranks[cur]), a.R) : a.R;
     const float by = a.scales ? a.scales[cur] : 1.0f;
-    const Columns<CT> col = columns_of<CT>(members, lane, wave);
+    const Columns col = columns_of(members, lane, wave);
     if (col.idle) return;
     const uint16_t* w = a.b + (int64_t)cur * a.N * a.R;
     const int n_of = 16 * (c >> 2) + (c & 3);
     struct Unit {
-      u32x4 y[CT][2], f[KS][4];
+      u32x4 y[2], f[KS][4];
     };
     auto load = [&](Unit& u, int unit) {
       const int n0 = 64 * unit, mine = min(n0 + 16 * p, a.N - 16);  // the lane's 16 of out
 #pragma unroll
-      for (int j = 0; j < CT; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          u.y[j][i] = __builtin_nontemporal_load(
-              reinterpret_cast<const u32x4*>(a.y + (t0 + col.token[j]) * a.y_st + mine + 8 * i));
+      for (int i = 0; i < 2; ++i)
+        u.y[i] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>(a.y + (t0 + col.token) * a.y_st + mine + 8 * i));
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const int r = 32 * s + 8 * p < rank ? 32 * s + 8 * p : 0;  // (past the rank: masked below)
@@ -291,51 +289,30 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
 
     // the lane's eight of each 32 of h, scaled, and, after the power of 2 that takes the token's largest
     // to 2^14 .. 2^15, their two parts
-    u32x4 hi[CT][KS], lo[CT][KS];
-    int up[CT];
-#pragma unroll
-    for (int j = 0; j < CT; ++j) {
+    u32x4 hi[KS], lo[KS];
+    int up;
+    {
       float h[KS][8];
       float most = 0.0f;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         f32x4 sum[2] = {};
         const int r = 32 * s + 8 * p;
-        if (r < rank) {
-          const float* from = a.h + (t0 + col.token[j]) * (16 * RT) + r;
-          const int64_t apart = a.T * (16 * RT);
-          int q = 0;
-          for (; q + 4 <= slices; q += 4) {
-            f32x4 four[4][2];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                four[k][i] = *reinterpret_cast<const f32x4*>(from + (q + k) * apart + 4 * i);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) sum[i] += four[k][i];
-          }
-          for (; q < slices; ++q)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) sum[i] += *reinterpret_cast<const f32x4*>(from + q * apart + 4 * i);
-        }
+        if (r < rank) sum_slices(a.h + (t0 + col.token) * (16 * RT) + r, a.T * (16 * RT), slices, sum);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           h[s][e] = r + e < rank ? sum[e >> 2][e & 3] * by : 0.0f;
           most = fmaxf(most, fabsf(h[s][e]));
         }
       }
-      most = column_max(most);
-      up[j] = 15 - __builtin_amdgcn_frexp_expf(most);
+      up = 15 - __builtin_amdgcn_frexp_expf(column_max(most));
 #pragma unroll
-      for (int s = 0; s < KS; ++s) two_parts<E>(h[s], up[j], hi[j][s], lo[j][s]);
+      for (int s = 0; s < KS; ++s) two_parts<E>(h[s], up, hi[s], lo[s]);
     }
 
     auto finish = [&](Unit& now, int unit) __attribute__((always_inline)) {
       const int mine = 64 * unit + 16 * p;
-      f32x4 o[CT][4] = {};
+      f32x4 o[4] = {};
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         if (32 * s >= rank) break;
@@ -348,31 +325,26 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
             for (int i = 0; i < 4; ++i) now.f[s][i][e] &= keep;
           }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < CT; ++j) {
-            o[j][i] = E::mfma(now.f[s][i], hi[j][s], o[j][i]);
-            o[j][i] = E::mfma(now.f[s][i], lo[j][s], o[j][i]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          o[i] = E::mfma(now.f[s][i], hi[s], o[i]);
+          o[i] = E::mfma(now.f[s][i], lo[s], o[i]);
+        }
       }
+      if (!col.in || mine >= a.N) return;
+      u32x4 out[2];
 #pragma unroll
-      for (int j = 0; j < CT; ++j) {
-        if (!col.in[j] || mine >= a.N) continue;
-        u32x4 out[2];
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int k = 0; k < 4; k += 2) {
+          const uint32_t was = now.y[i >> 1][2 * (i & 1) + k / 2];
+          const float v0 = E::value((uint16_t)(was & 0xFFFFu)) + __builtin_amdgcn_ldexpf(o[i][k], -up);
+          const float v1 = E::value((uint16_t)(was >> 16)) + __builtin_amdgcn_ldexpf(o[i][k + 1], -up);
+          out[i >> 1][2 * (i & 1) + k / 2] = E::bits(v0) | (uint32_t)E::bits(v1) << 16;
+        }
 #pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            const uint32_t was = now.y[j][i >> 1][2 * (i & 1) + k / 2];
-            const float v0 = E::value((uint16_t)(was & 0xFFFFu)) + __builtin_amdgcn_ldexpf(o[j][i][k], -up[j]);
-            const float v1 = E::value((uint16_t)(was >> 16)) + __builtin_amdgcn_ldexpf(o[j][i][k + 1], -up[j]);
-            out[i >> 1][2 * (i & 1) + k / 2] = E::bits(v0) | (uint32_t)E::bits(v1) << 16;
-          }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          __builtin_nontemporal_store(
-              out[i], reinterpret_cast<u32x4*>(a.out + (t0 + col.token[j]) * a.out_st + mine + 8 * i));
-      }
+      for (int i = 0; i < 2; ++i)
+        __builtin_nontemporal_store(
+            out[i], reinterpret_cast<u32x4*>(a.out + (t0 + col.token) * a.out_st + mine + 8 * i));
     };
     // (no branch between a unit's loads and the next one's, so that the wait for the first leaves the
     // second on their way)
@@ -398,14 +370,6 @@ __device__ __forceinline__ int placed(int row, int piece) {
   return piece ^ (PR >= 16 ? row & 15 : PR == 8 ? row & 7 : row >> 1 & 3);
 }
 
-// The tile's members of one adapter in order: member i's token (of the tile) in lane i.
-__device__ __forceinline__ int members_list(uint64_t members, int lane) {
-  const int n = __builtin_popcountll(members);
-  const bool mine = members >> lane & 1;
-  const int rank = __builtin_popcountll(members & ((1ull << lane) - 1));
-  return __builtin_amdgcn_ds_permute((mine ? rank : n + lane - rank) << 2, lane);
-}
-
 typedef __attribute__((address_space(1))) const void* global_ptr_t;
 
 // h of a tile and a slice of K, 128 deep stages of it in LDS, two of them.  A wave takes 32 tokens and half
@@ -429,32 +393,35 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_shrink_tiles_kernel(const
     const int rank = a.ranks ? min(max(0, a.ranks[cur]), a.R) : a.R;
     const int tiles = (rank + 15) / 16, n = __builtin_popcountll(members);
     const int list = members_list(members, lane);
-    // the rows that this wave stages, four at a time: lane / 16 of them, piece lane % 16
+    // the rows that this wave stages, four a load: lane / 16 of them, piece lane % 16
     const uint16_t* from[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int row = (wave * kLoads + i) * 4 + p, piece = placed<16>(row, c);
+      const int row = (i * kWaves + wave) * 4 + p, piece = placed<16>(row, c);
       const int token = __builtin_amdgcn_ds_bpermute((row < n ? row : 0) << 2, list);
       from[i] = (row < kTile ? a.x + (t0 + token) * a.x_st
                              : a.a + ((int64_t)cur * a.R + min(row - kTile, a.R - 1)) * a.K) +
                 piece * 8;
     }
-    auto stage = [&](int g) {
+    auto stage = [&](int g, int slot) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        __builtin_amdgcn_global_load_lds(
-            (global_ptr_t)(from[i] + g * 128),
-            (lds_ptr_t)(lds + (g & 1) * kStage + (wave * kLoads + i) * 1024), 16, 0, 0);
+      for (int i = 0; i < kLoads; ++i) {
+        const int row = (i * kWaves + wave) * 4;
+        if (row < kTile && row >= (n + 15) / 16 * 16) continue;  // (no token's)
+        __builtin_amdgcn_global_load_lds((global_ptr_t)(from[i] + g * 128),
+                                         (lds_ptr_t)(lds + slot * kStage + row * 256), 16, 0, 0);
+      }
     };
     f32x4 h[2][RT] = {};
     const int first = wave >> 1 << 5, half = wave & 1;  // the wave's tokens, its half of a stage
-    stage(g0);
+    if (g0 < g1) stage(g0, 0);
     for (int g = g0; g < g1; ++g) {
       wait_vm<0>();
       lds_barrier();  // the stage has come, and the one before has been read
-      if (g + 1 < g1) stage(g + 1);
+      const int slot = g - g0 & 1;
+      if (g + 1 < g1) stage(g + 1, slot ^ 1);
+      const char* at = lds + slot * kStage;
       if (first >= n) continue;
-      const char* at = lds + (g & 1) * kStage;
       auto fragment = [&](int row, int step) {
         return *reinterpret_cast<const u32x4*>(at + row * 256 + placed<16>(row, half * 8 + step * 4 + p) * 16);
       };
@@ -495,10 +462,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_shrink_tiles_kernel(const
 
 // out of a tile and a block of its columns, 128 at a time: B's rows in LDS, two such units of them.  A wave
 // takes 16 tokens, as the MFMAs' rows; column c of tile i is n = 8 c + i, so that a lane has eight
-// consecutive n of four tokens, and 16 lanes 256 bytes of each.  h's slices have been joined.
+// consecutive n of four tokens, and 16 lanes 256 bytes of each.
 template <class E, int RT>
 __global__ __launch_bounds__(64 * kWaves, 3) void lora_expand_tiles_kernel(const LoraArgs a, int turns,
-                                                                           int blocks) {
+                                                                           int blocks, int slices) {
   constexpr int KS = (RT + 1) / 2, PR = 4 * KS, kStage = 128 * PR * 16;
   constexpr int kLoads = kStage / 1024 / kWaves;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
@@ -569,14 +536,11 @@ __global__ __launch_bounds__(64 * kWaves, 3) void lora_expand_tiles_kernel(const
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const int r = 32 * s + 8 * p;
-        f32x4 part[2] = {};
-        if (r < rank) {
-          part[0] = *reinterpret_cast<const f32x4*>(from + r);
-          part[1] = *reinterpret_cast<const f32x4*>(from + r + 4);
-        }
+        f32x4 sum[2] = {};
+        if (r < rank && works) sum_slices(from + r, a.T * (16 * RT), slices, sum);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          h[s][e] = r + e < rank ? part[e >> 2][e & 3] * by : 0.0f;
+          h[s][e] = r + e < rank ? sum[e >> 2][e & 3] * by : 0.0f;
           most = fmaxf(most, fabsf(h[s][e]));
         }
       }
@@ -642,7 +606,7 @@ __global__ __launch_bounds__(64 * kWaves, 3) void lora_expand_tiles_kernel(const
 namespace {
 
 struct Layout {
-  int row_tiles, column_tiles, tiles, turns, slices, blocks;
+  int row_tiles, tiles, turns, slices, blocks;
   bool join, staged;
 };
 
@@ -650,19 +614,28 @@ Layout layout_of(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   Layout p;
   const int64_t need = (R + 15) / 16;
   p.row_tiles = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : 16;
-  p.column_tiles = T > kTile && p.row_tiles <= 4 ? 2 : 1;
   p.tiles = (int)((T + kTile - 1) / kTile);
   const int64_t cu = device_cu_count();
   auto within = [](int64_t v, int64_t low, int64_t high) { return (int)std::max(low, std::min(v, high)); };
-  // Workgroups for each adapter of a decoding step's tile, where many may occur; prompts' tiles hold
-  // few, which one workgroup takes after the other.
-  p.turns = within(p.tiles == 1 ? T : cu / (4 * p.tiles), 1, std::min<int64_t>(T, kTile));
-  const int64_t adapters = p.tiles == 1 ? within(L, 1, p.turns) : 1;  // at once
-  p.slices = within((p.tiles == 1 ? 1 : 2) * cu / (p.tiles * adapters), 1, std::min<int64_t>(K / 128, 16));
-  p.blocks = within((p.tiles == 1 ? 4 : 2) * cu / p.tiles, 1, (N + 255) / 256);
+  // Workgroups for each adapter of a decoding step's tile, where many may occur (as many as the pool has:
+  // 64 tokens over 40 adapters 28.6 us, with workgroups for 64 that 35.2); prompts' tiles hold few, which
+  // one workgroup takes after the other.
+  p.turns = within(p.tiles == 1 ? L : cu / (4 * p.tiles), 1, std::min<int64_t>(T, kTile));
+  const int64_t adapters = p.tiles == 1 ? p.turns : 1;  // at once
+  // Whole lines through LDS pay where a tile's tokens share an adapter: prompts 72 us against 95 straight
+  // from memory.  One tile is faster without (64 tokens over 40: 31.5 against 28.6; one
+  // token 10.1 against 8.7), and wider rows than 64 ranks do not leave LDS for two workgroups.
+  p.staged = p.tiles > 1 && p.row_tiles <= 4;
+  // Two workgroups a compute unit: prompts' h 22.0 us against 26.7 with one, 64 tokens over 40
+  // alike (28.6 and 28.8).  Of out's columns twice that for prompts, whose workgroups are unlike;
+  // decoding steps pay for each with another sum of h's slices (64 tokens: 17.7 us, twice as
+  // many 21.2, half 19.7).
+  p.slices = within(2 * cu / (p.tiles * adapters), 1, std::min<int64_t>(K / 128, 16));
+  p.blocks = p.staged ? within(4 * cu / p.tiles, 1, (N + 127) / 128)
+                      : within(2 * cu / (p.tiles * adapters), 1, (N + 255) / 256);
+  // Every block sums h's slices, or a launch before does once: prompts 72 us against 77.5, fewer tiles than
+  // eight without it (a launch is 3 us).
   p.join = p.slices > 1 && p.tiles >= 8;
-  p.staged = p.tiles >= 8 && p.row_tiles <= 4;
-  if (p.staged) p.blocks = within(4 * cu / p.tiles, 1, (N + 127) / 128);
   return p;
 }
 
@@ -682,29 +655,22 @@ hipError_t launch_tiles(const LoraArgs& a, const Layout& p, hipStream_t stream) 
   if (e != hipSuccess) return e;
   return launch_kernel_lds(lora_expand_tiles_kernel<E, RT>,
                            dim3((unsigned)(p.turns * p.blocks), (unsigned)p.tiles), dim3(64 * kWaves),
-                           2 * 128 * 64 * ((RT + 1) / 2), stream, a, p.turns, p.blocks);
-}
-
-template <class E, int RT, int CT>
-hipError_t launch(const LoraArgs& a, const Layout& p, hipStream_t stream) {
-  hipError_t e = launch_kernel(lora_shrink_kernel<E, RT, CT>,
-                               dim3((unsigned)(p.turns * p.slices), (unsigned)p.tiles),
-                               dim3(64 * kWaves), stream, a, p.turns, p.slices);
-  if (e != hipSuccess) return e;
-  if (p.join) e = launch_slices_join(a, p, stream);
-  if (e != hipSuccess) return e;
-  return launch_kernel(lora_expand_kernel<E, RT, CT>,
-                       dim3((unsigned)(p.turns * p.blocks), (unsigned)p.tiles), dim3(64 * kWaves),
-                       stream, a, p.turns, p.blocks, p.join ? 1 : p.slices);
+                           2 * 128 * 64 * ((RT + 1) / 2), stream, a, p.turns, p.blocks,
+                           p.join ? 1 : p.slices);
 }
 
 template <class E, int RT>
 hipError_t launch(const LoraArgs& a, const Layout& p, hipStream_t stream) {
-  if constexpr (RT <= 4) {
+  if constexpr (RT <= 4)
     if (p.staged) return launch_tiles<E, RT>(a, p, stream);
-    if (p.column_tiles == 2) return launch<E, RT, 2>(a, p, stream);
-  }
-  return launch<E, RT, 1>(a, p, stream);
+  hipError_t e = launch_kernel(lora_shrink_kernel<E, RT>,
+                               dim3((unsigned)(p.turns * p.slices), (unsigned)p.tiles),
+                               dim3(64 * kWaves), stream, a, p.turns, p.slices);
+  if (e == hipSuccess && p.join) e = launch_slices_join(a, p, stream);
+  if (e != hipSuccess) return e;
+  return launch_kernel(lora_expand_kernel<E, RT>,
+                       dim3((unsigned)(p.turns * p.blocks), (unsigned)p.tiles), dim3(64 * kWaves),
+                       stream, a, p.turns, p.blocks, p.join ? 1 : p.slices);
 }
 
 template <class E>
