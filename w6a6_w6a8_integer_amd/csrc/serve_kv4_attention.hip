@@ -197,6 +197,9 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
   constexpr int kRows = 16 / FOLD;  // of a group
   constexpr int kKeys = 8 / FOLD;   // whose scores a lane holds
   constexpr bool kTwoParts = std::is_same_v<E, Half>;
+  // Two groups of rows are often two waves that read the same keys: the second finds them in L2 (trees of
+  // seven on 24 contexts of 8k 70 us, passed by 72; one wave's keys passed by 52, kept 56).
+  constexpr int kKept = RG == 2 ? 0 : kNonTemporal;
   constexpr int kTiles = 2 * DT;  // of O, and quads of consecutive d that a lane ends up with
   extern __shared__ __attribute__((aligned(1024))) char lds[];
 
@@ -339,12 +342,12 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
           from = (i < D ? keys : values) + (j < D / 2 ? at0 : at1) + j % (D / 2) * 16;
         }
         __builtin_amdgcn_global_load_lds((global_ptr_t)from, (lds_ptr_t)(to + u * 1024), 16, 0,
-                                         kNonTemporal);
+                                         kKept);
       }
       const char* from = reinterpret_cast<const char*>(a.scales) +
                          (int64_t)max(lane < 32 ? b0 : b1, 0) * 128 + (lane & 31) * 4;
       __builtin_amdgcn_global_load_lds((global_ptr_t)from, (lds_ptr_t)(to + 32 * D), 4, 0,
-                                       kNonTemporal);
+                                       kKept);
       const int after = next(ahead);
       ahead = after;
       const int then = actual(min(after, end - 1));

@@ -67,23 +67,37 @@ __device__ __forceinline__ Columns columns_of(uint64_t members, int lane, int wa
   return c;
 }
 
-// Eight consecutive fp32 of each of `slices` planes `apart` from one another, added in order.
-__device__ __forceinline__ void sum_slices(const float* from, int64_t apart, int slices, f32x4 (&sum)[2]) {
-  int q = 0;
-  for (; q + 4 <= slices; q += 4) {
-    f32x4 four[4][2];
+// sum[k] += the eight fp32 at from + r[k] in each `step`-th of `slices` planes `apart` from one another,
+// from the `first` on and in order, a few of them on their way at once.
+template <int KS>
+__device__ __forceinline__ void sum_slices(const float* from, const int (&r)[KS], int64_t apart, int first,
+                                           int step, int slices, f32x4 (&sum)[KS][2]) {
+  constexpr int U = KS <= 2 ? 4 : 1;
+  int q = first;
+  for (; q + step < slices; q += U * step) {  // (two at least)
+    f32x4 v[U][KS][2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int u = 0; u < U; ++u) {
+      const float* at = from + min(q + u * step, slices - 1) * apart;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) four[k][i] = *reinterpret_cast<const f32x4*>(from + (q + k) * apart + 4 * i);
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+        for (int i = 0; i < 2; ++i) v[u][k][i] = *reinterpret_cast<const f32x4*>(at + r[k] + 4 * i);
+    }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) sum[i] += four[k][i];
+    for (int u = 0; u < U; ++u)
+      if (q + u * step < slices)
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) sum[k][i] += v[u][k][i];
   }
-  for (; q < slices; ++q)
+  if (q < slices)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) sum[i] += *reinterpret_cast<const f32x4*>(from + q * apart + 4 * i);
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        sum[k][i] += *reinterpret_cast<const f32x4*>(from + q * apart + r[k] + 4 * i);
 }
 
 // Eight of h times 2^up as two parts each (an infinite or NaN one is its first part alone).
@@ -238,6 +252,7 @@ template <class E, int RT>
 __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs a, int turns,
                                                                  int blocks, int slices) {
   constexpr int KS = (RT + 1) / 2;  // 32-deep steps over the rank
+  __shared__ __attribute__((aligned(16))) f32x4 sums[kWaves * KS * 2 * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, p = lane >> 4;
@@ -282,10 +297,34 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
         }
       }
     };
+    // h's slices: waves that share the tokens sum some each, and exchange
+    int at[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) at[s] = 32 * s + 8 * p < rank ? 32 * s + 8 * p : 0;
+    f32x4 sum[KS][2] = {};
+    sum_slices<KS>(a.h + (t0 + col.token) * (16 * RT), at, a.T * (16 * RT), col.part, col.parts, slices, sum);
     int unit = unit0 + col.part;
-    if (unit >= unit1) return;
+    const bool works = unit < unit1;
     Unit now;
-    load(now, unit);
+    if (works) load(now, unit);
+    if (col.parts > 1) {
+      f32x4* mine = sums + wave * (KS * 2 * 64) + lane;
+      lds_barrier();  // the sums of the adapter before have been read
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) mine[(2 * s + i) * 64] = sum[s][i];
+      lds_barrier();
+      const f32x4* all = sums + (wave - col.part) * (KS * 2 * 64) + lane;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          sum[s][i] = all[(2 * s + i) * 64];
+          for (int w = 1; w < col.parts; ++w) sum[s][i] += all[(w * KS * 2 + 2 * s + i) * 64];
+        }
+    }
+    if (!works) return;
 
     // the lane's eight of each 32 of h, scaled, and, after the power of 2 that takes the token's largest
     // to 2^14 .. 2^15, their two parts
@@ -296,12 +335,10 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
       float most = 0.0f;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        f32x4 sum[2] = {};
         const int r = 32 * s + 8 * p;
-        if (r < rank) sum_slices(a.h + (t0 + col.token) * (16 * RT) + r, a.T * (16 * RT), slices, sum);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          h[s][e] = r + e < rank ? sum[e >> 2][e & 3] * by : 0.0f;
+          h[s][e] = r + e < rank ? sum[s][e >> 2][e & 3] * by : 0.0f;
           most = fmaxf(most, fabsf(h[s][e]));
         }
       }
@@ -530,17 +567,19 @@ __global__ __launch_bounds__(64 * kWaves, 3) void lora_expand_tiles_kernel(const
     {
       const int column = 16 * wave + c;
       const int mine = __builtin_amdgcn_ds_bpermute((column < n_members ? column : 0) << 2, list);
-      const float* from = a.h + (t0 + mine) * (16 * RT);
+      int at[KS];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) at[s] = 32 * s + 8 * p < rank ? 32 * s + 8 * p : 0;
+      f32x4 sum[KS][2] = {};
+      if (works) sum_slices<KS>(a.h + (t0 + mine) * (16 * RT), at, a.T * (16 * RT), 0, 1, slices, sum);
       float h[KS][8];
       float most = 0.0f;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const int r = 32 * s + 8 * p;
-        f32x4 sum[2] = {};
-        if (r < rank && works) sum_slices(from + r, a.T * (16 * RT), slices, sum);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          h[s][e] = r + e < rank ? sum[e >> 2][e & 3] * by : 0.0f;
+          h[s][e] = r + e < rank ? sum[s][e >> 2][e & 3] * by : 0.0f;
           most = fmaxf(most, fabsf(h[s][e]));
         }
       }
@@ -627,12 +666,12 @@ Layout layout_of(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   // token 10.1 against 8.7), and wider rows than 64 ranks do not leave LDS for two workgroups.
   p.staged = p.tiles > 1 && p.row_tiles <= 4;
   // Two workgroups a compute unit: prompts' h 22.0 us against 26.7 with one, 64 tokens over 40
-  // alike (28.6 and 28.8).  Of out's columns twice that for prompts, whose workgroups are unlike;
-  // decoding steps pay for each with another sum of h's slices (64 tokens: 17.7 us, twice as
-  // many 21.2, half 19.7).
+  // alike (28.6 and 28.8).  Of out's columns four for prompts, whose workgroups are unlike, and three in
+  // decoding steps, which pay for each with another sum of h's slices (64 tokens: 15.5 us; four
+  // 17.3, two 16.3).
   p.slices = within(2 * cu / (p.tiles * adapters), 1, std::min<int64_t>(K / 128, 16));
   p.blocks = p.staged ? within(4 * cu / p.tiles, 1, (N + 127) / 128)
-                      : within(2 * cu / (p.tiles * adapters), 1, (N + 255) / 256);
+                      : within(3 * cu / (p.tiles * adapters), 1, (N + 255) / 256);
   // Every block sums h's slices, or a launch before does once: prompts 72 us against 77.5, fewer tiles than
   // eight without it (a launch is 3 us).
   p.join = p.slices > 1 && p.tiles >= 8;
