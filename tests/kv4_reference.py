@@ -6,10 +6,14 @@ may truncate); a sum of n products in any order errs by at most n u sum|products
 
 * attention: a score is s (q.(c - 8) + 8 Q) + b Q with Q = sum q.  The product and Q are sums
   of D terms, so the score errs by d = (D + 16) u scale S, S = sum|q| (s (|c - 8| + 8) + |b|); a
-  query below 2^-24 of the row's largest |q| errs by 2^-34 of that, in the product.  A probability
+  query below 2^-24 of the row's largest |q| errs by 2^-34 of that, in the product.  (Formed as
+  s (q.(64 + c) - 64 Q), D / 32 steps that each round a sum of at most (64 + 79) sum|q| err by
+  4.5 D u s sum|q|, less than the 8 D u s sum|q| that are in d.)  A probability
   errs by a factor 1 +- 2 d; the sums over the keys add (L / 32 + 64) u, and p s enters as two
   halves, within 2^-22 of itself or 2^-35 of the row's largest p s.  A value is
-  (p s) (c - 8) + p (b + 8 s), so all of that is relative to V = s |c - 8| + |b| + 8 s.
+  (p s) (c - 8) + p (b + 8 s), so all of that is relative to V = s |c - 8| + |b| + 8 s.  For
+  bfloat16 p s enters as one half, p s (1 + e) with |e| <= 2^-11, in (p s) (c - 8) and in 8 (p s)
+  alike: together (p s) c e, so out errs by 2^-11 of the mean of s c besides.
 * adapters: h = A x errs by (K + 16) u sum|a||x|, and enters as two parts, within e = 2^-17
   (fp16: 2^-22) of itself or 2^-38 of the token's largest; B h by (2 R + 64) u sum|b||h|.
 * an output is rounded once: half a step (2^-11 fp16, 2^-8 bf16), subnormal ones half of the
@@ -98,7 +102,7 @@ def attended(ctx, n, mask, window, sinks):
     return seen
 
 
-def attention(q, key, value, seen, scale):
+def attention(q, key, value, seen, scale, dtype=torch.float16):
     """One request: q float64 [n][H][D]; key, value as read() gives them, for its tokens (NaN in
     places that are not attended does not matter); seen bool [n][L].  Returns (out, lse,
     tolerance of out without its rounding, of lse)."""
@@ -132,6 +136,8 @@ def attention(q, key, value, seen, scale):
             rel = 2 * d + 2.0 ** -22 + (L / 32 + 64) * U
             least = 2.0 ** -35 * (w * vs).max(1, keepdims=True) * 8 * L
             tol[t, g] = 2 * rel[:, None] * (w @ V) + least
+            if dtype == torch.bfloat16:
+                tol[t, g] += 2.0 ** -11 * (w @ (vc * vs[:, None]))
             tol_lse[t, g] = 2 * d + (L / 32 + 64) * U + 4 * U * np.abs(lse[t, g])
     return out, lse, tol, tol_lse
 

@@ -276,7 +276,8 @@ def check(p, out, lse, scale, window=0, sinks=0, skip=(), rms=True):
         slots = np.where(good, pages, 0) * p["page"] + pos % p["page"]
         key, value = ref.read(*arrays, slots, Hkv, D, p["page"])
         seen = ref.attended(ctx, n, p["masks"][b], window, sinks) & good
-        want, want_lse, tol, tol_lse = ref.attention(q[rows], key, value, seen, scale)
+        want, want_lse, tol, tol_lse = ref.attention(q[rows], key, value, seen, scale,
+                                                     p["dtype"])
         err = np.abs(out[rows] - want)
         tol = tol + eps * np.abs(want) * (1 + 2.0 ** -7) + least
         wrong += [(b, *i, float(err[tuple(i)]), float(tol[tuple(i)])) for i in np.argwhere(~(err <= tol))[:3]]

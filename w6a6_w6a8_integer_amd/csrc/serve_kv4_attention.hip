@@ -2,26 +2,36 @@
 // an optional sliding window whose first tokens stay visible.
 //
 // A key is k = b + s c with codes c = 0 .. 15 and a scale and an offset for its token and head, a
-// value likewise.  For a row with queries q, Q = sum q:
-//   q.k = s (q.(c - 8) + 8 Q) + b Q
-//   sum_j p_j v_j = sum_j (p_j s_j) (c_j - 8) + sum_j p_j (b_j + 8 s_j)
-// so both products are MFMAs on c - 8, which fp16 holds exactly, whatever the tensors' type, and the
-// scales meet scores and probabilities.  (c - 8 rather than c: sums of codes of one sign would
-// err with their size, not their result's.)  The queries enter as fp16 after a row's power of
-// two, whole down to 2^-24 of the row's largest and below within 2^-34 of it.
-// w_j = p_j s_j enters as the sum of two fp16 parts, within 2^-22 of itself or 2^-35 of the row's
-// largest, whichever is more.
+// value likewise.  For a row with queries q, Q = sum q, and w_j = p_j s_j, W = sum w_j:
+//   q.k = s (q.(64 + c) - 64 Q) + b Q
+//   sum_j p_j v_j = sum_j w_j (c_j - 8) + 8 W + sum_j p_j b_j
+// so both products are MFMAs on whole numbers that fp16 holds, whatever the tensors' type, and the
+// scales meet scores and probabilities.  A key's code enters as 64 + c (its bits under 64's exponent: one
+// and-or a pair) with -64 Q as what the MFMAs begin from; that errs by D / 32 roundings of at
+// most (64 + 79) sum|q|, less than sums of q.(c - 8) and 8 Q are allowed.  A value's enters as c - 8 (or
+// 16 (c - 8), of the next four bits), an and-or and an addition a pair: sums over a long context of
+// codes of one sign would err with their size, not with their result's.
 //
-// Codes to fp16, nine instructions for eight: an and-or puts the code's bits below an exponent
-// (1024 + c, or 1024 + 16 c of the next four bits), and one addition of a pair takes the rest
-// off, leaving c - 8 or 16 (c - 8).  The factor 16 goes into the queries or out of the sums.
+// In how many bits: scores, statistics and sums are fp32.  The queries enter as fp16 after a row's power of
+// two, whole down to 2^-24 of the row's largest and below within 2^-34 of it.  w_j enters as the sum of two
+// fp16 parts for fp16 rows, within 2^-22 of itself or 2^-35 of the row's largest, whichever is more; for
+// bfloat16 rows, whose own rounding is 2^-8, as one, within 2^-11 of itself (with two, trees of seven
+// over 8k 79.9 us against 72.5).  W sums the very parts that meet the codes, so that what a weight
+// errs by meets its value's s c alone.
 //
 // A wave stages its own 32-key steps in LDS straight from memory, S - 1 of them on their way while one
 // is worked on, and needs no barrier until a request's end.  Rows are
 // columns of the MFMAs (16 a group), so a lane owns one row's statistics, and the keys are
 // dealt to the score tiles' rows so that a lane's scores are those that its fragment of P takes:
 // row r of score tile t holds key 8 (r / 4) + 4 t + r % 4, lane l keys 8 (l / 16) .. + 7.  Waves
-// that the rows leave over take the steps in turn and add up in LDS.
+// that the rows leave over take the steps in turn and add up in LDS; columns that they leave over
+// hold the same rows again, each for a part of a step's keys, so that few rows do not pay for 16.
+//
+// What bounds it: two contexts of 128k, 64 heads on 8, 52 us (4.7 TB/s of the cache's bytes; its loads
+// alone 44, its arithmetic alone 42); a window of 4k on eight requests of 40 heads 38 (4.7; 38 and 34).  Many
+// short requests and trees of many rows wait for chains of latencies (a step's LDS reads, MFMAs, maximum,
+// exponentials) with two or three waves a SIMD: 32 single tokens over 4k 24 us (3.2 TB/s), trees of
+// seven over 8k 70 (vector units busy half of the time, MFMAs a sixth).
 #include <type_traits>
 
 #include "serve_plan.h"
@@ -676,6 +686,7 @@ struct Layout {
 Layout layout_of(int64_t max_new, int64_t H, int64_t Hkv, int64_t D) {
   Layout p;
   const int64_t rows = max_new * (H / Hkv);
+  // two groups of rows a wave share the conversion of the codes (256-wide heads have no registers for it)
   p.groups = rows <= 16 || D > 128 ? 1 : 2;
   p.fold = rows <= 4 ? 4 : rows <= 8 ? 2 : 1;
   const int64_t waves = (rows + 16 * p.groups - 1) / (16 * p.groups);  // that hold rows
