@@ -120,6 +120,38 @@ __device__ __forceinline__ void two_parts(const float (&h)[8], int up, u32x4& hi
   }
 }
 
+// out = y for the tile's tokens `rows` and columns n0 .. n1: a wave 16 tokens and 256 columns at a time, all
+// of them on their way together (one after the other, a tile without adapters took 20 us).
+__device__ __forceinline__ void copy_rows(const LoraArgs& a, int64_t t0, uint64_t rows, int n0, int n1, int lane,
+                                          int wave) {
+  const int count = __builtin_popcountll(rows), list = members_list(rows, lane);
+  if (16 * wave >= count) return;
+  int64_t token[4];
+  bool in[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = 16 * wave + 4 * u + (lane >> 4);
+    in[u] = i < count;
+    token[u] = t0 + __builtin_amdgcn_ds_bpermute((in[u] ? i : 0) << 2, list);
+  }
+  for (int n = n0 + 8 * (lane & 15); n < n1; n += 256) {
+    u32x4 v[2][4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        v[c][u] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>(a.y + token[u] * a.y_st + (n + 128 * c < n1 ? n + 128 * c : n)));
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (in[u] && n + 128 * c < n1)
+          __builtin_nontemporal_store(v[c][u],
+                                      reinterpret_cast<u32x4*>(a.out + token[u] * a.out_st + n + 128 * c));
+  }
+}
+
 // f(adapter, tokens that have it) for the adapters of the tile, in the order of their first tokens, from
 // the turn-th on every turns-th.
 template <class F>
@@ -269,13 +301,8 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
   const int unit1 = (int)((int64_t)units * (block + 1) / blocks);
   const int id = adapter_of(a, t0, lane);
   if (turn == 0 && a.out != a.y) {  // tokens without an adapter
-    const int n0 = 64 * unit0, n1 = min(64 * unit1, a.N);
-    for (uint64_t left = __ballot(id < 0 && t0 + lane < a.T); left != 0; left &= left - 1) {
-      const int64_t t = t0 + __builtin_ctzll(left);
-      for (int n = n0 + 8 * (int)threadIdx.x; n < n1; n += 8 * 64 * kWaves)
-        *reinterpret_cast<u32x4*>(a.out + t * a.out_st + n) =
-            *reinterpret_cast<const u32x4*>(a.y + t * a.y_st + n);
-    }
+    const uint64_t rows = __ballot(id < 0 && t0 + lane < a.T);
+    copy_rows(a, t0, rows, 64 * unit0, min(64 * unit1, a.N), lane, wave);
   }
   each_adapter(id, turn, turns, [&](int cur, uint64_t members) {
     const int rank = a.ranks ? min(max(0, a.ranks[cur]), a.R) : a.R;
@@ -522,13 +549,8 @@ __global__ __launch_bounds__(64 * kWaves, 3) void lora_expand_tiles_kernel(const
   const int unit1 = (int)((int64_t)units * (block + 1) / blocks);
   const int id = adapter_of(a, t0, lane);
   if (turn == 0 && a.out != a.y) {  // tokens without an adapter
-    const int n0 = 128 * unit0, n1 = min(128 * unit1, a.N);
-    for (uint64_t left = __ballot(id < 0 && t0 + lane < a.T); left != 0; left &= left - 1) {
-      const int64_t t = t0 + __builtin_ctzll(left);
-      for (int n = n0 + 8 * (int)threadIdx.x; n < n1; n += 8 * 64 * kWaves)
-        *reinterpret_cast<u32x4*>(a.out + t * a.out_st + n) =
-            *reinterpret_cast<const u32x4*>(a.y + t * a.y_st + n);
-    }
+    const uint64_t rows = __ballot(id < 0 && t0 + lane < a.T);
+    copy_rows(a, t0, rows, 128 * unit0, min(128 * unit1, a.N), lane, wave);
   }
   if (unit0 >= unit1) return;
   each_adapter(id, turn, turns, [&](int cur, uint64_t members) {
