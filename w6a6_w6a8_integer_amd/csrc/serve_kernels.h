@@ -36,6 +36,7 @@ struct AttentionArgs {
   // single token over 37 10.1 us, as then there is a join, against 8.2).
   static constexpr uint32_t kHead = 5, kMinShare = 8;
   static constexpr bool kWindowed = false;
+  __host__ __device__ static constexpr uint32_t least_share() { return kMinShare; }
   const uint16_t* q;
   int64_t q_st, q_sh;
   const uint16_t* kc;
@@ -62,7 +63,9 @@ hipError_t launch_tree_attention(const AttentionArgs& a, bool bf16, hipStream_t 
 struct Kv4AttentionArgs : AttentionArgs {
   // (steps of a quarter of the bytes: 32 single tokens over 4k 24.0 us, a window of 4k on eight requests
   // 38.0, trees of seven over 8k 69.7; with 5 and 8 as above 25.2, 38.9, 70.9, with 3 and 8 27.9, 39.3, 71.9)
-  static constexpr uint32_t kHead = 16, kMinShare = 16;
+  static constexpr uint32_t kHead = 16;
+  uint32_t key_waves;  // waves that take a share's steps in turn, four each at the least
+  __host__ __device__ uint32_t least_share() const { return 4 * key_waves; }
   static constexpr bool kWindowed = true;
   uint32_t group, group_inverse;  // H / Hkv, floor(2^32 / group) (less one for a group of one)
   const uint16_t* scales;

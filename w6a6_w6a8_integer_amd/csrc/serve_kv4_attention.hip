@@ -699,14 +699,15 @@ Layout layout_of(int64_t max_new, int64_t H, int64_t Hkv, int64_t D) {
 }
 
 template <class E, int DT>
-hipError_t launch_rows(const Kv4AttentionArgs& a, hipStream_t stream) {
+hipError_t launch_rows(Kv4AttentionArgs a, hipStream_t stream) {
   Layout p = layout_of(a.max_new, a.H, a.Hkv, a.D);
+  a.key_waves = (uint32_t)p.key_waves;
   // no more shares than the tables' room can fill (short contexts: one, and no join)
   int64_t room = (((int64_t)a.max_blocks << a.page_shift) + 31) / 32;
   if (a.window > 0)  // (rounded out to whole steps)
     room = std::min<int64_t>(room, ((int64_t)a.window + a.max_new + a.sinks) / 32 + 4);
   p.shares = (int)std::min<int64_t>(
-      p.shares, std::max<int64_t>(1, a.B * (a.kHead + room) / a.kMinShare));
+      p.shares, std::max<int64_t>(1, a.B * (a.kHead + room) / a.least_share()));
   const int64_t units = (int64_t)p.shares * a.Hkv;
   const dim3 grid = p.row_blocks == 1 ? dim3((unsigned)a.Hkv, (unsigned)p.shares)
                                       : dim3((unsigned)((units + 7) / 8 * 8 * p.row_blocks));

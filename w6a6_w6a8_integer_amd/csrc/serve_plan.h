@@ -143,7 +143,7 @@ __device__ __forceinline__ Plan make_plan(const A& a, uint32_t shares, uint32_t 
   const uint32_t inc = inclusive_sum(sum);
   const uint32_t total = __builtin_amdgcn_readlane(inc, 63);
   Plan plan;
-  plan.shares = min(shares, max(1u, total / A::kMinShare));
+  plan.shares = min(shares, max(1u, total / a.least_share()));
   plan.size = total / plan.shares;
   plan.longer = total - plan.size * plan.shares;
   b = a.B;
