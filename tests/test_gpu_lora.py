@@ -106,7 +106,12 @@ TILES = [(66, 128, 128, 8, 1), (100, 144, 384, 64, 3), (129, 272, 2176, 24, 6), 
          (321, 400, 640, 40, 70), (513, 16, 1152, 64, 5), (700, 272, 384, 32, 9), (1025, 528, 256, 16, 2)]
 
 
-@pytest.mark.parametrize("T,N,K,R,L", TILES)
+# rows of up to 128 ranks come through LDS as well, longer ones straight from memory
+WIDE = [(65, 16, 128, 72, 2), (150, 400, 640, 128, 3), (520, 272, 1280, 96, 12), (577, 144, 384, 104, 1),
+        (140, 208, 384, 136, 2), (600, 80, 256, 256, 3)]
+
+
+@pytest.mark.parametrize("T,N,K,R,L", TILES + WIDE)
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_several_tiles(fq, T, N, K, R, L, dtype):
     """Adapters mixed in every tile, then in runs; out apart, and in place the same."""
@@ -119,6 +124,25 @@ def test_several_tiles(fq, T, N, K, R, L, dtype):
         check(p, out)
         p2 = {**p, "y": y}
         assert call(fq, p2).data_ptr() == y.data_ptr() and torch.equal(out, y)
+
+
+@pytest.mark.parametrize("T,N,R,L", [(64, 4112, 16, 40), (64, 592, 200, 1), (1, 8208, 8, 1), (130, 16, 8, 2),
+                                     (4159, 6160, 8, 2)])
+def test_tokens_without_an_adapter(fq, T, N, R, L):
+    """Whole tiles of them and a few, over blocks of many columns: y bit for bit."""
+    r = rng(50, T, N, R)
+    for few in (False, True):
+        ids = np.full(T, -1)
+        if few:
+            ids[r.permutation(T)[:max(1, T // 9)]] = r.integers(L)
+        p = problem(r, T, N, 128, R, L, BF16, ids)
+        y = p["y"].to(DEV)
+        out = call(fq, p, out=torch.full_like(y, NAN))
+        none = torch.from_numpy(ids < 0).to(DEV)
+        assert torch.equal(out[none], y[none])
+        if few:
+            keep = np.nonzero(ids >= 0)[0][:40]
+            check({**p, "x": p["x"][keep], "y": p["y"][keep], "ids": ids[keep]}, out[keep])
 
 
 @pytest.mark.parametrize("n", [1, 16, 17, 31, 32, 33, 48, 49, 63, 64])

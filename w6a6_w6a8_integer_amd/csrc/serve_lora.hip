@@ -534,7 +534,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_shrink_tiles_kernel(const
 // takes 16 tokens, as the MFMAs' rows; column c of tile i is n = 8 c + i, so that a lane has eight
 // consecutive n of four tokens, and 16 lanes 256 bytes of each.
 template <class E, int RT>
-__global__ __launch_bounds__(64 * kWaves, 3) void lora_expand_tiles_kernel(const LoraArgs a, int turns,
+__global__ __launch_bounds__(64 * kWaves, RT > 4 ? 2 : 3) void lora_expand_tiles_kernel(const LoraArgs a, int turns,
                                                                            int blocks, int slices) {
   constexpr int KS = (RT + 1) / 2, PR = 4 * KS, kStage = 128 * PR * 16;
   constexpr int kLoads = kStage / 1024 / kWaves;
@@ -690,15 +690,15 @@ Layout layout_of(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   p.turns = within(p.tiles == 1 ? L : cu / (4 * p.tiles), 1, std::min<int64_t>(T, kTile));
   const int64_t adapters = p.tiles == 1 ? p.turns : 1;  // at once
   // Whole lines through LDS pay where a tile's tokens share an adapter: prompts 72 us against 95 straight
-  // from memory.  One tile is faster without (64 tokens over 40: 31.5 against 28.6; one
-  // token 10.1 against 8.7), and wider rows than 64 ranks do not leave LDS for two workgroups.
-  p.staged = p.tiles > 1 && p.row_tiles <= 4;
+  // from memory, with 128 ranks 95 against 194.  One tile is faster without (64 tokens over 40:
+  // 31.5 against 28.6; one token 10.1 against 8.7), and a stage of 256 ranks does not fit twice.
+  p.staged = p.tiles > 1 && p.row_tiles <= 8;
   // Two workgroups a compute unit: prompts' h 22.0 us against 26.7 with one, 64 tokens over 40
-  // alike (28.6 and 28.8).  Of out's columns four for prompts, whose workgroups are unlike, and three in
-  // decoding steps, which pay for each with another sum of h's slices (64 tokens: 15.5 us; four
-  // 17.3, two 16.3).
+  // alike (28.6 and 28.8).  Of out's columns as many as fit at once for prompts: four, two from 64 ranks on
+  // (1200 tokens of 128 ranks 25.8 us, four 30.9), and three in decoding steps, which pay for each with
+  // another sum of h's slices (64 tokens: 15.5 us; four 17.3, two 16.3).
   p.slices = within(2 * cu / (p.tiles * adapters), 1, std::min<int64_t>(K / 128, 16));
-  p.blocks = p.staged ? within(4 * cu / p.tiles, 1, (N + 127) / 128)
+  p.blocks = p.staged ? within((p.row_tiles > 4 ? 2 : 4) * cu / p.tiles, 1, (N + 127) / 128)
                       : within(3 * cu / (p.tiles * adapters), 1, (N + 255) / 256);
   // Every block sums h's slices, or a launch before does once: prompts 72 us against 77.5, fewer tiles than
   // eight without it (a launch is 3 us).
@@ -728,7 +728,7 @@ hipError_t launch_tiles(const LoraArgs& a, const Layout& p, hipStream_t stream) 
 
 template <class E, int RT>
 hipError_t launch(const LoraArgs& a, const Layout& p, hipStream_t stream) {
-  if constexpr (RT <= 4)
+  if constexpr (RT <= 8)
     if (p.staged) return launch_tiles<E, RT>(a, p, stream);
   hipError_t e = launch_kernel(lora_shrink_kernel<E, RT>,
                                dim3((unsigned)(p.turns * p.slices), (unsigned)p.tiles),
