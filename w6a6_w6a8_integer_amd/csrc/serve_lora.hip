@@ -687,7 +687,7 @@ Layout layout_of(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   // Workgroups for each adapter of a decoding step's tile, where many may occur (as many as the pool has:
   // 64 tokens over 40 adapters 28.6 us, with workgroups for 64 that 35.2); prompts' tiles hold few, which
   // one workgroup takes after the other.
-  p.turns = within(p.tiles == 1 ? L : cu / (4 * p.tiles), 1, std::min<int64_t>(T, kTile));
+  p.turns = within(p.tiles == 1 ? L : std::min(L, cu / (4 * p.tiles)), 1, std::min<int64_t>(T, kTile));
   const int64_t adapters = p.tiles == 1 ? p.turns : 1;  // at once
   // Whole lines through LDS pay where a tile's tokens share an adapter: prompts 72 us against 95 straight
   // from memory, with 128 ranks 95 against 194.  One tile is faster without (64 tokens over 40:
@@ -700,6 +700,12 @@ Layout layout_of(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   p.slices = within(2 * cu / (p.tiles * adapters), 1, std::min<int64_t>(K / 128, 16));
   p.blocks = p.staged ? within((p.row_tiles > 4 ? 2 : 4) * cu / p.tiles, 1, (N + 127) / 128)
                       : within(3 * cu / (p.tiles * adapters), 1, (N + 255) / 256);
+  // A few tiles may hold single tokens of many adapters as well as prompts: a quarter of both (200 tokens
+  // over 37 adapters 41 us, 63 with all; a prompt of 116 tokens 18.9 and 22.4).
+  if (p.staged && p.tiles < 8) {
+    p.slices = std::max(1, p.slices / 4);
+    p.blocks = std::max(1, p.blocks / 4);
+  }
   // Every block sums h's slices, or a launch before does once: prompts 72 us against 77.5, fewer tiles than
   // eight without it (a launch is 3 us).
   p.join = p.slices > 1 && p.tiles >= 8;
