@@ -2,7 +2,7 @@
 // cut into shares of equal work on the GPU, where a share keeps what others join, and the
 // kernel that joins it.  A is the kernel's argument struct (AttentionArgs or one that extends
 // it) with its tuning: A::kHead, what starting on a request costs in 32-key steps,
-// A::kMinShare, the least share of a workgroup, and A::kWindowed, whether keys between the
+// A::least_share(), the least share of a workgroup, and A::kWindowed, whether keys between the
 // first tokens and a sliding window are passed over.
 #pragma once
 #include <algorithm>
