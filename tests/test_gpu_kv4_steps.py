@@ -149,3 +149,35 @@ def test_prompts_and_steps(fq):
             assert torch.equal(a, b), i
     assert int(m.ctx.sum()) == sum(PROMPTS) + STEPS * B and int(twin.ctx.sum()) == int(m.ctx.sum())
     assert not bool(y.isnan().any()) and math.isfinite(float(got.float().abs().max()))
+
+
+def test_two_models_at_once(fq):
+    """Two streams with a model each, their steps interleaved and never waited for: what each
+    gives alone."""
+    r = np.random.default_rng(52)
+    x = [torch.from_numpy(r.standard_normal((sum(PROMPTS), HIDDEN)).astype(np.float32)).half().to(DEV)
+         for _ in range(2)]
+    rows, new, one = i32(np.repeat(IDS, PROMPTS)), i32(PROMPTS), i32([1] * len(IDS))
+    ids = [i32(IDS), i32([2, 2, -1, 0])]
+
+    def run(m, i, outs):
+        outs.append(m.step(x[i], new, rows, max(PROMPTS)))
+        for k in range(6):
+            outs.append(m.step(x[i][k:k + len(IDS)], one, ids[i], 1))
+
+    want = [[], []]
+    for i in range(2):
+        run(Model(fq, np.random.default_rng(60 + i)), i, want[i])
+    models = [Model(fq, np.random.default_rng(60 + i)) for i in range(2)]
+    torch.cuda.synchronize()
+    got, streams = [[], []], [torch.cuda.Stream() for _ in range(2)]
+    for k in range(7):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                m = models[i]
+                got[i].append(m.step(x[i], new, rows, max(PROMPTS)) if k == 0 else
+                              m.step(x[i][k - 1:k - 1 + len(IDS)], one, ids[i], 1))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(got[i], want[i])), i
+        assert len(got[i]) == len(want[i]) == 7
