@@ -14,9 +14,9 @@
 //
 // In how many bits: scores, statistics and sums are fp32.  The queries enter as fp16 after a row's power of
 // two, whole down to 2^-24 of the row's largest and below within 2^-34 of it.  w_j enters as the sum of two
-// fp16 parts for fp16 rows, within 2^-22 of itself or 2^-35 of the row's largest, whichever is more; for
-// bfloat16 rows, whose own rounding is 2^-8, as one, within 2^-11 of itself (with two, trees of seven
-// over 8k 79.9 us against 72.5).  W sums the very parts that meet the codes, so that what a weight
+// fp16 parts, within 2^-22 of itself or 2^-35 of the row's largest, whichever is more, for bfloat16 rows
+// too: values that cancel leave what a weight errs by alone in the output, where one part's 2^-11 is
+// no longer under the rounding's 2^-8.  W sums the very parts that meet the codes, so that what a weight
 // errs by meets its value's s c alone.
 //
 // A wave stages its own 32-key steps in LDS straight from memory, S - 1 of them on their way while one
@@ -206,7 +206,6 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
   constexpr int D = 32 * DT;
   constexpr int kRows = 16 / FOLD;  // of a group
   constexpr int kKeys = 8 / FOLD;   // whose scores a lane holds
-  constexpr bool kTwoParts = std::is_same_v<E, Half>;
   // Two groups of rows are often two waves that read the same keys: the second finds them in L2 (trees of
   // seven on 24 contexts of 8k 70 us, passed by 72; one wave's keys passed by 52, kept 56).
   constexpr int kKept = RG == 2 ? 0 : kNonTemporal;
@@ -541,17 +540,15 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
           uint32_t bits = __builtin_bit_cast(uint32_t, h);
           asm("" : "+v"(bits));  // the very bits that the product takes are what is left out of the rest
           hi[g][i] = bits;
-          if constexpr (kTwoParts) {
-            h = pair_of(bits);
+          h = pair_of(bits);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) rest[j] = (_Float16)fmaf(prob[j], step[j], -(float)h[j]);
-            lo[g][i] = __builtin_bit_cast(uint32_t, rest);
-          }
+          for (int j = 0; j < 2; ++j) rest[j] = (_Float16)fmaf(prob[j], step[j], -(float)h[j]);
+          lo[g][i] = __builtin_bit_cast(uint32_t, rest);
         }
         if constexpr (FOLD > 1) gather<FOLD>(hi[g]);
-        if constexpr (FOLD > 1 && kTwoParts) gather<FOLD>(lo[g]);
+        if constexpr (FOLD > 1) gather<FOLD>(lo[g]);
         W[g] = Half::mfma(ones, hi[g], W[g]);
-        if constexpr (kTwoParts) W[g] = Half::mfma(ones, lo[g], W[g]);
+        W[g] = Half::mfma(ones, lo[g], W[g]);
       }
       uint32_t vd[2 * DT];
 #pragma unroll
@@ -568,10 +565,8 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
         for (int g = 0; g < RG; ++g) {
           o[g][2 * i] = Half::mfma(even, hi[g], o[g][2 * i]);
           o[g][2 * i + 1] = Half::mfma(odd, hi[g], o[g][2 * i + 1]);
-          if constexpr (kTwoParts) {
-            o[g][2 * i] = Half::mfma(even, lo[g], o[g][2 * i]);
-            o[g][2 * i + 1] = Half::mfma(odd, lo[g], o[g][2 * i + 1]);
-          }
+          o[g][2 * i] = Half::mfma(even, lo[g], o[g][2 * i]);
+          o[g][2 * i + 1] = Half::mfma(odd, lo[g], o[g][2 * i + 1]);
         }
       }
     };
