@@ -709,6 +709,10 @@ Layout layout_of(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   // Every block sums h's slices, or a launch before does once: prompts 72 us against 77.5, fewer tiles than
   // eight without it (a launch is 3 us).
   p.join = p.slices > 1 && p.tiles >= 8;
+  if (L == 0) {  // no adapter is loaded: there is no h and no workspace for one, and out is y
+    p.turns = p.slices = 1;
+    p.join = false;
+  }
   return p;
 }
 
@@ -720,10 +724,11 @@ hipError_t launch_slices_join(const LoraArgs& a, const Layout& p, hipStream_t st
 
 template <class E, int RT>
 hipError_t launch_tiles(const LoraArgs& a, const Layout& p, hipStream_t stream) {
-  hipError_t e = launch_kernel_lds(lora_shrink_tiles_kernel<E, RT>,
-                                   dim3((unsigned)(p.turns * p.slices), (unsigned)p.tiles),
-                                   dim3(64 * kWaves), 2 * (kTile + 16 * RT) * 256, stream, a, p.turns,
-                                   p.slices);
+  hipError_t e = hipSuccess;
+  if (a.L > 0)
+    e = launch_kernel_lds(lora_shrink_tiles_kernel<E, RT>,
+                          dim3((unsigned)(p.turns * p.slices), (unsigned)p.tiles), dim3(64 * kWaves),
+                          2 * (kTile + 16 * RT) * 256, stream, a, p.turns, p.slices);
   if (e == hipSuccess && p.join) e = launch_slices_join(a, p, stream);
   if (e != hipSuccess) return e;
   return launch_kernel_lds(lora_expand_tiles_kernel<E, RT>,
@@ -736,9 +741,11 @@ template <class E, int RT>
 hipError_t launch(const LoraArgs& a, const Layout& p, hipStream_t stream) {
   if constexpr (RT <= 8)
     if (p.staged) return launch_tiles<E, RT>(a, p, stream);
-  hipError_t e = launch_kernel(lora_shrink_kernel<E, RT>,
-                               dim3((unsigned)(p.turns * p.slices), (unsigned)p.tiles),
-                               dim3(64 * kWaves), stream, a, p.turns, p.slices);
+  hipError_t e = hipSuccess;
+  if (a.L > 0)
+    e = launch_kernel(lora_shrink_kernel<E, RT>,
+                      dim3((unsigned)(p.turns * p.slices), (unsigned)p.tiles), dim3(64 * kWaves),
+                      stream, a, p.turns, p.slices);
   if (e == hipSuccess && p.join) e = launch_slices_join(a, p, stream);
   if (e != hipSuccess) return e;
   return launch_kernel(lora_expand_kernel<E, RT>,
@@ -765,6 +772,7 @@ size_t lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R, int64_t 
 }
 
 hipError_t launch_lora(const LoraArgs& a, bool bf16, hipStream_t stream) {
+  if (a.L == 0 && a.out == a.y) return hipSuccess;
   const Layout p = layout_of(a.T, a.N, a.K, a.R, a.L);
   return bf16 ? launch_rank<Bfloat>(a, p, stream) : launch_rank<Half>(a, p, stream);
 }
