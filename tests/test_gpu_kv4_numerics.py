@@ -57,3 +57,49 @@ def test_values_that_cancel(fq, ctx, new, H, Hkv, D, tree, dtype):
     p["cache"][2][..., 2, :], p["cache"][2][..., 3, :] = 1.0, -15.0
     out, lse = base.run(fq, p, max(new))
     check_two_parts(p, out, lse, D ** -0.5)
+
+
+def two_kinds(fq, r, n, H, Hkv, D, dtype, first, rest, drop):
+    """One request of n tokens whose keys are one number each, so that a score is scale * sum(q) times it:
+    0.37 for every seventh token from the first on, and less by `drop` powers of 2 for the others.
+    Their values' scales are 2^first and 2^rest, and all values are 0."""
+    p = base.problem(fq, r, [n - 1], [1], H, Hkv, D, 16, dtype, False)
+    scores = np.full(n, 0.37 - drop * np.log(2) / D ** 0.5)
+    steps = np.full(n, 2.0 ** rest)
+    scores[::7], steps[::7] = 0.37, 2.0 ** first
+    sc = base.flat(p["cache"])[2].copy().reshape(-1, Hkv, 1, 4, 16)
+    for i in range(n):
+        page = int(p["table"][0, i // 16])
+        sc[page, :, 0, :, i % 16] = 0.0, scores[i], steps[i], -15 * steps[i]
+    p["cache"][1].fill_(-1)
+    p["cache"][2].copy_(torch.from_numpy(sc))
+    near = 1 + 0.03 * r.random((1, H, 1))                 # (sums of q that differ from head to head)
+    p["q"].copy_(torch.from_numpy(np.broadcast_to(near, (1, H, D)).copy()).to(dtype))
+    return p
+
+
+# of every eight keys that a lane holds some take nearly all, with scales far below the others'
+@pytest.mark.parametrize("n,H,Hkv", [(2, 4, 1), (8, 8, 1), (9, 16, 1), (30, 32, 1), (50, 4, 4), (900, 4, 2)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_small_scales_of_the_keys_that_count(fq, n, H, Hkv, dtype):
+    """The scales of the values that count are 2^30 below those of the ones that do not, whose p s is still
+    the smaller: p s of the first keep their bits."""
+    p = two_kinds(fq, base.rng(63, n, H), n, H, Hkv, 64, dtype, -18, 12, 36)
+    out, lse = base.run(fq, p, 1)
+    check_two_parts(p, out, lse, 0.125)
+
+
+@pytest.mark.parametrize("n,H,Hkv", [(2, 4, 1), (9, 16, 1), (30, 32, 1), (900, 4, 2)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_rows_without_a_scale(fq, n, H, Hkv, dtype):
+    """Constant rows of values (scale 0) that take nearly all, others far below them with the largest
+    scales: neither probabilities nor sums leave their range."""
+    for drop in (40, 90):
+        p = two_kinds(fq, base.rng(64, n, H, drop), n, H, Hkv, 64, dtype, 0, 12, drop)
+        sc = p["cache"][2]
+        first = sc[:, :, :, 2] == 1.0
+        sc[:, :, :, 2][first] = 0.0
+        sc[:, :, :, 3][first] = 1.25
+        out, lse = base.run(fq, p, 1)
+        check_two_parts(p, out, lse, 0.125)
+        assert bool(((out.float() - 1.25).abs() < 0.01).all())

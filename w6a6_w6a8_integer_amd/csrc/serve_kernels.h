@@ -35,7 +35,7 @@ struct AttentionArgs {
   // (counting no start: 32 single tokens over 4k 57 us against 54; shares down to one step: a
   // single token over 37 10.1 us, as then there is a join, against 8.2).
   static constexpr uint32_t kHead = 5, kMinShare = 8;
-  static constexpr bool kWindowed = false;
+  static constexpr bool kWindowed = false, kScaledReference = false;
   __host__ __device__ static constexpr uint32_t least_share() { return kMinShare; }
   const uint16_t* q;
   int64_t q_st, q_sh;
@@ -66,7 +66,7 @@ struct Kv4AttentionArgs : AttentionArgs {
   static constexpr uint32_t kHead = 16;
   uint32_t key_waves;  // waves that take a share's steps in turn, four each at the least
   __host__ __device__ uint32_t least_share() const { return 4 * key_waves; }
-  static constexpr bool kWindowed = true;
+  static constexpr bool kWindowed = true, kScaledReference = true;
   uint32_t group, group_inverse;  // H / Hkv, floor(2^32 / group) (less one for a group of one)
   const uint16_t* scales;
   int32_t window, sinks;

@@ -48,6 +48,7 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 // A row's largest w is held as 2^(kTop - 1) to 2^(kTop + kLag): fp16 reaches no further up, and
 // down to 2^-24, so that small ones keep their bits.
 constexpr float kTop = 11.0f, kLag = 4.0f;
+constexpr uint16_t kMostBits = (15 + 11 + 4) << 10;  // 2^(kTop + kLag) in fp16
 
 // Workgroups a compute unit holds.
 constexpr int units_per_cu(int64_t D, int groups) { return groups == 1 && D <= 128 ? 3 : 2; }
@@ -495,24 +496,57 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
         }
       }
 
-      // A row's reference m is a whole number that its exponents with the values' scales
-      // exceed by kLag at most; raised where they would, it takes the sums down by a power of 2.
+      // A row's reference m is a whole number that no exponent of p s exceeds by more than kLag.  The
+      // probabilities are formed under the reference that the row has; where some p s passes 2^(kTop + kLag)
+      // (rare after a request's first step) it goes up to the largest exponent of p s, each key's own,
+      // the sums come down by a power of 2 and the probabilities are formed again.  A scale of 0
+      // counts as 2^-60, which keeps the sums of p and p b in fp32's range.
       u32x4 hi[RG], lo[RG];
 #pragma unroll
       for (int g = 0; g < RG; ++g) {
-        float top = raw[g][0];
+        float sum, offset;
+        auto form = [&]() __attribute__((always_inline)) {
+          // (over nothing every key's is infinite)
+          const float ref = m[g] == -INFINITY ? 3e38f : kTop - m[g];
+          sum = offset = 0.0f;
 #pragma unroll
-        for (int e = 1; e < kKeys; ++e) top = fmaxf(top, raw[g][e]);
-        // (scales are not negative: their bits are in their order)
+          for (int i = 0; i < kKeys / 2; ++i) {
+            float prob[2], step[2];
+            f16x2 h, rest;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              prob[j] = __builtin_amdgcn_exp2f(fmaf(raw[g][2 * i + j], by[g], ref));
+              step[j] = half_at(vs[g], 2 * i + j);
+              sum += prob[j];
+              offset = fmaf(prob[j], half_at(vb[g], 2 * i + j), offset);
+              h[j] = (_Float16)fmaf(prob[j], step[j], zero);
+            }
+            uint32_t bits = __builtin_bit_cast(uint32_t, h);
+            asm("" : "+v"(bits));  // the very bits that the product takes are what is left out of the rest
+            hi[g][i] = bits;
+            h = pair_of(bits);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) rest[j] = (_Float16)fmaf(prob[j], step[j], -(float)h[j]);
+            lo[g][i] = __builtin_bit_cast(uint32_t, rest);
+          }
+        };
+        form();
+        // (p s are not negative: their bits are in their order)
         u16x2 most = {0, 0};
 #pragma unroll
-        for (int i = 0; i < kKeys / 2; ++i)
-          most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, vs[g][i]));
-        const float scale = half_bits_to_float(most[0] > most[1] ? most[0] : most[1]);
-        top = fmaf(top, by[g], (float)__builtin_amdgcn_frexp_expf(scale));
-        if (__ballot(top > m[g] + kLag)) {  // rare after a request's first step
+        for (int i = 0; i < kKeys / 2; ++i) {
+          const uint32_t two = hi[g][i];
+          most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, two));
+        }
+        if (__ballot((most[0] > most[1] ? most[0] : most[1]) > kMostBits || sum > 0x1p80f)) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kKeys; ++e) {
+            const float s = half_at(vs[g], e);
+            top = fmaxf(top, fmaf(raw[g][e], by[g], s > 0.0f ? __builtin_amdgcn_logf(s) : -60.0f));
+          }
           top = fold_max<FOLD>(top);
-          top = fmaxf(m[g], ceilf(top));
+          top = top > m[g] + kLag ? ceilf(top) : m[g];  // (a row's own keys alone raise it)
           const float down = m[g] - (top == -INFINITY ? 0.0f : top);
           m[g] = top;
           l[g] = scaled(l[g], down);
@@ -523,28 +557,10 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
           for (int t = 0; t < kTiles; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[g][t][i] = scaled(o[g][t][i], down);
+          form();
         }
-        const float ref = m[g] == -INFINITY ? 0.0f : kTop - m[g];
-#pragma unroll
-        for (int i = 0; i < kKeys / 2; ++i) {
-          float prob[2], step[2];
-          f16x2 h, rest;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            prob[j] = __builtin_amdgcn_exp2f(fmaf(raw[g][2 * i + j], by[g], ref));
-            step[j] = half_at(vs[g], 2 * i + j);
-            l[g] += prob[j];
-            B[g] = fmaf(prob[j], half_at(vb[g], 2 * i + j), B[g]);
-            h[j] = (_Float16)fmaf(prob[j], step[j], zero);
-          }
-          uint32_t bits = __builtin_bit_cast(uint32_t, h);
-          asm("" : "+v"(bits));  // the very bits that the product takes are what is left out of the rest
-          hi[g][i] = bits;
-          h = pair_of(bits);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) rest[j] = (_Float16)fmaf(prob[j], step[j], -(float)h[j]);
-          lo[g][i] = __builtin_bit_cast(uint32_t, rest);
-        }
+        l[g] += sum;
+        B[g] += offset;
         if constexpr (FOLD > 1) gather<FOLD>(hi[g]);
         if constexpr (FOLD > 1) gather<FOLD>(lo[g]);
         W[g] = Half::mfma(ones, hi[g], W[g]);

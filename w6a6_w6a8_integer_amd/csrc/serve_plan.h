@@ -2,8 +2,9 @@
 // cut into shares of equal work on the GPU, where a share keeps what others join, and the
 // kernel that joins it.  A is the kernel's argument struct (AttentionArgs or one that extends
 // it) with its tuning: A::kHead, what starting on a request costs in 32-key steps,
-// A::least_share(), the least share of a workgroup, and A::kWindowed, whether keys between the
-// first tokens and a sliding window are passed over.
+// A::least_share(), the least share of a workgroup, A::kWindowed, whether keys between the
+// first tokens and a sliding window are passed over, and A::kScaledReference, whether a row's
+// reference follows its values' scales.
 #pragma once
 #include <algorithm>
 
@@ -191,18 +192,25 @@ __device__ __forceinline__ float scaled(float x, float n) {
   return __builtin_ldexpf(x, (int)fminf(fmaxf(n, -1e4f), 1e4f));
 }
 
-// Four elements of a row of out, and its lse.
-template <class E>
-__device__ __forceinline__ void write_row(const AttentionArgs& a, int64_t t, int h, int d4,
-                                          f32x4 acc, float ref, float total) {
+// Four elements of a row of out, and its lse.  With A::kScaledReference, where the reference
+// follows more than the row's scores, total's exponent goes to the whole ref first, so that lse is
+// rounded alike whatever the reference is.
+template <class E, class A>
+__device__ __forceinline__ void write_row(const A& a, int64_t t, int h, int d4, f32x4 acc, float ref,
+                                          float total) {
   const float by = total != 0.0f ? 1.0f / total : 0.0f;
   u32x2 v;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     v[k] = E::bits(acc[2 * k] * by) | (uint32_t)E::bits(acc[2 * k + 1] * by) << 16;
   *reinterpret_cast<u32x2*>(a.out + (t * a.H + h) * a.D + 4 * d4) = v;
-  if (a.lse && d4 == 0)
+  if (a.lse && d4 == 0) {
+    if constexpr (A::kScaledReference) {
+      ref += (float)__builtin_amdgcn_frexp_expf(total);
+      total = __builtin_amdgcn_frexp_mantf(total);
+    }
     a.lse[t * a.H + h] = total != 0.0f ? (ref + log2f(total)) * kLn2 : -INFINITY;
+  }
 }
 
 // Joins the parts of requests that several shares hold, in a fixed order: D / 4 threads (four
