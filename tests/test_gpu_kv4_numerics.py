@@ -103,3 +103,14 @@ def test_rows_without_a_scale(fq, n, H, Hkv, dtype):
         out, lse = base.run(fq, p, 1)
         check_two_parts(p, out, lse, 0.125)
         assert bool(((out.float() - 1.25).abs() < 0.01).all())
+
+
+@pytest.mark.parametrize("by,scale,dtype", [(2.0 ** -50, 1e-30, BF16), (2.0 ** -120, 0.125, BF16), (1.0, 1e-44, F16),
+                                            (1.0, 1e-44, BF16), (2.0 ** -20, -1e-42, F16)])
+def test_scores_that_vanish(fq, by, scale, dtype):
+    """A scale and queries whose product fp32 does not hold: every attended key counts alike, and masked
+    ones (the ends of steps, a tree's, those before a window) not at all."""
+    for tree, window in ((False, 0), (True, 0), (False, 33)):
+        p = base.problem(fq, base.rng(65, tree, window), [40, 133, 3], [2, 1, 4], 4, 2, 64, 16, dtype, tree, by=by)
+        out, lse = base.run(fq, p, 4, scale=scale, window=window or None, sinks=3)
+        base.check(p, out, lse, scale, window, 3 if window else 0, rms=False)

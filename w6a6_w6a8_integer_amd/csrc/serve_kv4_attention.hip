@@ -169,7 +169,9 @@ __device__ __forceinline__ float scaled_queries(u32x4 (&q)[DT], float scale) {
         q[i][e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(v0, v1));
       }
   }
-  return __builtin_amdgcn_ldexpf(scale != 0.0f ? fabsf(scale) * kLog2e : 1.0f, -up);
+  // (neither 0 nor infinite: a masked score's -inf and a score of 0 keep their products)
+  return fminf(fmaxf(__builtin_amdgcn_ldexpf(scale != 0.0f ? fabsf(scale) * kLog2e : 1.0f, -up), 0x1p-126f),
+               0x1.fffffep+127f);
 }
 
 // The pairs of the lanes that hold a row's other keys, behind the lane's own.  (Only the first 16 / FOLD
