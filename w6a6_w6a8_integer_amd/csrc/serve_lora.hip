@@ -17,6 +17,7 @@
 // h enters the second product as two 16-bit parts, after a power of two that takes a token's largest
 // to 2^14 .. 2^15: within 2^-17 of itself, for fp16 2^-22 or 2^-39 of the largest.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "serve_device.h"
@@ -28,6 +29,8 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kTile = 64;  // tokens, one a lane
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // over the lanes that hold one column
 __device__ __forceinline__ float column_max(float x) {
@@ -106,19 +109,59 @@ __device__ __forceinline__ void sum_slices(const float* from, const int (&r)[KS]
         sum[k][i] += *reinterpret_cast<const f32x4*>(from + q * apart + r[k] + 4 * i);
 }
 
+// The 16 bits of v = 2^n h.  An h that is not 0 is at least the type's least value (bfloat16's least normal
+// one) there: an infinite weight gives it an infinity.
+template <class E>
+__device__ __forceinline__ uint32_t first_part(float h, float v) {
+  constexpr bool kHalf = std::is_same_v<E, Half>;
+  const uint32_t b = E::bits(v);
+  return h != 0.0f && (b & (kHalf ? 0x7FFFu : 0x7F80u)) == 0 ? (b & 0x8000u) | (kHalf ? 1u : 0x80u) : b;
+}
+
 // Eight of h times 2^up as two parts each (an infinite or NaN one is its first part alone).
 template <class E>
 __device__ __forceinline__ void two_parts(const float (&h)[8], int up, u32x4& hi, u32x4& lo) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float v0 = __builtin_amdgcn_ldexpf(h[2 * i], up), v1 = __builtin_amdgcn_ldexpf(h[2 * i + 1], up);
-    const uint32_t b0 = E::bits(v0), b1 = E::bits(v1);
+    const uint32_t b0 = first_part<E>(h[2 * i], v0), b1 = first_part<E>(h[2 * i + 1], v1);
     const float r0 = v0 - E::value((uint16_t)b0), r1 = v1 - E::value((uint16_t)b1);
     hi[i] = b0 | b1 << 16;
     lo[i] = E::bits(fabsf(r0) < INFINITY ? r0 : 0.0f) |
             (uint32_t)E::bits(fabsf(r1) < INFINITY ? r1 : 0.0f) << 16;
   }
 }
+
+// An infinite weight times two parts, of which the second may be 0 or of the other sign, is NaN where the
+// first part alone gives the infinity: where a wave meets weights that are not finite, the second parts
+// meet zeros in their place.  0 times every weight, summed, tells.
+template <class E>
+struct Finite {
+  f16x2 halves = {0, 0};
+  float sum = 0.0f;
+  __device__ __forceinline__ void add(u32x4 f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t two = f[e];
+      if constexpr (std::is_same_v<E, Half>)
+        halves = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, two), f16x2{0, 0}, halves);
+      else
+        sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, two), bf16x2{0, 0}, sum, false);
+    }
+  }
+  __device__ __forceinline__ bool all() const {  // of the wave's
+    const bool odd = std::is_same_v<E, Half> ? (__builtin_bit_cast(uint32_t, halves) & 0x7FFF7FFFu) != 0
+                                             : !(sum == 0.0f);
+    return __ballot(odd) == 0;
+  }
+  static __device__ __forceinline__ u32x4 kept(u32x4 f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      f[e] &= ((f[e] & E::kExponent) == E::kExponent ? 0xFFFF0000u : ~0u) &
+              ((f[e] >> 16 & E::kExponent) == E::kExponent ? 0xFFFFu : ~0u);
+    return f;
+  }
+};
 
 // out = y for the tile's tokens `rows` and columns n0 .. n1: a wave 16 tokens and 256 columns at a time, all
 // of them on their way together (one after the other, a tile without adapters took 20 us).
@@ -287,7 +330,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(float* h, int64_t quads,
 // one is worked on.  Row r of the MFMA's 16-row tile i is n = 16 (r / 4) + 4 i + r % 4 of the
 // unit, so that a lane ends up with 16 consecutive n of its tokens.
 template <class E, int RT>
-__global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs a, int turns,
+__global__ __launch_bounds__(64 * kWaves, RT <= 4 ? 3 : 1) void lora_expand_kernel(const LoraArgs a, int turns,
                                                                  int blocks, int slices) {
   constexpr int KS = (RT + 1) / 2;  // 32-deep steps over the rank
   __shared__ __attribute__((aligned(16))) f32x4 sums[kWaves * KS * 2 * 64];
@@ -394,11 +437,16 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_kernel(const LoraArgs
 #pragma unroll
             for (int i = 0; i < 4; ++i) now.f[s][i][e] &= keep;
           }
+        Finite<E> weights;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o[i] = E::mfma(now.f[s][i], hi[s], o[i]);
-          o[i] = E::mfma(now.f[s][i], lo[s], o[i]);
-        }
+        for (int i = 0; i < 4; ++i) weights.add(now.f[s][i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = E::mfma(now.f[s][i], hi[s], o[i]);
+        if (!weights.all())
+#pragma unroll
+          for (int i = 0; i < 4; ++i) now.f[s][i] = Finite<E>::kept(now.f[s][i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = E::mfma(now.f[s][i], lo[s], o[i]);
       }
       if (!col.in || mine >= a.N) return;
       u32x4 out[2];
@@ -626,24 +674,35 @@ __global__ __launch_bounds__(64 * kWaves, RT > 4 ? 2 : 3) void lora_expand_tiles
       u32x4 out[4];
       if (works) {
         const char* at = lds + (unit & 1) * kStage;
-        f32x4 o[8] = {};
+        f32x4 o[8];
+        Finite<E> weights;
+        auto multiply = [&](auto finite) __attribute__((always_inline)) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          if (32 * s >= rank) break;
+          for (int i = 0; i < 8; ++i) o[i] = f32x4{};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = 16 * i + c;
-            u32x4 f = *reinterpret_cast<const u32x4*>(at + (row * PR + placed<PR>(row, 4 * s + p)) * 16);
-            if (32 * s + 32 > rank)  // what an adapter's rows hold past its rank does not matter
+          for (int s = 0; s < KS; ++s) {
+            if (32 * s >= rank) break;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int r = 32 * s + 8 * p + 2 * e;
-                f[e] &= (r < rank ? 0xFFFFu : 0u) | (r + 1 < rank ? 0xFFFF0000u : 0u);
-              }
-            o[i] = E::mfma(hi[s], f, o[i]);
-            o[i] = E::mfma(lo[s], f, o[i]);
+            for (int i = 0; i < 8; ++i) {
+              const int row = 16 * i + c;
+              u32x4 f = *reinterpret_cast<const u32x4*>(at + (row * PR + placed<PR>(row, 4 * s + p)) * 16);
+              if (32 * s + 32 > rank)  // what an adapter's rows hold past its rank does not matter
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int r = 32 * s + 8 * p + 2 * e;
+                  f[e] &= (r < rank ? 0xFFFFu : 0u) | (r + 1 < rank ? 0xFFFF0000u : 0u);
+                }
+              o[i] = E::mfma(hi[s], f, o[i]);
+              if constexpr (decltype(finite)::value)
+                weights.add(f);
+              else
+                f = Finite<E>::kept(f);
+              o[i] = E::mfma(lo[s], f, o[i]);
+            }
           }
-        }
+        };
+        multiply(std::true_type{});
+        if (!weights.all()) multiply(std::false_type{});
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
