@@ -94,3 +94,29 @@ def test_infinite_weights_meet_the_least_sums(fq, T):
     assert bool((out[:, 7] == float("inf")).all()) and bool((out[:, 9] == -float("inf")).all())
     rest = [n for n in range(N) if n not in (7, 9)]
     assert torch.equal(out[:, rest], clean[:, rest])
+
+
+@pytest.mark.parametrize("T,R", LAYOUTS)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_an_infinite_sum_beside_ordinary_ones(fq, T, R, dtype):
+    """A token whose h has an infinity among numbers of tens: its outputs are infinities of the sign that
+    the infinite one gives, whatever the others'."""
+    base.say("infinite h", T, R, dtype)
+    r = base.rng(68, T, R)
+    N, K = 144, 256
+    p = base.problem(r, T, N, K, R, 2, dtype, [1] * T, [R, R])
+    p["a"] *= 30
+    p["a"][1, 4, 9] = float("inf")
+    p["x"][:, 9] = 0
+    hit = torch.arange(T) % 3 == 0
+    p["x"][hit, 9] = 1.0
+    p["a"][1, 4, 10], p["x"][:, 10] = 1.0, 1.0
+    rest = {**p, "a": p["a"].clone()}
+    rest["a"][1, 4, 9] = 0
+    out, base_out = apart(fq, p), apart(fq, rest)
+    sign = torch.sign(p["b"][1, :, 4].double()) * float(p["scales"][1])
+    want = torch.where(sign == 0, float("nan"), sign * float("inf"))
+    got = out[hit].double()
+    assert torch.equal(got.nan_to_num(7.0), want.expand_as(got).nan_to_num(7.0))
+    assert bool(out[~hit].isnan().all())                   # (0 times infinity)
+    assert bool(base_out.isfinite().all())

@@ -38,6 +38,9 @@ __device__ __forceinline__ float column_max(float x) {
   return fmaxf(x, __shfl_xor(x, 32));
 }
 
+// |h|, and 0 for an infinite one: the largest that is not sets a token's power of two.
+__device__ __forceinline__ float finite_size(float h) { return fabsf(h) < INFINITY ? fabsf(h) : 0.0f; }
+
 // The adapter of token t0 + lane, -1 where it has none.
 __device__ __forceinline__ int adapter_of(const LoraArgs& a, int64_t t0, int lane) {
   const int id = t0 + lane < a.T ? a.adapters[t0 + lane] : -1;
@@ -415,7 +418,7 @@ __global__ __launch_bounds__(64 * kWaves, RT <= 4 ? 3 : 1) void lora_expand_kern
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           h[s][e] = r + e < rank ? sum[s][e >> 2][e & 3] * by : 0.0f;
-          most = fmaxf(most, fabsf(h[s][e]));
+          most = fmaxf(most, finite_size(h[s][e]));
         }
       }
       up = 15 - __builtin_amdgcn_frexp_expf(column_max(most));
@@ -656,7 +659,7 @@ __global__ __launch_bounds__(64 * kWaves, RT > 4 ? 2 : 3) void lora_expand_tiles
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           h[s][e] = r + e < rank ? sum[s][e >> 2][e & 3] * by : 0.0f;
-          most = fmaxf(most, fabsf(h[s][e]));
+          most = fmaxf(most, finite_size(h[s][e]));
         }
       }
       const int up = 15 - __builtin_amdgcn_frexp_expf(column_max(most));
