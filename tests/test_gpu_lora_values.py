@@ -120,3 +120,15 @@ def test_an_infinite_sum_beside_ordinary_ones(fq, T, R, dtype):
     assert torch.equal(got.nan_to_num(7.0), want.expand_as(got).nan_to_num(7.0))
     assert bool(out[~hit].isnan().all())                   # (0 times infinity)
     assert bool(base_out.isfinite().all())
+
+
+@pytest.mark.parametrize("T,R", LAYOUTS)
+def test_large_bfloat16_weights_and_small_sums(fq, T, R):
+    """Weights of B near bfloat16's largest and far below 1 whose products with h are ordinary numbers."""
+    base.say("large B", T, R)
+    r = base.rng(69, T, R)
+    for by in (2.0 ** 118, 2.0 ** -90):
+        p = base.problem(r, T, 144, 256, R, 3, BF16)
+        p["b"] *= by
+        p["a"] /= by
+        base.check(p, base.call(fq, p))

@@ -14,8 +14,8 @@
 // for 203 MB: x at 2.9 TB/s through LDS (20), h's slices joined (5), y and out at 3.3 with an
 // adapter's rows again for each tile (44).
 //
-// h enters the second product as two 16-bit parts, after a power of two that takes a token's largest
-// to 2^14 .. 2^15: within 2^-17 of itself, for fp16 2^-22 or 2^-39 of the largest.
+// h enters the second product as two 16-bit parts, for fp16 after a power of two that takes a token's
+// largest to 2^14 .. 2^15: within 2^-17 of itself, for fp16 2^-22 or 2^-39 of the largest.
 #include <algorithm>
 #include <type_traits>
 
@@ -40,6 +40,13 @@ __device__ __forceinline__ float column_max(float x) {
 
 // |h|, and 0 for an infinite one: the largest that is not sets a token's power of two.
 __device__ __forceinline__ float finite_size(float h) { return fabsf(h) < INFINITY ? fabsf(h) : 0.0f; }
+
+// The power of 2 that a token's sums enter the second product with: for fp16 it takes the largest to
+// 2^14 .. 2^15; bfloat16 holds them as they are, and weights near its largest would take more past fp32.
+template <class E>
+__device__ __forceinline__ int power_of(float most) {
+  return std::is_same_v<E, Half> ? 15 - __builtin_amdgcn_frexp_expf(most) : 0;
+}
 
 // The adapter of token t0 + lane, -1 where it has none.
 __device__ __forceinline__ int adapter_of(const LoraArgs& a, int64_t t0, int lane) {
@@ -405,8 +412,7 @@ __global__ __launch_bounds__(64 * kWaves, RT <= 4 ? 3 : 1) void lora_expand_kern
     }
     if (!works) return;
 
-    // the lane's eight of each 32 of h, scaled, and, after the power of 2 that takes the token's largest
-    // to 2^14 .. 2^15, their two parts
+    // the lane's eight of each 32 of h, scaled, and, after the token's power of 2, their two parts
     u32x4 hi[KS], lo[KS];
     int up;
     {
@@ -421,7 +427,7 @@ __global__ __launch_bounds__(64 * kWaves, RT <= 4 ? 3 : 1) void lora_expand_kern
           most = fmaxf(most, finite_size(h[s][e]));
         }
       }
-      up = 15 - __builtin_amdgcn_frexp_expf(column_max(most));
+      up = power_of<E>(column_max(most));
 #pragma unroll
       for (int s = 0; s < KS; ++s) two_parts<E>(h[s], up, hi[s], lo[s]);
     }
@@ -662,7 +668,7 @@ __global__ __launch_bounds__(64 * kWaves, RT > 4 ? 2 : 3) void lora_expand_tiles
           most = fmaxf(most, finite_size(h[s][e]));
         }
       }
-      const int up = 15 - __builtin_amdgcn_frexp_expf(column_max(most));
+      const int up = power_of<E>(column_max(most));
 #pragma unroll
       for (int s = 0; s < KS; ++s) two_parts<E>(h[s], up, hi[s], lo[s]);
 #pragma unroll
