@@ -55,3 +55,30 @@ def test_no_adapter_is_loaded(tmp_path):
         assert (in_place, apart) == (0, 1), (T, K, R, in_place, apart)
         assert loaded[0] == loaded[1] and loaded[0] in ((2,) if T < 449 else (2, 3)), (T, K, R, loaded)
     assert rows[4][5] == 3
+
+
+def test_tensors_that_require_grad_are_refused():
+    """There is no backward pass: what would lose a gradient without a word is refused, unless the
+    caller has said that none is wanted."""
+    import torch
+    import w6a6_w6a8_integer_amd as fq
+
+    def tensors():
+        return {"x": torch.zeros(3, 256, dtype=torch.float16), "y": torch.zeros(3, 48, dtype=torch.float16),
+                "adapters": torch.zeros(3, dtype=torch.int32),
+                "a": torch.zeros(2, 8, 256, dtype=torch.float16), "b": torch.zeros(2, 48, 8, dtype=torch.float16),
+                "scales": torch.ones(2), "out": torch.zeros(3, 48, dtype=torch.float16)}
+
+    for name in ("x", "y", "a", "b", "scales", "out"):
+        args = tensors()
+        args[name].requires_grad_()
+        with pytest.raises(ValueError, match=f"{name} requires grad"):
+            fq.lora_add(**args)
+        args = {k: v for k, v in args.items() if k in ("x", "y", "adapters", "a", "b", name)}
+        with pytest.raises(ValueError, match=f"{name} requires grad"):
+            fq.lora_add(**args)
+        for off in (torch.no_grad, torch.inference_mode):
+            with off(), pytest.raises(TypeError, match="CUDA"):       # the next refusal
+                fq.lora_add(**args)
+    with pytest.raises(TypeError, match="CUDA"):
+        fq.lora_add(**tensors())

@@ -10,6 +10,7 @@
 // ABI sees a pointer, and FlexqError for a status it returns.
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
@@ -129,6 +130,12 @@ int32_t half_type(const Tensor& t, const char* name) {
   if (t.scalar_type() == at::kBFloat16) return FLEXQ_BF16;
   refuse(PyExc_TypeError, name, " must be float16 or bfloat16, got ",
          dtype_text(t.scalar_type()));
+}
+
+// no tensor that autograd would ask for a gradient of
+void no_grad_check(const Tensor& t, const char* name) {
+  value_check(!t.defined() || !t.requires_grad() || !c10::GradMode::is_enabled(), name,
+              " requires grad, and there is no backward pass: call it under torch.no_grad()");
 }
 
 int64_t integer(PyObject* o, const char* name) {
@@ -569,22 +576,29 @@ PyObject* lora_add(PyObject* const* p) {
               ", which must be a multiple of 8 up to 256");
   exact(a, dtype, "a", {L, R, K});
   const Tensor& b = exact(tensor(p[4], "b"), dtype, "b", {L, N, R});
+  Tensor ranks, scales, out = y, ws;
+  if (given(p[5])) ranks = exact(tensor(p[5], "ranks"), at::kInt, "ranks", {L});
+  if (given(p[6])) scales = exact(tensor(p[6], "scales"), at::kFloat, "scales", {L});
+  if (given(p[7])) {
+    out = rows(tensor(p[7], "out"), dtype, "out", 2);
+    value_check(out.sizes() == y.sizes(), "out must have shape ", shape_text(y.sizes()), ", got ",
+                shape_text(out.sizes()));
+  }
+  no_grad_check(x, "x");
+  no_grad_check(y, "y");
+  no_grad_check(a, "a");
+  no_grad_check(b, "b");
+  no_grad_check(scales, "scales");
+  no_grad_check(out, "out");
   OneGpu gpu;
   gpu.add(x, "x");
   gpu.add(y, "y");
   gpu.add(adapters, "adapters");
   gpu.add(a, "a");
   gpu.add(b, "b");
-  Tensor ranks, scales, out = y, ws;
-  if (given(p[5])) gpu.add(ranks = exact(tensor(p[5], "ranks"), at::kInt, "ranks", {L}), "ranks");
-  if (given(p[6]))
-    gpu.add(scales = exact(tensor(p[6], "scales"), at::kFloat, "scales", {L}), "scales");
-  if (given(p[7])) {
-    out = rows(tensor(p[7], "out"), dtype, "out", 2);
-    value_check(out.sizes() == y.sizes(), "out must have shape ", shape_text(y.sizes()), ", got ",
-                shape_text(out.sizes()));
-    gpu.add(out, "out");
-  }
+  if (ranks.defined()) gpu.add(ranks, "ranks");
+  if (scales.defined()) gpu.add(scales, "scales");
+  gpu.add(out, "out");
   const int64_t need = (int64_t)library.lora_add_workspace_bytes(T, N, K, R, L);
   if (given(p[8]))
     ws = flat(tensor(p[8], "workspace"), at::kByte, "workspace", need);

@@ -287,5 +287,6 @@ def lora_add(x: torch.Tensor, y: torch.Tensor, adapters: torch.Tensor, a: torch.
     of x [T][K] with adapter i = adapters[t] (int32; none where that is outside [0, L)) adds
     scales[i] * b[i] (a[i] x[t]) to y[t] [N], a [L][R][K] and b [L][N][R] of which the first
     ranks[i] rows and columns count (all R where ranks is None).  x and y are fp16 or bf16 and may
-    be strided rows.  In place on y unless `out` is given; returns it."""
+    be strided rows.  In place on y unless `out` is given; returns it.  There is no backward
+    pass: with gradients enabled, tensors that require them are refused."""
     return (_calls or _native()).lora_add(x, y, adapters, a, b, ranks, scales, out, workspace)
