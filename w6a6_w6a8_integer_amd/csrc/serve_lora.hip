@@ -117,13 +117,12 @@ __device__ __forceinline__ void sum_slices(const float* from, const int (&r)[KS]
         sum[k][i] += *reinterpret_cast<const f32x4*>(from + q * apart + r[k] + 4 * i);
 }
 
-// The 16 bits of v = 2^n h.  An h that is not 0 is at least the type's least value (bfloat16's least normal
-// one) there: an infinite weight gives it an infinity.
+// The 16 bits of v = 2^n h.  An h that is not 0 is at least the type's least value there: an infinite
+// weight gives it an infinity.
 template <class E>
 __device__ __forceinline__ uint32_t first_part(float h, float v) {
-  constexpr bool kHalf = std::is_same_v<E, Half>;
   const uint32_t b = E::bits(v);
-  return h != 0.0f && (b & (kHalf ? 0x7FFFu : 0x7F80u)) == 0 ? (b & 0x8000u) | (kHalf ? 1u : 0x80u) : b;
+  return h != 0.0f && (b & 0x7FFFu) == 0 ? b | 1u : b;
 }
 
 // Eight of h times 2^up as two parts each (an infinite or NaN one is its first part alone).
