@@ -234,11 +234,12 @@ flexq_status flexq_kv4_cache_read(const uint32_t* k_codes, const uint32_t* v_cod
            drafted tokens those from there on too; a tree's bits hold whatever the window.
    sinks   with a window, the first `sinks` tokens of the request stay visible; without one it
            plays no part.
-   Keys that no token's window holds are not read.  Scores, statistics and sums are fp32; the
-   queries enter whole down to 2^-24 of a row's largest, and below within 2^-34 of it; probabilities
-   times the values' scales enter their product as two fp16 parts, within 2^-22 of themselves or 2^-35 of
-   the row's largest, whichever is more (a scale of 0 counting as 2^-60); out is rounded once.  What masked places, unused slots and
-   pages hold does not matter.  A row that attends a NaN key or value is NaN.
+   Keys before every window of the request's tokens (behind the sinks) are not read.  Scores,
+   statistics and sums are fp32; the queries enter whole down to 2^-24 of a row's largest, and
+   below within 2^-34 of it; probabilities times the values' scales enter their product as two
+   fp16 parts, within 2^-22 of themselves or 2^-35 of the row's largest, whichever is more (a scale
+   of 0 counting as 2^-60); out is rounded once.  What masked places, unused slots and pages hold
+   does not matter.  A row that attends a NaN key or value is NaN.
    All else (arguments, masks, rows that attend nothing, rows past cu_new[B], workspace, limits,
    errors) as flexq_tree_attention, with the workspace of the function below; INVALID_VALUE also
    for a negative window or negative sinks. */

@@ -62,7 +62,7 @@ hipError_t launch_tree_attention(const AttentionArgs& a, bool bf16, hipStream_t 
 // `window` of a token's positions are left out, but for the first `sinks` (window 0: none are).
 struct Kv4AttentionArgs : AttentionArgs {
   // (steps of a quarter of the bytes: 32 single tokens over 4k 24.0 us, a window of 4k on eight requests
-  // 38.0, trees of seven over 8k 69.7; with 5 and 8 as above 25.2, 38.9, 70.9, with 3 and 8 27.9, 39.3, 71.9)
+  // 38.7, trees of seven over 8k 80.0; with 5 and 8 as above 25.5, 39.8, 81.7, with 3 and 8 28.3, 40.7, 81.0)
   static constexpr uint32_t kHead = 16;
   uint32_t key_waves;  // waves that take a share's steps in turn, four each at the least
   __host__ __device__ uint32_t least_share() const { return 4 * key_waves; }

@@ -28,10 +28,11 @@
 // hold the same rows again, each for a part of a step's keys, so that few rows do not pay for 16.
 //
 // What bounds it: two contexts of 128k, 64 heads on 8, 52 us (4.7 TB/s of the cache's bytes; its loads
-// alone 44, its arithmetic alone 42); a window of 4k on eight requests of 40 heads 38 (4.7; 38 and 34).  Many
-// short requests and trees of many rows wait for chains of latencies (a step's LDS reads, MFMAs, maximum,
-// exponentials) with two or three waves a SIMD: 32 single tokens over 4k 24 us (3.2 TB/s), trees of
-// seven over 8k 70 (vector units busy half of the time, MFMAs a sixth).
+// alone 41, its arithmetic alone 42); a window of 4k on eight requests of 40 heads 39 (4.6; 33 and 35).  Many
+// short requests and trees of many rows wait for chains of latencies (a step's LDS reads, MFMAs, exponentials,
+// the look for what leaves fp16's range) with two or three waves a SIMD: 32 single tokens over 4k 24 us (3.2
+// TB/s; loads 18, arithmetic 22), trees of seven over 8k 80 (loads 36, arithmetic 79: vector units busy half of
+// the time, MFMAs a fifth).
 #include <type_traits>
 
 #include "serve_plan.h"
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(64 * kWaves, units_per_cu(32 * DT, RG)) void kv4_at
   constexpr int kRows = 16 / FOLD;  // of a group
   constexpr int kKeys = 8 / FOLD;   // whose scores a lane holds
   // Two groups of rows are often two waves that read the same keys: the second finds them in L2 (trees of
-  // seven on 24 contexts of 8k 70 us, passed by 72; one wave's keys passed by 52, kept 56).
+  // seven on 24 contexts of 8k 80 us, passed by 82; one wave's keys, two contexts of 128k, passed by 52, kept 55).
   constexpr int kKept = RG == 2 ? 0 : kNonTemporal;
   constexpr int kTiles = 2 * DT;  // of O, and quads of consecutive d that a lane ends up with
   extern __shared__ __attribute__((aligned(1024))) char lds[];

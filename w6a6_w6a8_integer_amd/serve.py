@@ -267,9 +267,10 @@ def kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor,
     """:func:`tree_attention` over the 4-bit cache (flexq_kv4_attention), q fp16 or bf16.
 
     With a window a token attends the last `window` positions, its own among them, and the
-    first `sinks` of its request; the keys between are not read.  In a tree the drafted
-    tokens that a token attends are the last of its window's positions, and are attended
-    whatever the window."""
+    first `sinks` of its request; keys between, before every window of the request's tokens, are
+    not read (a prompt that begins within its window reads its keys from the first on for
+    every block of rows).  In a tree the drafted tokens that a token attends are the last of its
+    window's positions, and are attended whatever the window."""
     return (_calls or _native()).kv4_attention(q, k_codes, v_codes, scales, block_table, ctx_lens,
                                                cu_new, tree_mask, scale, max_new, window, sinks,
                                                out, lse, return_lse, workspace)
