@@ -751,12 +751,14 @@ Layout layout_of(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   // from memory, with 128 ranks 95 against 194.  One tile is faster without (64 tokens over 40:
   // 31.5 against 28.6; one token 10.1 against 8.7), and a stage of 256 ranks does not fit twice.
   p.staged = p.tiles > 1 && p.row_tiles <= 8;
-  // Two workgroups a compute unit: prompts' h 22.0 us against 26.7 with one, 64 tokens over 40
-  // alike (28.6 and 28.8).  Of out's columns as many as fit at once for prompts: four, two from 64 ranks on
-  // (1200 tokens of 128 ranks 25.8 us, four 30.9), and three in decoding steps, which pay for each with
-  // another sum of h's slices (64 tokens: 15.5 us; four 17.3, two 16.3).
+  // h: workgroups for two a compute unit (prompts 22.0 us, for one 26.7; 64 tokens over 40 alike, 28.6 and
+  // 28.8).  With 72 to 128 ranks, whose stages take 96 KB, one is there at a time and the second follows: 1200
+  // tokens 15.9 us, for one 17.2, 3500 tokens alike.  Of out's columns for prompts as many as a compute unit
+  // holds: three (3500 tokens 44.1 us, for four 45.8), two above 64 ranks (1200 tokens of 128 ranks 25.8 us, for
+  // four 30.9); and three in decoding steps, which pay for each with another sum of h's slices (64 tokens:
+  // 15.5 us; four 17.3, two 16.3).
   p.slices = within(2 * cu / (p.tiles * adapters), 1, std::min<int64_t>(K / 128, 16));
-  p.blocks = p.staged ? within((p.row_tiles > 4 ? 2 : 4) * cu / p.tiles, 1, (N + 127) / 128)
+  p.blocks = p.staged ? within((p.row_tiles > 4 ? 2 : 3) * cu / p.tiles, 1, (N + 127) / 128)
                       : within(3 * cu / (p.tiles * adapters), 1, (N + 255) / 256);
   // A few tiles may hold single tokens of many adapters as well as prompts: a quarter of both (200 tokens
   // over 37 adapters 41 us, 63 with all; a prompt of 116 tokens 18.9 and 22.4).
