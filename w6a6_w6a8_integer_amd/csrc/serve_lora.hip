@@ -36,14 +36,27 @@ __device__ __forceinline__ float column_max(float x) {
   return fmaxf(x, __shfl_xor(x, 32));
 }
 
-// |h|, and 0 for an infinite one: the largest that is not sets a token's power of two.
-__device__ __forceinline__ float finite_size(float h) { return fabsf(h) < INFINITY ? fabsf(h) : 0.0f; }
-
-// The power of 2 that a token's sums enter the second product with: for fp16 it takes the largest to
-// 2^14 .. 2^15; bfloat16 holds them as they are, and weights near its largest would take more past fp32.
-template <class E>
-__device__ __forceinline__ int power_of(float most) {
-  return std::is_same_v<E, Half> ? 15 - __builtin_amdgcn_frexp_expf(most) : 0;
+// The power of 2 that a token's sums enter the second product with, h the lane's of the token (0 past its
+// rank): for fp16 it takes the largest that is finite to 2^14 .. 2^15; bfloat16 holds them as they are, and
+// weights near its largest would take more past fp32.
+template <class E, int KS>
+__device__ __forceinline__ int power_of(const float (&h)[KS][8]) {
+  if constexpr (!std::is_same_v<E, Half>) return 0;
+  float most = 0.0f;
+#pragma unroll
+  for (int s = 0; s < KS; ++s)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(h[s][e]));
+  most = column_max(most);
+  if (__builtin_expect(__ballot(most == INFINITY) != 0, 0)) {
+    most = 0.0f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(h[s][e]) < INFINITY ? fabsf(h[s][e]) : 0.0f);
+    most = column_max(most);
+  }
+  return 15 - __builtin_amdgcn_frexp_expf(most);
 }
 
 // The adapter of token t0 + lane, -1 where it has none.
@@ -117,32 +130,46 @@ __device__ __forceinline__ void sum_slices(const float* from, const int (&r)[KS]
         sum[k][i] += *reinterpret_cast<const f32x4*>(from + q * apart + r[k] + 4 * i);
 }
 
-// The 16 bits of v = 2^n h.  An h that is not 0 is at least the type's least value there: an infinite
-// weight gives it an infinity.
-template <class E>
-__device__ __forceinline__ uint32_t first_part(float h, float v) {
-  const uint32_t b = E::bits(v);
-  return h != 0.0f && (b & 0x7FFFu) == 0 ? b | 1u : b;
-}
-
-// Eight of h times 2^up as two parts each (an infinite or NaN one is its first part alone).
-template <class E>
-__device__ __forceinline__ void two_parts(const float (&h)[8], int up, u32x4& hi, u32x4& lo) {
+// h times 2^up as two parts each (an infinite or NaN one is its first part alone).  An h that is not 0 is at
+// least the type's least value in its first part, so that an infinite weight gives it an infinity: rounded
+// to 0 it is looked for by the smallest of the bits without the sign, less one.
+template <class E, int KS>
+__device__ __forceinline__ void two_parts(const float (&h)[KS][8], int up, u32x4 (&hi)[KS], u32x4 (&lo)[KS]) {
+  uint32_t least = ~0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float v0 = __builtin_amdgcn_ldexpf(h[2 * i], up), v1 = __builtin_amdgcn_ldexpf(h[2 * i + 1], up);
-    const uint32_t b0 = first_part<E>(h[2 * i], v0), b1 = first_part<E>(h[2 * i + 1], v1);
-    const float r0 = v0 - E::value((uint16_t)b0), r1 = v1 - E::value((uint16_t)b1);
-    hi[i] = b0 | b1 << 16;
-    lo[i] = E::bits(fabsf(r0) < INFINITY ? r0 : 0.0f) |
-            (uint32_t)E::bits(fabsf(r1) < INFINITY ? r1 : 0.0f) << 16;
+  for (int s = 0; s < KS; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v0 = __builtin_amdgcn_ldexpf(h[s][2 * i], up), v1 = __builtin_amdgcn_ldexpf(h[s][2 * i + 1], up);
+      const uint32_t b0 = E::bits(v0), b1 = E::bits(v1);
+      const float r0 = v0 - E::value((uint16_t)b0), r1 = v1 - E::value((uint16_t)b1);
+      hi[s][i] = b0 | b1 << 16;
+      lo[s][i] = E::bits(fabsf(r0) < INFINITY ? r0 : 0.0f) |
+                 (uint32_t)E::bits(fabsf(r1) < INFINITY ? r1 : 0.0f) << 16;
+      least = min(least, min((__float_as_uint(h[s][2 * i]) << 1) - 1, (__float_as_uint(h[s][2 * i + 1]) << 1) - 1));
+    }
+  // (half of the least value, times 2^-up)
+  const float half = __builtin_amdgcn_ldexpf(1.0f, (std::is_same_v<E, Half> ? -25 : -134) - up);
+  if (__builtin_expect(__ballot(least < __float_as_uint(half) << 1) != 0, 0)) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (h[s][2 * i + k] != 0.0f && (hi[s][i] >> 16 * k & 0x7FFFu) == 0) {
+            hi[s][i] |= 1u << 16 * k;
+            const float v = __builtin_amdgcn_ldexpf(h[s][2 * i + k], up);
+            lo[s][i] = (lo[s][i] & 0xFFFF0000u >> 16 * k) |
+                       (uint32_t)E::bits(v - E::value((uint16_t)(hi[s][i] >> 16 * k))) << 16 * k;
+          }
   }
 }
 
 // An infinite weight times two parts, of which the second may be 0 or of the other sign, is NaN where the
 // first part alone gives the infinity: a wave that finds a NaN among its sums forms them again, zeros in
 // the place of weights that are not finite where the second parts meet them.  (Looking at the sums
-// costs less than looking at every weight: prompts with 128 ranks 99 us against 106.)
+// costs less than looking at every weight: prompts with 128 ranks 98 us against 106.)
 template <int N>
 __device__ __forceinline__ bool any_nan(const f32x4 (&o)[N]) {
   bool nan = false;
@@ -404,19 +431,12 @@ __global__ __launch_bounds__(64 * kWaves, RT <= 4 ? 3 : 1) void lora_expand_kern
     int up;
     {
       float h[KS][8];
-      float most = 0.0f;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int r = 32 * s + 8 * p;
+      for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          h[s][e] = r + e < rank ? sum[s][e >> 2][e & 3] * by : 0.0f;
-          most = fmaxf(most, finite_size(h[s][e]));
-        }
-      }
-      up = power_of<E>(column_max(most));
-#pragma unroll
-      for (int s = 0; s < KS; ++s) two_parts<E>(h[s], up, hi[s], lo[s]);
+        for (int e = 0; e < 8; ++e) h[s][e] = 32 * s + 8 * p + e < rank ? sum[s][e >> 2][e & 3] * by : 0.0f;
+      up = power_of<E, KS>(h);
+      two_parts<E, KS>(h, up, hi, lo);
     }
 
     auto finish = [&](Unit& now, int unit) __attribute__((always_inline)) {
@@ -439,7 +459,7 @@ __global__ __launch_bounds__(64 * kWaves, RT <= 4 ? 3 : 1) void lora_expand_kern
           o[i] = E::mfma(now.f[s][i], lo[s], o[i]);
         }
       }
-      if (any_nan(o)) {
+      if (__builtin_expect(any_nan(o), 0)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           o[i] = f32x4{};
@@ -652,19 +672,12 @@ __global__ __launch_bounds__(64 * kWaves, RT > 4 ? 2 : 3) void lora_expand_tiles
       f32x4 sum[KS][2] = {};
       if (works) sum_slices<KS>(a.h + (t0 + mine) * (16 * RT), at, a.T * (16 * RT), 0, 1, slices, sum);
       float h[KS][8];
-      float most = 0.0f;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int r = 32 * s + 8 * p;
+      for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          h[s][e] = r + e < rank ? sum[s][e >> 2][e & 3] * by : 0.0f;
-          most = fmaxf(most, finite_size(h[s][e]));
-        }
-      }
-      const int up = power_of<E>(column_max(most));
-#pragma unroll
-      for (int s = 0; s < KS; ++s) two_parts<E>(h[s], up, hi[s], lo[s]);
+        for (int e = 0; e < 8; ++e) h[s][e] = 32 * s + 8 * p + e < rank ? sum[s][e >> 2][e & 3] * by : 0.0f;
+      const int up = power_of<E, KS>(h);
+      two_parts<E, KS>(h, up, hi, lo);
 #pragma unroll
       for (int k = 0; k < 4; ++k) down[k] = -__builtin_amdgcn_ds_bpermute((4 * p + k) << 2, up);
     }
@@ -701,7 +714,7 @@ __global__ __launch_bounds__(64 * kWaves, RT > 4 ? 2 : 3) void lora_expand_tiles
           }
         };
         multiply(std::false_type{});
-        if (any_nan(o)) multiply(std::true_type{});
+        if (__builtin_expect(any_nan(o), 0)) multiply(std::true_type{});
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
