@@ -8,11 +8,11 @@
 // are read once a tile, so a decoding step (one tile) reads each adapter once, and prompts
 // (long runs of one adapter) once a tile, from L2.  No sorting launch comes before.
 //
-// What bounds it: one token with 16 ranks through 4096 x 4096 8.4 us in two launches, chains of latencies
-// (adapters, ranks, rows, sums); 64 tokens over 40 adapters of 64 ranks through 10240 x 8192 26.4 us for
-// 57 MB (the same chains, and few loads an adapter on their way); prompts of 3500 tokens there 69 us
-// for 203 MB: x at 2.9 TB/s through LDS (20), h's slices joined (5), y and out at 3.3 with an
-// adapter's rows again for each tile (44).
+// What bounds it: one token with 16 ranks through 4096 x 4096 8.8 us in two launches, chains of latencies
+// (adapters, ranks, rows, sums); 64 tokens over 40 adapters of 64 ranks through 10240 x 8192 26.3 us for
+// 57 MB (the same chains, and few loads an adapter on their way); prompts of 3500 tokens there 68 us
+// for 203 MB: x at 2.9 TB/s through LDS (20), h's slices joined (5), y and out at 3.4 with an
+// adapter's rows again for each tile (43).
 //
 // h enters the second product as two 16-bit parts, for fp16 after a power of two that takes a token's
 // largest to 2^14 .. 2^15: within 2^-17 of itself, for fp16 2^-22 or 2^-39 of the largest.
