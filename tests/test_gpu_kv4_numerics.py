@@ -114,3 +114,26 @@ def test_scores_that_vanish(fq, by, scale, dtype):
         p = base.problem(fq, base.rng(65, tree, window), [40, 133, 3], [2, 1, 4], 4, 2, 64, 16, dtype, tree, by=by)
         out, lse = base.run(fq, p, 4, scale=scale, window=window or None, sinks=3)
         base.check(p, out, lse, scale, window, 3 if window else 0, rms=False)
+
+
+@pytest.mark.parametrize("ctx,new,H,Hkv,D,tree", CANCEL[:6])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_stays_alone(fq, ctx, new, H, Hkv, D, tree, bad):
+    """Its row of one head is not finite, and every other row has the bits it had."""
+    p = base.problem(fq, base.rng(70, *ctx, H, D), ctx, new, H, Hkv, D, 16, BF16, tree)
+    clean, clean_lse = base.run(fq, p, max(new))
+    t, h = sum(new) - 1, H // 2
+    p["q"][t, h, 3] = bad
+    out, lse = base.run(fq, p, max(new))
+    assert not bool(out[t, h].isfinite().any())
+    out[t, h], lse[t, h] = clean[t, h], clean_lse[t, h]
+    assert torch.equal(out, clean) and torch.equal(lse, clean_lse)
+
+
+def test_most_requests_with_windows(fq):
+    """As many requests as a step may have, some without new tokens, under a window."""
+    r = base.rng(71)
+    ctx, new = r.integers(0, 40, 4096).tolist(), r.integers(0, 3, 4096).tolist()
+    p = base.problem(fq, r, ctx, new, 2, 1, 64, 16, F16, False)
+    out, lse = base.run(fq, p, 2, window=9, sinks=2)
+    base.check(p, out, lse, 0.125, 9, 2)
